@@ -6,7 +6,10 @@ no fallback: if the shared library is missing or a call fails, an error is
 raised.
 
 The C ABI is declared in include/strata_moe.h; the names here mirror it:
-``workspace_bytes``, ``route``, ``forward``, ``kernel_names``.
+``workspace_bytes``, ``route``, ``forward``, ``kernel_names``.  The operators
+around the layer (include/strata_ops.h) are bound in ``ops`` and reached from
+here: ``sort_picks``, ``dispatch``, ``combine``, ``grouped_product``,
+``block_norm`` and their gradients.
 """
 from __future__ import annotations
 
@@ -14,6 +17,12 @@ import ctypes
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
+
+from . import ops as _ops
+from .ops import (GATE_CHANNEL, GATE_SIGMOID, GATE_TOKEN, POST_NORM, PRE_NORM, BlockNormArgs,  # noqa: F401
+                  block_norm, block_norm_args, block_norm_backward, block_norm_backward_workspace_bytes, combine,
+                  combine_backward, dispatch, dispatch_backward, grouped_dgrad, grouped_product, grouped_wgrad,
+                  grouped_workspace_bytes, sort_picks, sort_workspace_bytes)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libstrata_moe.so")
@@ -101,6 +110,7 @@ def load_library(path: str = LIB_PATH):
     lib.strata_probe_hbm_read.argtypes = [vp, sz, vp, i32, vp]
     lib.strata_probe_mfma_bf16.restype = ctypes.c_int
     lib.strata_probe_mfma_bf16.argtypes = [i32, vp, i32, ctypes.POINTER(ctypes.c_double), vp]
+    _ops.declare(lib)
     _lib = lib
     return lib
 
@@ -109,7 +119,7 @@ EXPORTED_SYMBOLS = ("strata_moe_workspace_bytes", "strata_moe_route", "strata_mo
                     "strata_moe_counts_accumulate", "strata_moe_resident_topn", "strata_moe_kernel_names",
                     "strata_status_str", "strata_probe_hbm_read", "strata_probe_mfma_bf16",
                     "strata_moe_forward_noalloc", "strata_moe_host_workspace_bytes", "strata_moe_host_isa",
-                    "strata_moe_host_misses", "strata_moe_forward_coprocess")
+                    "strata_moe_host_misses", "strata_moe_forward_coprocess") + _ops.SYMBOLS
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # STRATA_NOALLOC_SCRATCH_BYTES
 

@@ -1,0 +1,307 @@
+// Token rows to their picks' slots and back (strata_moe_dispatch, _combine
+// and their gradients).
+//
+// All four are bound by HBM: a pick's row is read or written once, a token's
+// row once.  The work is token-major: a group of G threads takes one token,
+// keeps a V-element piece of its row in registers and meets the k picked
+// rows, so x and dout are read once however many picks a token has and
+// every sum runs over r in order in one thread.  G is the power of two from
+// 16 to 256 that leaves the fewest threads without a piece, V the widest
+// vector up to 16 bytes that divides the row.
+#include "ops.hpp"
+
+namespace strata {
+
+constexpr int PB = 16;   // picked rows in flight per thread
+
+// Token of this thread's group and its place in the group.
+template <int G> __device__ __forceinline__ bool row_group(int T, int &t, int &lane) {
+    t = (int)blockIdx.x * (256 / G) + (int)(threadIdx.x / G);
+    if (G >= 64) t = __builtin_amdgcn_readfirstlane(t);
+    lane = threadIdx.x % G;
+    return t < T;
+}
+
+template <typename P, int G>
+__global__ __launch_bounds__(256) void dispatch_kernel(const P *__restrict__ x, const int32_t *__restrict__ pos,
+                                                       P *__restrict__ xs, int T, int k, int nc, int rows) {
+    int t, lane;
+    if (!row_group<G>(T, t, lane)) return;
+    const int32_t *pt = pos + (int64_t)t * k;
+    for (int c = lane; c < nc; c += G) {
+        const P v = x[(int64_t)t * nc + c];
+        for (int r = 0; r < k; ++r) {
+            const int p = pt[r];
+            if ((uint32_t)p < (uint32_t)rows) xs[(int64_t)p * nc + c] = v;
+        }
+    }
+}
+
+template <typename Y, typename O, int V, int G>
+__global__ __launch_bounds__(256) void combine_rows_kernel(const Y *__restrict__ ys, const int32_t *__restrict__ pos,
+                                                           const float *__restrict__ w, const O *base, O *out, int T,
+                                                           int k, int d, int rows) {
+    int t, lane;
+    if (!row_group<G>(T, t, lane)) return;
+    const int32_t *pt = pos + (int64_t)t * k;
+    const float *wt = w ? w + (int64_t)t * k : nullptr;
+    for (int i = lane * V; i < d; i += G * V) {
+        float s[V];
+        if (base) {
+            load_values<V>(base, (int64_t)t * d + i, s);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = 0.f;
+        }
+        for (int r0 = 0; r0 < k; r0 += PB) {
+            float v[PB][V];
+            float g[PB];
+            bool has[PB];
+#pragma unroll
+            for (int r = 0; r < PB; ++r) {
+                const int p = r0 + r < k ? pt[r0 + r] : -1;
+                has[r] = (uint32_t)p < (uint32_t)rows;
+                if (has[r]) {
+                    g[r] = wt ? wt[r0 + r] : 1.f;
+                    load_values<V>(ys, (int64_t)p * d + i, v[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < PB; ++r) {
+                if (has[r]) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) s[j] = fmaf(g[r], v[r][j], s[j]);
+                }
+            }
+        }
+        store_values<V>(out, (int64_t)t * d + i, s);
+    }
+}
+
+// Gradient of the combine: per token, each pick's row is read for its dot
+// product with dout and written as w * dout in the same pass.
+template <typename Y, typename O, int V, int G>
+__global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__ dout, const Y *ys,
+                                                           const int32_t *__restrict__ pos,
+                                                           const float *__restrict__ w, Y *dys, float *dw, float *dz,
+                                                           int T, int k, int d, int rows) {
+    constexpr int NG = 256 / G, NW = G / 64;   // tokens per block, waves per token
+    __shared__ float part[NG][NW][32];
+    int t, lane;
+    const bool live = row_group<G>(T, t, lane);
+    const int g = threadIdx.x / G, wv = (threadIdx.x % G) / 64;
+    const bool dots = dw || dz;
+    if (live) {
+        const int32_t *pt = pos + (int64_t)t * k;
+        const float *wt = w + (int64_t)t * k;
+        for (int r0 = 0; r0 < k; r0 += PB) {
+            float dot[PB];
+#pragma unroll
+            for (int r = 0; r < PB; ++r) dot[r] = 0.f;
+            for (int i = lane * V; i < d; i += G * V) {
+                float o[V];
+                load_values<V>(dout, (int64_t)t * d + i, o);
+                float v[PB][V];
+#pragma unroll
+                for (int r = 0; r < PB; ++r) {
+                    const int p = r0 + r < k ? pt[r0 + r] : -1;
+                    if (dots && (uint32_t)p < (uint32_t)rows) load_values<V>(ys, (int64_t)p * d + i, v[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < PB; ++r) {
+                    const int p = r0 + r < k ? pt[r0 + r] : -1;
+                    if ((uint32_t)p < (uint32_t)rows) {
+                        if (dots) {
+#pragma unroll
+                            for (int j = 0; j < V; ++j) dot[r] = fmaf(o[j], v[r][j], dot[r]);
+                        }
+                        if (dys) {
+                            const float gw = wt[r0 + r];
+                            float q[V];
+#pragma unroll
+                            for (int j = 0; j < V; ++j) q[j] = gw * o[j];
+                            store_values<V>(dys, (int64_t)p * d + i, q);
+                        }
+                    }
+                }
+            }
+            if (dots) {
+#pragma unroll
+                for (int r = 0; r < PB; ++r) {
+                    if (r0 + r < k) {
+                        const float s = wave_sum_dpp(dot[r]);
+                        if ((threadIdx.x & 63) == 63) part[g][wv][r0 + r] = s;
+                    }
+                }
+            }
+        }
+    }
+    if (!dots) return;
+    __syncthreads();
+    const int th = threadIdx.x % G;
+    if (live && th < 32) {   // lane r of the group's first wave: pick r
+        float s = 0.f;
+        if (th < k) {
+#pragma unroll
+            for (int q = 0; q < NW; ++q) s += part[g][q][th];
+            if (dw) dw[(int64_t)t * k + th] = s;
+        }
+        if (dz) {
+            const float wr = th < k ? w[(int64_t)t * k + th] : 0.f;
+            const int p = th < k ? pos[(int64_t)t * k + th] : -1;
+            float q = (uint32_t)p < (uint32_t)rows ? wr * s : 0.f;   // a skipped pick's weight enters no sum
+            q += __shfl_xor(q, 16, 32);
+            q += __shfl_xor(q, 8, 32);
+            q += __shfl_xor(q, 4, 32);
+            q += __shfl_xor(q, 2, 32);
+            q += __shfl_xor(q, 1, 32);
+            if (th < k) dz[(int64_t)t * k + th] = wr * (s - q);
+        }
+    }
+}
+
+namespace {
+
+// Threads per token for nc pieces: fewest idle threads, the larger of equals.
+int row_threads(int64_t nc, int least) {
+    int best = 256;
+    int64_t cost = (nc + 255) / 256 * 256;
+    for (int g = 128; g >= least; g /= 2) {
+        const int64_t c = (nc + g - 1) / g * g;
+        if (c < cost) {
+            cost = c;
+            best = g;
+        }
+    }
+    return best;
+}
+
+strata_status check_rows(const void *a, const void *b, const int32_t *pos, int32_t rows, int32_t T, int32_t k,
+                         int32_t d) {
+    if (T < 0 || rows < 0 || k < 1 || k > 32 || d < 1) return STRATA_EINVAL;
+    if (T == 0) return STRATA_OK;
+    if (!pos || bad_rows(b)) return STRATA_EINVAL;
+    if (rows > 0 ? bad_rows(a) : (a && !aligned16(a))) return STRATA_EINVAL;
+    if (T > MAX_ROWS || (int64_t)T * k > INT32_MAX) return STRATA_EUNSUPPORTED;
+    return STRATA_OK;
+}
+
+dim3 row_grid(int T, int g) { return dim3((unsigned)(((int64_t)T + 256 / g - 1) / (256 / g))); }
+
+template <typename P>
+void launch_dispatch(const void *x, const int32_t *pos, void *xs, int T, int k, int nc, int rows, hipStream_t s) {
+    const int g = row_threads(nc, 16);
+#define DISPATCH(G)                                                                                                  \
+    case G:                                                                                                          \
+        STRATA_LAUNCH((dispatch_kernel<P, G>), row_grid(T, G), dim3(256), 0, s, (const P *)x, pos, (P *)xs, T, k, nc, \
+                      rows);                                                                                         \
+        break;
+    switch (g) { DISPATCH(16) DISPATCH(32) DISPATCH(64) DISPATCH(128) DISPATCH(256) }
+#undef DISPATCH
+}
+
+struct RowCall {
+    const void *ys, *in;   // in: base (combine) or dout (its gradient)
+    const int32_t *pos;
+    const float *w;
+    void *out;             // out, or dys
+    float *dw, *dz;
+    int T, k, d, rows;
+    hipStream_t s;
+};
+
+struct Combine {
+    template <typename Y, typename O, int V> static void run(const RowCall &c) {
+#define COMBINE(G)                                                                                                 \
+    case G:                                                                                                        \
+        STRATA_LAUNCH((combine_rows_kernel<Y, O, V, G>), row_grid(c.T, G), dim3(256), 0, c.s, (const Y *)c.ys, c.pos, \
+                      c.w, (const O *)c.in, (O *)c.out, c.T, c.k, c.d, c.rows);                                    \
+        break;
+        switch (row_threads(c.d / V, 16)) { COMBINE(16) COMBINE(32) COMBINE(64) COMBINE(128) COMBINE(256) }
+#undef COMBINE
+    }
+};
+
+struct CombineBack {
+    template <typename Y, typename O, int V> static void run(const RowCall &c) {
+#define BACK(G)                                                                                                    \
+    case G:                                                                                                        \
+        STRATA_LAUNCH((combine_back_kernel<Y, O, V, G>), row_grid(c.T, G), dim3(256), 0, c.s, (const O *)c.in,     \
+                      (const Y *)c.ys, c.pos, c.w, (Y *)c.out, c.dw, c.dz, c.T, c.k, c.d, c.rows);                 \
+        break;
+        switch (row_threads(c.d / V, 64)) { BACK(64) BACK(128) BACK(256) }
+#undef BACK
+    }
+};
+
+// The widest pieces that divide the row: 8 values of bf16, 4 of fp32.
+template <typename F, typename Y, typename O> void row_width(const RowCall &c) {
+    if constexpr (sizeof(Y) == 2) {
+        if (c.d % 8 == 0) return F::template run<Y, O, 8>(c);
+    }
+    if (c.d % 4 == 0) return F::template run<Y, O, 4>(c);
+    if (c.d % 2 == 0) return F::template run<Y, O, 2>(c);
+    return F::template run<Y, O, 1>(c);
+}
+
+template <typename F> strata_status row_types(const RowCall &c, int ydtype, int odtype) {
+    const bool yb = ydtype == STRATA_X_BF16, ob = odtype == STRATA_X_BF16;
+    if (yb && ob) row_width<F, uint16_t, uint16_t>(c);
+    else if (yb) row_width<F, uint16_t, float>(c);
+    else if (ob) row_width<F, float, uint16_t>(c);
+    else row_width<F, float, float>(c);
+    return hip_status(hipGetLastError());
+}
+
+}  // namespace
+
+}  // namespace strata
+
+using namespace strata;
+
+extern "C" {
+
+strata_status strata_moe_dispatch(const void *x, strata_xdtype xdtype, int32_t T, int32_t k, int32_t d,
+                                  const int32_t *pos, void *xs, int32_t rows, void *stream) {
+    if (bad_dtype(xdtype)) return STRATA_EINVAL;
+    const strata_status st = check_rows(xs, x, pos, rows, T, k, d);
+    if (st != STRATA_OK || T == 0 || rows == 0) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const int64_t bytes = (int64_t)d * (xdtype == STRATA_X_BF16 ? 2 : 4);
+    if (bytes % 16 == 0) launch_dispatch<uint4>(x, pos, xs, T, k, (int)(bytes / 16), rows, s);
+    else if (bytes % 8 == 0) launch_dispatch<uint2>(x, pos, xs, T, k, (int)(bytes / 8), rows, s);
+    else if (bytes % 4 == 0) launch_dispatch<uint32_t>(x, pos, xs, T, k, (int)(bytes / 4), rows, s);
+    else launch_dispatch<uint16_t>(x, pos, xs, T, k, (int)(bytes / 2), rows, s);
+    return hip_status(hipGetLastError());
+}
+
+strata_status strata_moe_combine(const void *ys, strata_xdtype ydtype, int32_t rows, const int32_t *pos,
+                                 const float *w, int32_t T, int32_t k, int32_t d, const void *base, void *out,
+                                 strata_xdtype odtype, void *stream) {
+    if (bad_dtype(ydtype) || bad_dtype(odtype)) return STRATA_EINVAL;
+    const strata_status st = check_rows(ys, out, pos, rows, T, k, d);
+    if (st != STRATA_OK || T == 0) return st;
+    if (base && !aligned16(base)) return STRATA_EINVAL;
+    return row_types<Combine>(RowCall{ys, base, pos, w, out, nullptr, nullptr, T, k, d, rows, (hipStream_t)stream},
+                              ydtype, odtype);
+}
+
+strata_status strata_moe_dispatch_backward(const void *dxs, strata_xdtype xdtype, int32_t rows, const int32_t *pos,
+                                           int32_t T, int32_t k, int32_t d, void *dx, void *stream) {
+    return strata_moe_combine(dxs, xdtype, rows, pos, nullptr, T, k, d, nullptr, dx, xdtype, stream);
+}
+
+strata_status strata_moe_combine_backward(const void *dout, strata_xdtype odtype, const void *ys,
+                                          strata_xdtype ydtype, int32_t rows, const int32_t *pos, const float *w,
+                                          int32_t T, int32_t k, int32_t d, void *dys, float *dw, float *dz,
+                                          void *stream) {
+    if (bad_dtype(ydtype) || bad_dtype(odtype)) return STRATA_EINVAL;
+    const strata_status st = check_rows(ys, dout, pos, rows, T, k, d);
+    if (st != STRATA_OK || T == 0) return st;
+    if (!w || (dys && !aligned16(dys))) return STRATA_EINVAL;
+    if (!dys && !dw && !dz) return STRATA_OK;
+    return row_types<CombineBack>(RowCall{ys, dout, pos, w, dys, dw, dz, T, k, d, rows, (hipStream_t)stream}, ydtype,
+                                  odtype);
+}
+
+}  // extern "C"
