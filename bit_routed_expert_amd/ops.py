@@ -16,6 +16,11 @@ try:
 except ImportError:  # pragma: no cover -- the rest of the package imports without it
     torch = None
 
+# The current stream's handle of a device: torch's direct accessor where it has one (a Stream object costs
+# as much host time as the whole launch).
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
 POST_NORM, PRE_NORM, GATE_TOKEN, GATE_CHANNEL, GATE_SIGMOID = 1, 2, 4, 8, 16
 
 _XTYPES = {0: torch.bfloat16, 1: torch.float32} if torch else {}   # X_BF16, X_F32
@@ -62,61 +67,75 @@ def _bad(what: str):
     raise StrataError(_EINVAL, what)
 
 
-class _Call:
-    """The tensors of one call: their addresses, checked to be on one device."""
-    __slots__ = ("dev",)
+def _wrong(t, dtype, n: int, dev: int, name: str):
+    """Why _ptr refused a tensor."""
+    if t.get_device() != dev:
+        _bad(f"{name} is on {t.device}, not on cuda:{dev}" if dev >= 0 else f"{name} is not in device memory")
+    if t.dtype is not dtype:
+        _bad(f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() != n:
+        _bad(f"{name} has {t.numel()} elements, not {n}")
+    _bad(f"{name} is not contiguous")
 
-    def __init__(self):
-        self.dev = None
 
-    def ptr(self, t, dtype, n: int, name: str) -> Optional[int]:
-        """Address of a contiguous tensor of n elements (None and ints pass)."""
-        if t is None or t.__class__ is int:
-            return t
-        dev = t.device
-        if self.dev is None:
-            if dev.type != "cuda":
-                _bad(f"{name} is not in device memory")
-            self.dev = dev
-        elif dev != self.dev:
-            _bad(f"{name} is on {dev}, not on {self.dev}")
-        if t.dtype != dtype:
-            _bad(f"{name} is {t.dtype}, not {dtype}")
-        if t.numel() != n:
-            _bad(f"{name} has {t.numel()} elements, not {n}")
-        if not t.is_contiguous():
-            _bad(f"{name} is not contiguous")
-        return t.data_ptr()
+def _device(*tensors) -> int:
+    """Index of the first tensor's device; -2 when all are addresses or None."""
+    for t in tensors:
+        if t is not None and t.__class__ is not int:
+            dev = t.get_device()
+            if dev < 0:
+                _bad("a tensor is not in device memory")
+            return dev
+    return -2
 
-    def ws(self, t, n: int) -> Optional[int]:
-        """Address of a workspace said to hold n bytes."""
-        if t is None or t.__class__ is int:
-            return t
-        if self.dev is not None and t.device != self.dev:
-            _bad(f"the workspace is on {t.device}, not on {self.dev}")
-        if t.numel() * t.element_size() < n or not t.is_contiguous():
-            _bad("the workspace is smaller than ws_bytes")
-        return t.data_ptr()
 
-    def run(self, fn, *args, stream=None):
-        """fn(*args, stream) with the tensors' device current."""
-        if stream is not None and stream.__class__ is not int:
-            stream = stream.cuda_stream
-        dev = self.dev
-        if dev is not None and dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                s = torch.cuda.current_stream().cuda_stream if stream is None else stream
-                status = fn(*args, s)
-        else:
-            status = fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream)
-        if status:
-            from . import _check
-            _check(status)
+def _ptr(t, dtype, n: int, dev: int, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of n elements on the call's device (None and addresses pass)."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _wrong(t, dtype, n, dev, name)
+    return t.data_ptr()
+
+
+def _ws(t, n: int, dev: int) -> Optional[int]:
+    """Address of a workspace said to hold n bytes."""
+    if t is None or t.__class__ is int:
+        return t
+    if dev >= 0 and t.get_device() != dev:
+        _bad(f"the workspace is on {t.device}, not on cuda:{dev}")
+    if t.numel() * t.element_size() < n or not t.is_contiguous():
+        _bad("the workspace is smaller than ws_bytes")
+    return t.data_ptr()
+
+
+def _call(fn, dev: int, stream, *args):
+    """fn(*args, stream) with the tensors' device current, on its current stream unless one is given."""
+    if dev >= 0 and dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(dev, stream))
+    else:
+        status = fn(*args, _stream(dev, stream))
+    if status:
+        from . import _check
+        _check(status)
+
+
+def _stream(dev: int, stream) -> int:
+    if stream is not None:
+        return stream if stream.__class__ is int else stream.cuda_stream
+    return _raw_stream(dev if dev >= 0 else torch.cuda.current_device())
+
+
+_library = None
 
 
 def _lib():
-    from . import load_library
-    return load_library()
+    global _library
+    if _library is None:
+        from . import load_library
+        _library = load_library()
+    return _library
 
 
 def _xtype(code: int, name: str):
@@ -135,42 +154,42 @@ def sort_workspace_bytes(T: int, k: int, n_experts: int) -> int:
 
 def sort_picks(idx, T: int, k: int, n_experts: int, counts, offsets, perm, pos, ws, ws_bytes: int, stream=None):
     """Picks sorted by expert (see strata_moe_sort); any output may be None."""
-    c, i32, n = _Call(), torch.int32, T * k
-    c.run(_lib().strata_moe_sort, c.ptr(idx, i32, n, "idx"), T, k, n_experts,
-          c.ptr(counts, i32, n_experts, "counts"), c.ptr(offsets, i32, n_experts + 1, "offsets"),
-          c.ptr(perm, i32, n, "perm"), c.ptr(pos, i32, n, "pos"), c.ws(ws, ws_bytes), ws_bytes, stream=stream)
+    v, i32, n = _device(idx, counts, offsets, perm, pos), torch.int32, T * k
+    _call(_lib().strata_moe_sort, v, stream, _ptr(idx, i32, n, v, "idx"), T, k, n_experts,
+          _ptr(counts, i32, n_experts, v, "counts"), _ptr(offsets, i32, n_experts + 1, v, "offsets"),
+          _ptr(perm, i32, n, v, "perm"), _ptr(pos, i32, n, v, "pos"), _ws(ws, ws_bytes, v), ws_bytes)
 
 
 def dispatch(x, xdtype: int, T: int, k: int, d: int, pos, xs, rows: int, stream=None):
     """xs[pos[t*k + r]] = x[t] (see strata_moe_dispatch)."""
-    c, xt = _Call(), _xtype(xdtype, "xdtype")
-    c.run(_lib().strata_moe_dispatch, c.ptr(x, xt, T * d, "x"), xdtype, T, k, d, c.ptr(pos, torch.int32, T * k, "pos"),
-          c.ptr(xs, xt, rows * d, "xs"), rows, stream=stream)
+    v, xt = _device(x, xs), _xtype(xdtype, "xdtype")
+    _call(_lib().strata_moe_dispatch, v, stream, _ptr(x, xt, T * d, v, "x"), xdtype, T, k, d,
+          _ptr(pos, torch.int32, T * k, v, "pos"), _ptr(xs, xt, rows * d, v, "xs"), rows)
 
 
 def dispatch_backward(dxs, xdtype: int, rows: int, pos, T: int, k: int, d: int, dx, stream=None):
     """dx[t] = sum over r of dxs[pos[t*k + r]] (see strata_moe_dispatch_backward)."""
-    c, xt = _Call(), _xtype(xdtype, "xdtype")
-    c.run(_lib().strata_moe_dispatch_backward, c.ptr(dxs, xt, rows * d, "dxs"), xdtype, rows,
-          c.ptr(pos, torch.int32, T * k, "pos"), T, k, d, c.ptr(dx, xt, T * d, "dx"), stream=stream)
+    v, xt = _device(dx, dxs), _xtype(xdtype, "xdtype")
+    _call(_lib().strata_moe_dispatch_backward, v, stream, _ptr(dxs, xt, rows * d, v, "dxs"), xdtype, rows,
+          _ptr(pos, torch.int32, T * k, v, "pos"), T, k, d, _ptr(dx, xt, T * d, v, "dx"))
 
 
 def combine(ys, ydtype: int, rows: int, pos, w, T: int, k: int, d: int, out, odtype: int, base=None, stream=None):
     """out[t] = base[t] + sum over r of w[t][r] * ys[pos[t*k + r]] (see strata_moe_combine)."""
-    c, ot = _Call(), _xtype(odtype, "odtype")
-    c.run(_lib().strata_moe_combine, c.ptr(ys, _xtype(ydtype, "ydtype"), rows * d, "ys"), ydtype, rows,
-          c.ptr(pos, torch.int32, T * k, "pos"), c.ptr(w, torch.float32, T * k, "w"), T, k, d,
-          c.ptr(base, ot, T * d, "base"), c.ptr(out, ot, T * d, "out"), odtype, stream=stream)
+    v, ot = _device(out, ys), _xtype(odtype, "odtype")
+    _call(_lib().strata_moe_combine, v, stream, _ptr(ys, _xtype(ydtype, "ydtype"), rows * d, v, "ys"), ydtype, rows,
+          _ptr(pos, torch.int32, T * k, v, "pos"), _ptr(w, torch.float32, T * k, v, "w"), T, k, d,
+          _ptr(base, ot, T * d, v, "base"), _ptr(out, ot, T * d, v, "out"), odtype)
 
 
 def combine_backward(dout, odtype: int, ys, ydtype: int, rows: int, pos, w, T: int, k: int, d: int, dys=None, dw=None,
                      dz=None, stream=None):
     """Gradients of the combine's rows, weights and picked logits (see strata_moe_combine_backward)."""
-    c, yt, f32 = _Call(), _xtype(ydtype, "ydtype"), torch.float32
-    c.run(_lib().strata_moe_combine_backward, c.ptr(dout, _xtype(odtype, "odtype"), T * d, "dout"), odtype,
-          c.ptr(ys, yt, rows * d, "ys"), ydtype, rows, c.ptr(pos, torch.int32, T * k, "pos"),
-          c.ptr(w, f32, T * k, "w"), T, k, d, c.ptr(dys, yt, rows * d, "dys"), c.ptr(dw, f32, T * k, "dw"),
-          c.ptr(dz, f32, T * k, "dz"), stream=stream)
+    v, yt, f32 = _device(dout, ys), _xtype(ydtype, "ydtype"), torch.float32
+    _call(_lib().strata_moe_combine_backward, v, stream, _ptr(dout, _xtype(odtype, "odtype"), T * d, v, "dout"),
+          odtype, _ptr(ys, yt, rows * d, v, "ys"), ydtype, rows, _ptr(pos, torch.int32, T * k, v, "pos"),
+          _ptr(w, f32, T * k, v, "w"), T, k, d, _ptr(dys, yt, rows * d, v, "dys"), _ptr(dw, f32, T * k, v, "dw"),
+          _ptr(dz, f32, T * k, v, "dz"))
 
 
 def grouped_workspace_bytes(rows: int, n_experts: int, N: int, K: int) -> int:
@@ -183,29 +202,29 @@ def grouped_workspace_bytes(rows: int, n_experts: int, N: int, K: int) -> int:
 def grouped_product(x, W, offsets, rows: int, n_experts: int, N: int, K: int, y, ydtype: int, ws, ws_bytes: int,
                     stream=None):
     """y[s] = W_e x[s] over rows sorted by expert (see strata_moe_grouped_product)."""
-    c, bf = _Call(), torch.bfloat16
-    c.run(_lib().strata_moe_grouped_product, c.ptr(x, bf, rows * K, "x"), c.ptr(W, bf, n_experts * N * K, "W"),
-          c.ptr(offsets, torch.int32, n_experts + 1, "offsets"), rows, n_experts, N, K,
-          c.ptr(y, _xtype(ydtype, "ydtype"), rows * N, "y"), ydtype, c.ws(ws, ws_bytes), ws_bytes, stream=stream)
+    v, bf = _device(W, x, y), torch.bfloat16
+    _call(_lib().strata_moe_grouped_product, v, stream, _ptr(x, bf, rows * K, v, "x"),
+          _ptr(W, bf, n_experts * N * K, v, "W"), _ptr(offsets, torch.int32, n_experts + 1, v, "offsets"), rows,
+          n_experts, N, K, _ptr(y, _xtype(ydtype, "ydtype"), rows * N, v, "y"), ydtype, _ws(ws, ws_bytes, v), ws_bytes)
 
 
 def grouped_dgrad(dy, W, offsets, rows: int, n_experts: int, N: int, K: int, dx, xdtype: int, ws, ws_bytes: int,
                   stream=None):
     """dx[s] = W_e^T dy[s] (see strata_moe_grouped_dgrad)."""
-    c, bf = _Call(), torch.bfloat16
-    c.run(_lib().strata_moe_grouped_dgrad, c.ptr(dy, bf, rows * N, "dy"), c.ptr(W, bf, n_experts * N * K, "W"),
-          c.ptr(offsets, torch.int32, n_experts + 1, "offsets"), rows, n_experts, N, K,
-          c.ptr(dx, _xtype(xdtype, "xdtype"), rows * K, "dx"), xdtype, c.ws(ws, ws_bytes), ws_bytes, stream=stream)
+    v, bf = _device(W, dy, dx), torch.bfloat16
+    _call(_lib().strata_moe_grouped_dgrad, v, stream, _ptr(dy, bf, rows * N, v, "dy"),
+          _ptr(W, bf, n_experts * N * K, v, "W"), _ptr(offsets, torch.int32, n_experts + 1, v, "offsets"), rows,
+          n_experts, N, K, _ptr(dx, _xtype(xdtype, "xdtype"), rows * K, v, "dx"), xdtype, _ws(ws, ws_bytes, v),
+          ws_bytes)
 
 
 def grouped_wgrad(dy, x, offsets, rows: int, n_experts: int, N: int, K: int, dW, wdtype: int, ws, ws_bytes: int,
                   stream=None):
     """dW_e = sum over e's rows of dy[s] x[s]^T (see strata_moe_grouped_wgrad)."""
-    c, bf = _Call(), torch.bfloat16
-    c.run(_lib().strata_moe_grouped_wgrad, c.ptr(dy, bf, rows * N, "dy"), c.ptr(x, bf, rows * K, "x"),
-          c.ptr(offsets, torch.int32, n_experts + 1, "offsets"), rows, n_experts, N, K,
-          c.ptr(dW, _xtype(wdtype, "wdtype"), n_experts * N * K, "dW"), wdtype, c.ws(ws, ws_bytes), ws_bytes,
-          stream=stream)
+    v, bf = _device(dW, dy, x), torch.bfloat16
+    _call(_lib().strata_moe_grouped_wgrad, v, stream, _ptr(dy, bf, rows * N, v, "dy"), _ptr(x, bf, rows * K, v, "x"),
+          _ptr(offsets, torch.int32, n_experts + 1, v, "offsets"), rows, n_experts, N, K,
+          _ptr(dW, _xtype(wdtype, "wdtype"), n_experts * N * K, v, "dW"), wdtype, _ws(ws, ws_bytes, v), ws_bytes)
 
 
 def block_norm_args(T: int, d: int, x_dtype: int, y_dtype: int, u_dtype: int, flags: int, resid_scale: float = 1.0,
@@ -213,22 +232,23 @@ def block_norm_args(T: int, d: int, x_dtype: int, y_dtype: int, u_dtype: int, fl
     return BlockNormArgs(T, d, x_dtype, y_dtype, u_dtype, flags, resid_scale, branch_scale, eps)
 
 
-def _gate(c: _Call, a: BlockNormArgs, gate, yt, name: str):
+def _gate(a: BlockNormArgs, gate, yt, dev: int, name: str):
+    if gate is None:
+        return None
     if a.flags & GATE_TOKEN:
-        return c.ptr(gate, torch.float32, a.T, name)
-    return c.ptr(gate, yt, a.T * a.d, name)
+        return _ptr(gate, torch.float32, a.T, dev, name)
+    return _ptr(gate, yt, a.T * a.d, dev, name)
 
 
 def block_norm(args: BlockNormArgs, x, y, gate=None, g_post=None, g_pre=None, r=None, u=None, rstd_y=None,
                rstd_r=None, stream=None):
     """r = resid_scale x + branch_scale G norm(y), u = norm(r) (see strata_block_norm)."""
-    c, a, f32 = _Call(), args, torch.float32
-    T, d = a.T, a.d
-    n, xt, yt = T * d, _xtype(a.x_dtype, "x_dtype"), _xtype(a.y_dtype, "y_dtype")
-    c.run(_lib().strata_block_norm, ctypes.byref(a), c.ptr(x, xt, n, "x"), c.ptr(y, yt, n, "y"),
-          _gate(c, a, gate, yt, "gate"), c.ptr(g_post, f32, d, "g_post"), c.ptr(g_pre, f32, d, "g_pre"),
-          c.ptr(r, xt, n, "r"), c.ptr(u, _xtype(a.u_dtype, "u_dtype"), n, "u"), c.ptr(rstd_y, f32, T, "rstd_y"),
-          c.ptr(rstd_r, f32, T, "rstd_r"), stream=stream)
+    v, f32, T, d = _device(x, y, r, u), torch.float32, args.T, args.d
+    n, xt, yt = T * d, _xtype(args.x_dtype, "x_dtype"), _xtype(args.y_dtype, "y_dtype")
+    _call(_lib().strata_block_norm, v, stream, ctypes.byref(args), _ptr(x, xt, n, v, "x"), _ptr(y, yt, n, v, "y"),
+          _gate(args, gate, yt, v, "gate"), _ptr(g_post, f32, d, v, "g_post"), _ptr(g_pre, f32, d, v, "g_pre"),
+          _ptr(r, xt, n, v, "r"), _ptr(u, _xtype(args.u_dtype, "u_dtype"), n, v, "u"),
+          _ptr(rstd_y, f32, T, v, "rstd_y"), _ptr(rstd_r, f32, T, v, "rstd_r"))
 
 
 def block_norm_backward_workspace_bytes(args: BlockNormArgs) -> int:
@@ -242,12 +262,11 @@ def block_norm_backward(args: BlockNormArgs, dr, du, r, y, gate=None, g_post=Non
                         rstd_r=None, dx=None, dy=None, dgate=None, dg_post=None, dg_pre=None, ws=None,
                         ws_bytes: int = 0, stream=None):
     """Gradients of block_norm's rows, gate and gains (see strata_block_norm_backward)."""
-    c, a, f32 = _Call(), args, torch.float32
-    T, d = a.T, a.d
-    n, xt, yt, ut = T * d, _xtype(a.x_dtype, "x_dtype"), _xtype(a.y_dtype, "y_dtype"), _xtype(a.u_dtype, "u_dtype")
-    c.run(_lib().strata_block_norm_backward, ctypes.byref(a), c.ptr(dr, xt, n, "dr"), c.ptr(du, ut, n, "du"),
-          c.ptr(r, xt, n, "r"), c.ptr(y, yt, n, "y"), _gate(c, a, gate, yt, "gate"), c.ptr(g_post, f32, d, "g_post"),
-          c.ptr(g_pre, f32, d, "g_pre"), c.ptr(rstd_y, f32, T, "rstd_y"), c.ptr(rstd_r, f32, T, "rstd_r"),
-          c.ptr(dx, xt, n, "dx"), c.ptr(dy, yt, n, "dy"), _gate(c, a, dgate, yt, "dgate"),
-          c.ptr(dg_post, f32, d, "dg_post"), c.ptr(dg_pre, f32, d, "dg_pre"), c.ws(ws, ws_bytes), ws_bytes,
-          stream=stream)
+    v, f32, T, d = _device(dr, du, r, y, dx, dy, dg_post, dg_pre), torch.float32, args.T, args.d
+    n, xt, yt = T * d, _xtype(args.x_dtype, "x_dtype"), _xtype(args.y_dtype, "y_dtype")
+    _call(_lib().strata_block_norm_backward, v, stream, ctypes.byref(args), _ptr(dr, xt, n, v, "dr"),
+          _ptr(du, _xtype(args.u_dtype, "u_dtype"), n, v, "du"), _ptr(r, xt, n, v, "r"), _ptr(y, yt, n, v, "y"),
+          _gate(args, gate, yt, v, "gate"), _ptr(g_post, f32, d, v, "g_post"), _ptr(g_pre, f32, d, v, "g_pre"),
+          _ptr(rstd_y, f32, T, v, "rstd_y"), _ptr(rstd_r, f32, T, v, "rstd_r"), _ptr(dx, xt, n, v, "dx"),
+          _ptr(dy, yt, n, v, "dy"), _gate(args, dgate, yt, v, "dgate"), _ptr(dg_post, f32, d, v, "dg_post"),
+          _ptr(dg_pre, f32, d, v, "dg_pre"), _ws(ws, ws_bytes, v), ws_bytes)
