@@ -1,0 +1,272 @@
+// Tile products of the experts' grouped products on the gfx950 matrix cores.
+//
+// One block computes a tile C[BM][BN] = sum_c A[m][c] B[n][c] of one expert.
+// The contraction is cut into steps of 64; a step's tiles of A and B come
+// into LDS by direct global->LDS loads (16 bytes a lane, no registers) while
+// earlier steps run on the matrix cores: ST buffers in turn, one barrier a
+// step.
+//
+// An operand whose contraction runs along memory (x and W in the product)
+// lies in LDS as it does in memory, 64 values (128 bytes) to a row; a lane's
+// 8 values of a 32x32x16 product are one 16-byte read, and the row's chunks
+// are permuted by the row number so that 32 rows' reads meet no bank twice.
+// An operand whose contraction runs across memory (W in dgrad, both in wgrad)
+// lies as 64 rows of BM or BN values; the transposing LDS reads of gfx950
+// (four 16-bit rows of 16 columns per 16 lanes) hand each lane 4 values down
+// a column, two of them make its 8.  There the 64-byte pieces of a row are
+// permuted by the low two bits of the row number, so the four rows of a read
+// lie in different banks.
+//
+// What lies outside an operand reads as zero by the range check of its
+// buffer resource: rows behind the expert's last one, and the contraction
+// behind its end (pushed out of range by hand where memory goes on there).
+#pragma once
+#include "ops.hpp"
+
+namespace strata {
+
+constexpr int GP_C = 64;          // contraction per step
+
+struct GroupItem {
+    int32_t expert, row0, n;
+};
+
+struct GroupArgs {
+    const uint16_t *A, *B;      // product: x, W; dgrad: dy, W; wgrad: dy, x
+    void *C;
+    const int32_t *offsets;
+    GroupItem *items;           // tiles of up to tile_rows rows of one expert
+    int32_t *n_items;
+    int rows, E, N, K, tile_rows, c_bf16;
+};
+
+// One operand: R rows of it in the tile (m or n), NT threads stage it.
+template <int R, int ACROSS, int NT> struct Operand {
+    static constexpr int BYTES = R * GP_C * 2, LOADS = R * 8 / NT;
+    static_assert(LOADS * NT == R * 8, "whole chunks per thread");
+    const uint16_t *base;       // along: first row's first value; across: first contraction row
+    int ld, count, cd;          // row length in memory, rows of the tile in range (along), contraction
+    uint32_t off[LOADS];        // byte offset of this thread's chunks at step 0
+    int col0;
+
+    // p: the operand's first value; tile rows r0.. of `total`.
+    __device__ __forceinline__ void init(const uint16_t *p, int ld_, int r0, int total, int cd_) {
+        ld = ld_;
+        cd = cd_;
+        col0 = r0;
+        count = ACROSS ? 0 : min(total - r0, R);
+        base = ACROSS ? p : p + (int64_t)r0 * ld;
+        const int th = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int q = i * NT + th;
+            if (ACROSS) {
+                const int c = q / (R / 8), at = q % (R / 8);
+                off[i] = (uint32_t)c * (uint32_t)ld * 2u + (uint32_t)(r0 + 8 * (at ^ ((c & 3) << 2))) * 2u;
+            } else {
+                const int r = q >> 3, at = q & 7;
+                off[i] = (uint32_t)r * (uint32_t)ld * 2u + (uint32_t)(8 * (at ^ ((r ^ (r >> 3)) & 7))) * 2u;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load(int s, uint8_t *__restrict__ dst) const {
+        const int th = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(th >> 6);
+        const int left = cd - s * GP_C;   // contraction from this step on
+        const uint16_t *p = ACROSS ? base + (int64_t)s * GP_C * ld : base + (int64_t)s * GP_C;
+        const uint32_t bytes = ACROSS ? (uint32_t)min(left, GP_C) * (uint32_t)ld * 2u
+                                      : ((uint32_t)(count - 1) * (uint32_t)ld + (uint32_t)left) * 2u;
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p), 0, (int)bytes, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            uint32_t o = off[i];
+            if (!ACROSS && left < GP_C) {   // a last short step: chunks behind the end
+                const int q = i * NT + th, row = q >> 3;
+                if (8 * ((q & 7) ^ ((row ^ (row >> 3)) & 7)) >= left) o = 0x80000000u;
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (__attribute__((address_space(3))) void *)(dst + (i * NT + wv * 64) * 16), 16, o, 0, 0, 0);
+        }
+    }
+};
+
+// The 8 values a lane feeds to one 32x32x16 product: tile rows r0 + lane%32,
+// contraction 16 kk + 8 (lane/32) .. +8 of the staged step.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+template <int R, int ACROSS>
+__device__ __forceinline__ bf16x8_t read_frag(const uint8_t *__restrict__ t, int r0, int kk) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (!ACROSS) {
+        const int r = r0 + (lane & 31), c = 2 * kk + (lane >> 5);
+        return __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(t + r * 128 + 16 * (c ^ ((r ^ (r >> 3)) & 7))));
+    } else {
+        const int i = lane & 15, g = lane >> 4;
+        const int c = 16 * kk + 8 * (g >> 1) + (i >> 2);   // second read: c + 4, the same low bits
+        const int chunk = (r0 >> 3) + 2 * (g & 1) + ((i >> 1) & 1);
+        const uint8_t *p = t + c * (R * 2) + 16 * (chunk ^ ((c & 3) << 2)) + 8 * (i & 1);
+        typedef __attribute__((address_space(3))) s16x4_t lds4;
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 4 * R * 2));
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+}
+
+// All loads but the newest N done, this wave's LDS reads done, then the block's barrier.
+template <int N> __device__ __forceinline__ void wait_and_meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | ((N >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// One staged step on the wave's MT x NT2 subtiles of 32x32.  The fragments of
+// the next 16 are read while the current 16 are multiplied; the scheduling
+// barriers keep the compiler from reading the whole step ahead, which costs
+// more registers than the accumulators leave.
+template <int BM, int BN, int MT, int NT2, int TA, int TB>
+__device__ __forceinline__ void step_product(const uint8_t *__restrict__ ta, const uint8_t *__restrict__ tb, int m0,
+                                             int n0, f32x16_t (&acc)[MT][NT2]) {
+    bf16x8_t a[2][MT], b[2][NT2];
+#define READ_FRAGS(KK)                                                                                  \
+    {                                                                                                   \
+        _Pragma("unroll") for (int j = 0; j < NT2; ++j) b[(KK)&1][j] = read_frag<BN, TB>(tb, n0 + 32 * j, KK); \
+        _Pragma("unroll") for (int i = 0; i < MT; ++i) a[(KK)&1][i] = read_frag<BM, TA>(ta, m0 + 32 * i, KK);  \
+    }
+    READ_FRAGS(0)
+#pragma unroll
+    for (int kk = 0; kk < GP_C / 16; ++kk) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (kk + 1 < GP_C / 16) READ_FRAGS(kk + 1)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT2; ++j) acc[i][j] = mfma(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
+    }
+#undef READ_FRAGS
+}
+
+// The contraction with two buffers: step s+1 comes in while step s is
+// multiplied.  The four buffers are distinct restrict pointers so that the
+// compiler sees that a read does not wait for the loads into the others.
+template <typename OA, typename OB, int BM, int BN, int MT, int NT2, int TA, int TB>
+__device__ __forceinline__ void contract2(const OA &A, const OB &B, uint8_t *__restrict__ a0, uint8_t *__restrict__ b0,
+                                          uint8_t *__restrict__ a1, uint8_t *__restrict__ b1, int steps, int m0, int n0,
+                                          f32x16_t (&acc)[MT][NT2]) {
+    if (steps == 0) return;
+    A.load(0, a0);
+    B.load(0, b0);
+    int s = 0;
+    for (; s + 2 <= steps; s += 2) {
+        wait_and_meet<0>();
+        A.load(s + 1, a1);
+        B.load(s + 1, b1);
+        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, acc);
+        wait_and_meet<0>();
+        if (s + 2 < steps) {
+            A.load(s + 2, a0);
+            B.load(s + 2, b0);
+        }
+        step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, acc);
+    }
+    if (s < steps) {
+        wait_and_meet<0>();
+        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, acc);
+    }
+}
+
+// Rows m0 + .. < M, columns n0 + .. < Nn of the wave's subtiles to C (row length Nn).
+template <int MT, int NT2>
+__device__ __forceinline__ void store_tile(void *C, int c_bf16, int64_t row0, int m0, int M, int n0, int Nn,
+                                           const f32x16_t (&acc)[MT][NT2]) {
+    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int m = m0 + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+            if (m < M) {
+                const int64_t at = (row0 + m) * Nn;
+#pragma unroll
+                for (int j = 0; j < NT2; ++j) {
+                    const int n = n0 + 32 * j + l;
+                    if (n < Nn) {
+                        if (c_bf16) ((uint16_t *)C)[at + n] = f2bf(acc[i][j][v]);
+                        else ((float *)C)[at + n] = acc[i][j][v];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Block -> (tile, column tile): the column tiles of a row tile, and the row
+// tiles of an expert, on one XCD (blocks go to the 8 XCDs in turn).
+__device__ __forceinline__ bool group_tile(int nct, int n_items, int &item, int &ct) {
+    const int64_t total = (int64_t)nct * n_items;
+    const int64_t per = (total + 7) >> 3;
+    const int64_t q = blockIdx.x >> 3, bb = (blockIdx.x & 7) * per + q;
+    if (q >= per || bb >= total) return false;
+    item = (int)(bb / nct);
+    ct = (int)(bb - (int64_t)item * nct);
+    return true;
+}
+
+// BM x BN tiles, WM x WN waves, C rows are an expert's rows (product, dgrad).
+template <int BM, int BN, int WM, int WN, int TB>
+__global__ __launch_bounds__(64 * WM *WN) void grouped_rows_kernel(GroupArgs a) {
+    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
+    typedef Operand<BM, 0, NT> OA;
+    typedef Operand<BN, TB, NT> OB;
+    __shared__ __attribute__((aligned(128))) uint8_t a0[OA::BYTES], a1[OA::BYTES], b0[OB::BYTES], b1[OB::BYTES];
+    const int Cd = TB ? a.N : a.K, Nn = TB ? a.K : a.N;
+    int item, ct;
+    if (!group_tile((Nn + BN - 1) / BN, *a.n_items, item, ct)) return;
+    const GroupItem it = a.items[item];
+    OA A;
+    OB B;
+    A.init(a.A + (int64_t)it.row0 * Cd, Cd, 0, it.n, Cd);
+    B.init(a.B + (int64_t)it.expert * a.N * a.K, TB ? Nn : Cd, ct * BN, Nn, Cd);
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wv / WN) * 32 * MT, n0 = (wv % WN) * 32 * NT2;
+    f32x16_t acc[MT][NT2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    contract2<OA, OB, BM, BN, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, (Cd + GP_C - 1) / GP_C, m0, n0, acc);
+    store_tile<MT, NT2>(a.C, a.c_bf16, it.row0, m0, it.n, ct * BN + n0, Nn, acc);
+}
+
+// C is an expert's [N][K] weights' gradient.
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a) {
+    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
+    typedef Operand<BM, 1, NT> OA;
+    typedef Operand<BN, 1, NT> OB;
+    __shared__ __attribute__((aligned(128))) uint8_t a0[OA::BYTES], a1[OA::BYTES], b0[OB::BYTES], b1[OB::BYTES];
+    const int nk = (a.K + BN - 1) / BN, per_e = nk * ((a.N + BM - 1) / BM);
+    int e, t;
+    if (!group_tile(per_e, a.E, e, t)) return;
+    const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], 0), a.rows);
+    const int cd = max(hi - lo, 0), r0 = (t / nk) * BM, k0 = (t % nk) * BN;
+    OA A;
+    OB B;
+    A.init(a.A + (int64_t)lo * a.N, a.N, r0, a.N, cd);
+    B.init(a.B + (int64_t)lo * a.K, a.K, k0, a.K, cd);
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = (wv / WN) * 32 * MT, n0 = (wv % WN) * 32 * NT2;
+    f32x16_t acc[MT][NT2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    contract2<OA, OB, BM, BN, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, (cd + GP_C - 1) / GP_C, m0, n0, acc);
+    store_tile<MT, NT2>(a.C, a.c_bf16, (int64_t)e * a.N, r0 + m0, a.N, k0 + n0, a.K, acc);
+}
+
+}  // namespace strata
