@@ -93,6 +93,7 @@ template <int R, int ACROSS, int NT> struct Operand {
 
 // The 8 values a lane feeds to one 32x32x16 product: tile rows r0 + lane%32,
 // contraction 16 kk + 8 (lane/32) .. +8 of the staged step.
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 template <int R, int ACROSS>
 __device__ __forceinline__ bf16x8_t read_frag(const uint8_t *__restrict__ t, int r0, int kk) {
@@ -123,10 +124,18 @@ template <int N> __device__ __forceinline__ void wait_and_meet() {
 // One staged step on the wave's MT x NT2 subtiles of 32x32.  The fragments of
 // the next 16 are read while the current 16 are multiplied; the scheduling
 // barriers keep the compiler from reading the whole step ahead, which costs
-// more registers than the accumulators leave.
-template <int BM, int BN, int MT, int NT2, int TA, int TB>
+// more registers than the accumulators leave.  next(kk) issues the next
+// step's loads behind the reads, among the products (256 square, 32768 rows
+// of 16 experts, 2048 x 2048: dgrad 302 -> 268 us, wgrad 286 -> 256 us against
+// loads ahead of the step).  A wave without rows only stages.
+template <int BM, int BN, int MT, int NT2, int TA, int TB, typename Next>
 __device__ __forceinline__ void step_product(const uint8_t *__restrict__ ta, const uint8_t *__restrict__ tb, int m0,
-                                             int n0, f32x16_t (&acc)[MT][NT2]) {
+                                             int n0, bool active, f32x16_t (&acc)[MT][NT2], Next next) {
+    if (!active) {
+#pragma unroll
+        for (int kk = 0; kk < GP_C / 16; ++kk) next(kk);
+        return;
+    }
     bf16x8_t a[2][MT], b[2][NT2];
 #define READ_FRAGS(KK)                                                                                  \
     {                                                                                                   \
@@ -138,62 +147,84 @@ __device__ __forceinline__ void step_product(const uint8_t *__restrict__ ta, con
     for (int kk = 0; kk < GP_C / 16; ++kk) {
         __builtin_amdgcn_sched_barrier(0);
         if (kk + 1 < GP_C / 16) READ_FRAGS(kk + 1)
+        next(kk);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < NT2; ++j) acc[i][j] = mfma(a[kk & 1][i], b[kk & 1][j], acc[i][j]);
+            for (int j = 0; j < NT2; ++j) acc[i][j] = mfma(b[kk & 1][j], a[kk & 1][i], acc[i][j]);
     }
 #undef READ_FRAGS
 }
 
 // The contraction with two buffers: step s+1 comes in while step s is
-// multiplied.  The four buffers are distinct restrict pointers so that the
-// compiler sees that a read does not wait for the loads into the others.
+// multiplied, A's loads with the first 16, B's with the second.  The four
+// buffers are distinct restrict pointers so that the compiler sees that a
+// read does not wait for the loads into the others.  Two buffers of 64 beat
+// four of 32 (269 against 311 us for dgrad): the loads in flight are not
+// what bounds it.
 template <typename OA, typename OB, int BM, int BN, int MT, int NT2, int TA, int TB>
-__device__ __forceinline__ void contract2(const OA &A, const OB &B, uint8_t *__restrict__ a0, uint8_t *__restrict__ b0,
-                                          uint8_t *__restrict__ a1, uint8_t *__restrict__ b1, int steps, int m0, int n0,
-                                          f32x16_t (&acc)[MT][NT2]) {
+__device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *__restrict__ a0, uint8_t *__restrict__ b0,
+                                         uint8_t *__restrict__ a1, uint8_t *__restrict__ b1, int steps, int m0, int n0,
+                                         bool active, f32x16_t (&acc)[MT][NT2]) {
     if (steps == 0) return;
     A.load(0, a0);
     B.load(0, b0);
     int s = 0;
     for (; s + 2 <= steps; s += 2) {
         wait_and_meet<0>();
-        A.load(s + 1, a1);
-        B.load(s + 1, b1);
-        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, acc);
+        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, [&](int kk) {
+            if (kk == 0) A.load(s + 1, a1);
+            if (kk == 1) B.load(s + 1, b1);
+        });
         wait_and_meet<0>();
-        if (s + 2 < steps) {
-            A.load(s + 2, a0);
-            B.load(s + 2, b0);
-        }
-        step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, acc);
+        step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, active, acc, [&](int kk) {
+            if (kk == 0 && s + 2 < steps) A.load(s + 2, a0);
+            if (kk == 1 && s + 2 < steps) B.load(s + 2, b0);
+        });
     }
     if (s < steps) {
         wait_and_meet<0>();
-        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, acc);
+        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, [](int) {});
     }
 }
 
-// Rows m0 + .. < M, columns n0 + .. < Nn of the wave's subtiles to C (row length Nn).
+// The wave's subtiles to C (row length Nn): tile rows m0.. of `M`, columns
+// n0.. < Nn, C at the tile's first row.  B's fragments are the products'
+// first operand, so a lane holds one row, columns 8 (v/4) + 4 (lane/32) + v%4
+// of each subtile: 16-byte stores of fp32 as they are, of bf16 after the two
+// halves of the wave have exchanged every other group of four.  Rows and
+// columns outside the tile fall outside the buffer resource.
 template <int MT, int NT2>
-__device__ __forceinline__ void store_tile(void *C, int c_bf16, int64_t row0, int m0, int M, int n0, int Nn,
+__device__ __forceinline__ void store_tile(void *C, int c_bf16, int m0, int M, int n0, int Nn,
                                            const f32x16_t (&acc)[MT][NT2]) {
     const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+    const uint32_t esz = c_bf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(C, 0, (int)((uint32_t)M * (uint32_t)Nn * esz), 0x00020000);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
+        const uint32_t row = (uint32_t)(m0 + 32 * i + l) * (uint32_t)Nn;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            const int m = m0 + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-            if (m < M) {
-                const int64_t at = (row0 + m) * Nn;
+        for (int j = 0; j < NT2; ++j) {
+            const f32x16_t &v = acc[i][j];
+            if (c_bf16) {
 #pragma unroll
-                for (int j = 0; j < NT2; ++j) {
-                    const int n = n0 + 32 * j + l;
-                    if (n < Nn) {
-                        if (c_bf16) ((uint16_t *)C)[at + n] = f2bf(acc[i][j][v]);
-                        else ((float *)C)[at + n] = acc[i][j][v];
-                    }
+                for (int q = 0; q < 2; ++q) {
+                    // groups 2q and 2q+1 (4 values = 2 words each): after the swap words of 8 columns in a row
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[8 * q], v[8 * q + 1]),
+                                                                     bf16_pair(v[8 * q + 4], v[8 * q + 5]), false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[8 * q + 2], v[8 * q + 3]),
+                                                                     bf16_pair(v[8 * q + 6], v[8 * q + 7]), false, false);
+                    const int n = n0 + 32 * j + 16 * q + 8 * h;
+                    const uint32_t at = n < Nn ? (row + n) * 2u : 0xFFFFFFF0u;
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{s0[0], s1[0], s0[1], s1[1]}, r, at, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = n0 + 32 * j + 8 * q + 4 * h;
+                    const uint32_t at = n < Nn ? (row + n) * 4u : 0xFFFFFFF0u;
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        __builtin_bit_cast(u32x4_t, f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]}), r, at, 0, 0);
                 }
             }
         }
@@ -236,11 +267,28 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_rows_kernel(GroupArgs a) 
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    contract2<OA, OB, BM, BN, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, (Cd + GP_C - 1) / GP_C, m0, n0, acc);
-    store_tile<MT, NT2>(a.C, a.c_bf16, it.row0, m0, it.n, ct * BN + n0, Nn, acc);
+    contract<OA, OB, BM, BN, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, (Cd + GP_C - 1) / GP_C, m0, n0, m0 < it.n, acc);
+    store_tile<MT, NT2>((char *)a.C + (int64_t)it.row0 * Nn * (a.c_bf16 ? 2 : 4), a.c_bf16, m0, it.n, ct * BN + n0, Nn, acc);
 }
 
-// C is an expert's [N][K] weights' gradient.
+// The expert with the r-th most rows (of equals the lower index), E <= 64: lane e ranks expert e.
+__device__ __forceinline__ int expert_by_rows(const GroupArgs &a, int r) {
+    const int lane = threadIdx.x & 63;
+    const int n = lane < a.E ? (int)((uint32_t)a.offsets[lane + 1] - (uint32_t)a.offsets[lane]) : 0;
+    int rank = 0;
+    for (int j = 0; j < a.E; ++j) {
+        const int o = __builtin_amdgcn_readlane(n, j);
+        rank += (o > n || (o == n && j < lane)) ? 1 : 0;
+    }
+    return __ffsll((unsigned long long)__ballot(lane < a.E && rank == r)) - 1;
+}
+
+// C is an expert's [N][K] weights' gradient.  Rows go unevenly to experts, so
+// a tile's work does too: with up to 64 experts the blocks take them by
+// falling row count and spread each over the XCDs (16 unevenly picked experts over 32768
+// rows, 1536 x 2048: both gradients 697 -> 455 us with the loads moved among the products); with more, the
+// experts even out and an expert's tiles stay on one XCD, which reads its
+// rows into one L2.
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
@@ -249,7 +297,15 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a)
     __shared__ __attribute__((aligned(128))) uint8_t a0[OA::BYTES], a1[OA::BYTES], b0[OB::BYTES], b1[OB::BYTES];
     const int nk = (a.K + BN - 1) / BN, per_e = nk * ((a.N + BM - 1) / BM);
     int e, t;
-    if (!group_tile(per_e, a.E, e, t)) return;
+    if (a.E <= 64) {
+        // few experts: the one with the most rows first, each one's tiles dealt to all XCDs
+        t = blockIdx.x % per_e;
+        e = blockIdx.x / per_e;
+        if (e >= a.E) return;
+        e = expert_by_rows(a, e);
+    } else if (!group_tile(per_e, a.E, e, t)) {
+        return;
+    }
     const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], 0), a.rows);
     const int cd = max(hi - lo, 0), r0 = (t / nk) * BM, k0 = (t % nk) * BN;
     OA A;
@@ -265,8 +321,9 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a)
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    contract2<OA, OB, BM, BN, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, (cd + GP_C - 1) / GP_C, m0, n0, acc);
-    store_tile<MT, NT2>(a.C, a.c_bf16, (int64_t)e * a.N, r0 + m0, a.N, k0 + n0, a.K, acc);
+    contract<OA, OB, BM, BN, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, (cd + GP_C - 1) / GP_C, m0, n0, true, acc);
+    store_tile<MT, NT2>((char *)a.C + ((int64_t)e * a.N + r0) * a.K * (a.c_bf16 ? 2 : 4), a.c_bf16, m0, min(a.N - r0, BM), k0 + n0,
+                        a.K, acc);
 }
 
 }  // namespace strata

@@ -222,7 +222,10 @@ def test_positions_outside_the_rows_copy_nothing():
 GROUPS = [  # rows per expert, N, K, rows behind the last
     ([1], 8, 8, 0), ([0, 3, 0], 64, 128, 5), ([1, 0, 2, 1, 0, 1], 1536, 2048, 0), ([5, 64, 65, 0, 1], 72, 104, 3),
     ([130, 0, 257], 264, 520, 1), ([0, 0], 64, 64, 4), ([33] * 40, 128, 256, 0), ([300], 256, 1024, 0),
-    ([16, 17, 31, 32, 48], 2048, 768, 0), ([700, 3], 200, 24, 0), ([90, 70, 0, 110], 512, 1032, 2)]
+    ([16, 17, 31, 32, 48], 2048, 768, 0), ([700, 3], 200, 24, 0), ([90, 70, 0, 110], 512, 1032, 2),
+    # few rows against the experts: one to nine rows of the experts that have any
+    ([0, 1, 2, 0, 3, 4, 5] + [0] * 62 + [1], 200, 1032, 1), ([0] * 40 + [9], 72, 24, 0), ([0, 2] + [0] * 6, 1536, 2048, 0),
+    ([1] + [0] * 19 + [3], 88, 8192, 1), ([1] + [0] * 3, 8, 8, 0), ([0] * 9, 16, 16, 2)]
 
 
 def group_inputs(ns, N, K, tail, seed=1):
