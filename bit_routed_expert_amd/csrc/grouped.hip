@@ -14,8 +14,6 @@
 
 namespace strata {
 
-constexpr int GP_E = 1024;         // most experts
-constexpr int GP_SMALL = 128, GP_LARGE = 256;   // edges of the two tiles
 
 // One block: the rows of every expert (cut to 0..rows and made to ascend by
 // a running maximum, so tiles never overlap and their number is bounded),
@@ -172,10 +170,8 @@ __global__ __launch_bounds__(256) void grouped_few_kernel(GroupArgs a, int slabs
 
 namespace {
 
-constexpr size_t GP_HEAD = 256;   // the tile count, then the list
-
-// Rows per expert, on average, from which on the larger tile takes them.
-bool large_rows(int64_t rows, int E) { return rows >= 192 * (int64_t)E; }
+constexpr size_t GP_HEAD = 256;     // the tile count, then the list
+constexpr int GP_MIN_ROWS = 32;     // smallest row tile
 
 // Rows against experts up to which the product goes without the matrix cores.
 bool few_rows_path(int64_t rows, int E, int K) { return rows * 4 <= E && K <= GV_MAX_K; }
@@ -206,33 +202,55 @@ strata_status grouped_call(const void *A, const void *B, const int32_t *offsets,
     a.E = E;
     a.N = N;
     a.K = K;
-    a.tile_rows = large_rows(rows, E) ? GP_LARGE : GP_SMALL;
     a.c_bf16 = dtype == STRATA_X_BF16;
     return STRATA_OK;
 }
 
-template <int TB> strata_status grouped_rows(const GroupArgs &a, hipStream_t s) {
+// Blocks of a grid up to which each finds its own row tile; above, a launch
+// before lists them.  The list costs a launch and about 5 us; the search
+// about 1 us in every block.
+constexpr int64_t GP_FIND_BLOCKS = 512;
+
+template <int BM, int BN, int WM, int WN, int ST, int TB> strata_status launch_rows(GroupArgs &a, hipStream_t s) {
+    const int Nn = TB ? a.K : a.N;
+    a.tile_rows = BM;
+    const int64_t blocks = (max_tiles(a.rows, a.E, BM) * ((Nn + BN - 1) / BN) + 7) / 8 * 8;
+    if (blocks <= GP_FIND_BLOCKS) {
+        STRATA_LAUNCH((grouped_rows_kernel<BM, BN, WM, WN, ST, TB, 0>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
+        return hip_status(hipGetLastError());
+    }
     STRATA_LAUNCH(grouped_plan_kernel, dim3(1), dim3(1024), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return hip_status(e);
-    const int Nn = TB ? a.K : a.N;
-    const int64_t tiles = max_tiles(a.rows, a.E, a.tile_rows);
-    if (a.tile_rows == GP_LARGE) {
-        const int64_t blocks = (tiles * ((Nn + GP_LARGE - 1) / GP_LARGE) + 7) / 8 * 8;
-        STRATA_LAUNCH((grouped_rows_kernel<GP_LARGE, GP_LARGE, 2, 4, TB>), dim3((unsigned)blocks), dim3(512), 0, s, a);
-    } else {
-        const int64_t blocks = (tiles * ((Nn + GP_SMALL - 1) / GP_SMALL) + 7) / 8 * 8;
-        STRATA_LAUNCH((grouped_rows_kernel<GP_SMALL, GP_SMALL, 2, 2, TB>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-    }
+    STRATA_LAUNCH((grouped_rows_kernel<BM, BN, WM, WN, ST, TB, 1>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
     return hip_status(hipGetLastError());
 }
 
+// Tile by the average rows of an expert.  Up to 16, 32-row tiles: the weights
+// bound it and more, smaller blocks keep more of them in flight (E = 16, 16
+// rows each, 1536 x 2048: 22 us against 26 us for 128-row tiles; E = 512, 2
+// rows: 400 against 412).  Then 128 x 256 with three buffers (E = 512, 64
+// rows: 647 us, 5.0 TB/s, against 826 us).  From 384 rows on, and with tiles
+// enough for the 256 CUs, 256 x 256, whose operands are read half as often
+// (E = 16, 4096 rows: 406 against 438 us; with 256 rows 53 against 37 us).
+template <int TB> strata_status grouped_rows(GroupArgs &a, hipStream_t s) {
+    const int64_t rows = a.rows, E = a.E;
+    const int Nn = TB ? a.K : a.N;
+    if (rows <= 16 * E) return launch_rows<GP_MIN_ROWS, 128, 1, 4, 4, TB>(a, s);
+    if (rows < 384 * E || rows / 256 * ((Nn + 255) / 256) < 192) return launch_rows<128, 256, 2, 4, 3, TB>(a, s);
+    return launch_rows<256, 256, 2, 4, 2, TB>(a, s);
+}
+
+// The gradient's tiles: 256 square where there are enough for the 256 CUs,
+// else 128 square.
 strata_status grouped_weights(const GroupArgs &a, hipStream_t s) {
-    const bool large = a.N > GP_SMALL && a.K > GP_SMALL;
-    const int t = large ? GP_LARGE : GP_SMALL;
-    const int64_t blocks = ((int64_t)a.E * ((a.N + t - 1) / t) * ((a.K + t - 1) / t) + 7) / 8 * 8;
-    if (large) STRATA_LAUNCH((grouped_wgrad_kernel<GP_LARGE, GP_LARGE, 2, 4>), dim3((unsigned)blocks), dim3(512), 0, s, a);
-    else STRATA_LAUNCH((grouped_wgrad_kernel<GP_SMALL, GP_SMALL, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+    const int64_t large = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+    if (large >= 192 && a.N > 128 && a.K > 128) {
+        STRATA_LAUNCH((grouped_wgrad_kernel<256, 256, 2, 4, 2>), dim3((unsigned)((large + 7) / 8 * 8)), dim3(512), 0, s, a);
+    } else {
+        const int64_t blocks = ((int64_t)a.E * ((a.N + 127) / 128) * ((a.K + 127) / 128) + 7) / 8 * 8;
+        STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+    }
     return hip_status(hipGetLastError());
 }
 
@@ -246,7 +264,7 @@ extern "C" {
 
 size_t strata_moe_grouped_workspace_bytes(int32_t rows, int32_t n_experts, int32_t N, int32_t K) {
     if (check_grouped(rows, n_experts, N, K) != STRATA_OK) return 0;
-    return GP_HEAD + (size_t)(max_tiles(rows, n_experts, GP_SMALL) + 1) * sizeof(GroupItem);
+    return GP_HEAD + (size_t)(max_tiles(rows, n_experts, GP_MIN_ROWS) + 1) * sizeof(GroupItem);
 }
 
 strata_status strata_moe_grouped_product(const void *x, const void *W, const int32_t *offsets, int32_t rows,

@@ -3,8 +3,8 @@
 // One block computes a tile C[BM][BN] = sum_c A[m][c] B[n][c] of one expert.
 // The contraction is cut into steps of 64; a step's tiles of A and B come
 // into LDS by direct global->LDS loads (16 bytes a lane, no registers) while
-// earlier steps run on the matrix cores: ST buffers in turn, one barrier a
-// step.
+// earlier steps run on the matrix cores: 2 to 4 buffers in turn, one barrier
+// a step.
 //
 // An operand whose contraction runs along memory (x and W in the product)
 // lies in LDS as it does in memory, 64 values (128 bytes) to a row; a lane's
@@ -26,6 +26,7 @@
 namespace strata {
 
 constexpr int GP_C = 64;          // contraction per step
+constexpr int GP_E = 1024;        // most experts
 
 struct GroupItem {
     int32_t expert, row0, n;
@@ -72,10 +73,10 @@ template <int R, int ACROSS, int NT> struct Operand {
 
     __device__ __forceinline__ void load(int s, uint8_t *__restrict__ dst) const {
         const int th = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(th >> 6);
-        const int left = cd - s * GP_C;   // contraction from this step on
+        const int left = max(cd - s * GP_C, 0);   // contraction from this step on (0: a load behind the end, all zeros)
         const uint16_t *p = ACROSS ? base + (int64_t)s * GP_C * ld : base + (int64_t)s * GP_C;
         const uint32_t bytes = ACROSS ? (uint32_t)min(left, GP_C) * (uint32_t)ld * 2u
-                                      : ((uint32_t)(count - 1) * (uint32_t)ld + (uint32_t)left) * 2u;
+                                      : left ? ((uint32_t)(count - 1) * (uint32_t)ld + (uint32_t)left) * 2u : 0u;
         const __amdgpu_buffer_rsrc_t r =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p), 0, (int)bytes, 0x00020000);
 #pragma unroll
@@ -156,37 +157,67 @@ __device__ __forceinline__ void step_product(const uint8_t *__restrict__ ta, con
 #undef READ_FRAGS
 }
 
-// The contraction with two buffers: step s+1 comes in while step s is
-// multiplied, A's loads with the first 16, B's with the second.  The four
-// buffers are distinct restrict pointers so that the compiler sees that a
-// read does not wait for the loads into the others.  Two buffers of 64 beat
-// four of 32 (269 against 311 us for dgrad): the loads in flight are not
-// what bounds it.
-template <typename OA, typename OB, int BM, int BN, int MT, int NT2, int TA, int TB>
+// The contraction with ST buffers: step s is multiplied while the ST - 1
+// behind it come in, A's loads issued with the first 16, B's with the second.
+// The buffers are distinct restrict pointers so that the compiler sees that a
+// read does not wait for the loads into the others.  With more than two
+// buffers, loads behind the end fetch nothing and keep the count of loads in
+// flight the same.
+template <int ST, typename OA, typename OB, int BM, int BN, int MT, int NT2, int TA, int TB>
 __device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *__restrict__ a0, uint8_t *__restrict__ b0,
-                                         uint8_t *__restrict__ a1, uint8_t *__restrict__ b1, int steps, int m0, int n0,
-                                         bool active, f32x16_t (&acc)[MT][NT2]) {
+                                         uint8_t *__restrict__ a1, uint8_t *__restrict__ b1, uint8_t *__restrict__ a2,
+                                         uint8_t *__restrict__ b2, uint8_t *__restrict__ a3, uint8_t *__restrict__ b3,
+                                         int steps, int m0, int n0, bool active, f32x16_t (&acc)[MT][NT2]) {
+    constexpr int L = OA::LOADS + OB::LOADS;   // a wave's loads per step
     if (steps == 0) return;
+#define STEP(S, AR, BR, AW, BW)                                                                     \
+    {                                                                                               \
+        wait_and_meet<(ST - 2) * L>();                                                              \
+        step_product<BM, BN, MT, NT2, TA, TB>(AR, BR, m0, n0, active, acc, [&](int kk) {            \
+            const bool more = ST > 2 || (S) + 1 < steps;                                            \
+            if (kk == 0 && more) A.load((S) + ST - 1, AW);                                          \
+            if (kk == 1 && more) B.load((S) + ST - 1, BW);                                          \
+        });                                                                                         \
+    }
     A.load(0, a0);
     B.load(0, b0);
+    if constexpr (ST > 2) {
+        A.load(1, a1);
+        B.load(1, b1);
+    }
+    if constexpr (ST > 3) {
+        A.load(2, a2);
+        B.load(2, b2);
+    }
     int s = 0;
-    for (; s + 2 <= steps; s += 2) {
-        wait_and_meet<0>();
-        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, [&](int kk) {
-            if (kk == 0) A.load(s + 1, a1);
-            if (kk == 1) B.load(s + 1, b1);
-        });
-        wait_and_meet<0>();
-        step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, active, acc, [&](int kk) {
-            if (kk == 0 && s + 2 < steps) A.load(s + 2, a0);
-            if (kk == 1 && s + 2 < steps) B.load(s + 2, b0);
-        });
+    for (; s + ST <= steps; s += ST) {
+        if constexpr (ST == 2) {
+            STEP(s, a0, b0, a1, b1)
+            STEP(s + 1, a1, b1, a0, b0)
+        } else if constexpr (ST == 3) {
+            STEP(s, a0, b0, a2, b2)
+            STEP(s + 1, a1, b1, a0, b0)
+            STEP(s + 2, a2, b2, a1, b1)
+        } else {
+            STEP(s, a0, b0, a3, b3)
+            STEP(s + 1, a1, b1, a0, b0)
+            STEP(s + 2, a2, b2, a1, b1)
+            STEP(s + 3, a3, b3, a2, b2)
+        }
     }
-    if (s < steps) {
-        wait_and_meet<0>();
-        step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, [](int) {});
-    }
+#undef STEP
+    const auto none = [](int) {};
+    wait_and_meet<0>();   // the last steps, and no load outlives the loop
+    if (s < steps) step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, none);
+    if (ST > 2 && s + 1 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, active, acc, none);
+    if (ST > 3 && s + 2 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a2, b2, m0, n0, active, acc, none);
 }
+
+// The ST buffers of a block's two operands.
+#define GROUP_BUFFERS(ST, OA, OB)                                                                             \
+    __shared__ __attribute__((aligned(128))) uint8_t a0[OA::BYTES], a1[OA::BYTES], b0[OB::BYTES], b1[OB::BYTES]; \
+    __shared__ __attribute__((aligned(128))) uint8_t a2[ST > 2 ? OA::BYTES : 16], b2[ST > 2 ? OB::BYTES : 16],   \
+        a3[ST > 3 ? OA::BYTES : 16], b3[ST > 3 ? OB::BYTES : 16];
 
 // The wave's subtiles to C (row length Nn): tile rows m0.. of `M`, columns
 // n0.. < Nn, C at the tile's first row.  B's fragments are the products'
@@ -243,17 +274,80 @@ __device__ __forceinline__ bool group_tile(int nct, int n_items, int &item, int 
     return true;
 }
 
-// BM x BN tiles, WM x WN waves, C rows are an expert's rows (product, dgrad).
-template <int BM, int BN, int WM, int WN, int TB>
+// Row tile `item` of the call, found from the offsets by a block of NT
+// threads (each takes 1024 / NT experts), and how many there are in all.
+template <int NT> struct FindItem {
+    static constexpr int PE = GP_E / NT;
+    int n[PE], lo[PE], first, total;
+    __device__ __forceinline__ void scan(const GroupArgs &a, int *wsum) {
+        const int th = threadIdx.x, lane = th & 63, w = th >> 6;
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < PE; ++q) {
+            const int e = th * PE + q;
+            lo[q] = e < a.E ? min(max(a.offsets[e], 0), a.rows) : 0;
+            const int hi = e < a.E ? min(max(a.offsets[e + 1], 0), a.rows) : 0;
+            n[q] = max(hi - lo[q], 0);
+            c += (n[q] + a.tile_rows - 1) / a.tile_rows;
+        }
+        int s = c;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int q = __shfl_up(s, o, 64);
+            if (lane >= o) s += q;
+        }
+        if (lane == 63) wsum[w] = s;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int q = 0; q < NT / 64; ++q) {
+            const int v = wsum[q];
+            s += q < w ? v : 0;
+            total += v;
+        }
+        first = s - c;
+    }
+    __device__ __forceinline__ GroupItem get(const GroupArgs &a, int item, GroupItem *shared) const {
+        int f = first;
+#pragma unroll
+        for (int q = 0; q < PE; ++q) {
+            const int tiles = (n[q] + a.tile_rows - 1) / a.tile_rows;
+            if (item >= f && item < f + tiles) {
+                const int r = (item - f) * a.tile_rows;
+                *shared = GroupItem{(int)threadIdx.x * PE + q, lo[q] + r, min(a.tile_rows, n[q] - r)};
+            }
+            f += tiles;
+        }
+        __syncthreads();
+        return *shared;
+    }
+};
+
+// BM x BN tiles, WM x WN waves, ST buffers; C rows are an expert's rows
+// (product, dgrad).  LIST: the row tiles were listed by an earlier launch.
+template <int BM, int BN, int WM, int WN, int ST, int TB, int LIST>
 __global__ __launch_bounds__(64 * WM *WN) void grouped_rows_kernel(GroupArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
     typedef Operand<BM, 0, NT> OA;
     typedef Operand<BN, TB, NT> OB;
-    __shared__ __attribute__((aligned(128))) uint8_t a0[OA::BYTES], a1[OA::BYTES], b0[OB::BYTES], b1[OB::BYTES];
+    GROUP_BUFFERS(ST, OA, OB)
     const int Cd = TB ? a.N : a.K, Nn = TB ? a.K : a.N;
     int item, ct;
-    if (!group_tile((Nn + BN - 1) / BN, *a.n_items, item, ct)) return;
-    const GroupItem it = a.items[item];
+    GroupItem it;
+    if (LIST) {
+        if (!group_tile((Nn + BN - 1) / BN, *a.n_items, item, ct)) return;
+        it = a.items[item];
+    } else {
+        __shared__ int wsum[NT / 64];
+        __shared__ GroupItem found;
+        FindItem<NT> f;
+        f.scan(a, wsum);
+        if (!group_tile((Nn + BN - 1) / BN, f.total, item, ct)) return;
+        it = f.get(a, item, &found);
+        it.expert = __builtin_amdgcn_readfirstlane(it.expert);
+        it.row0 = __builtin_amdgcn_readfirstlane(it.row0);
+        it.n = __builtin_amdgcn_readfirstlane(it.n);
+    }
     OA A;
     OB B;
     A.init(a.A + (int64_t)it.row0 * Cd, Cd, 0, it.n, Cd);
@@ -267,8 +361,10 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_rows_kernel(GroupArgs a) 
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    contract<OA, OB, BM, BN, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, (Cd + GP_C - 1) / GP_C, m0, n0, m0 < it.n, acc);
-    store_tile<MT, NT2>((char *)a.C + (int64_t)it.row0 * Nn * (a.c_bf16 ? 2 : 4), a.c_bf16, m0, it.n, ct * BN + n0, Nn, acc);
+    contract<ST, OA, OB, BM, BN, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, (Cd + GP_C - 1) / GP_C, m0, n0,
+                                                 m0 < it.n, acc);
+    store_tile<MT, NT2>((char *)a.C + (int64_t)it.row0 * Nn * (a.c_bf16 ? 2 : 4), a.c_bf16, m0, it.n, ct * BN + n0, Nn,
+                        acc);
 }
 
 // The expert with the r-th most rows (of equals the lower index), E <= 64: lane e ranks expert e.
@@ -285,20 +381,19 @@ __device__ __forceinline__ int expert_by_rows(const GroupArgs &a, int r) {
 
 // C is an expert's [N][K] weights' gradient.  Rows go unevenly to experts, so
 // a tile's work does too: with up to 64 experts the blocks take them by
-// falling row count and spread each over the XCDs (16 unevenly picked experts over 32768
-// rows, 1536 x 2048: both gradients 697 -> 455 us with the loads moved among the products); with more, the
-// experts even out and an expert's tiles stay on one XCD, which reads its
-// rows into one L2.
-template <int BM, int BN, int WM, int WN>
+// falling row count and spread each over the XCDs (16 unevenly picked experts
+// over 32768 rows, 1536 x 2048: both gradients 697 -> 455 us with the loads
+// moved among the products); with more, the experts even out and an expert's
+// tiles stay on one XCD, which reads its rows into one L2.
+template <int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
     typedef Operand<BM, 1, NT> OA;
     typedef Operand<BN, 1, NT> OB;
-    __shared__ __attribute__((aligned(128))) uint8_t a0[OA::BYTES], a1[OA::BYTES], b0[OB::BYTES], b1[OB::BYTES];
+    GROUP_BUFFERS(ST, OA, OB)
     const int nk = (a.K + BN - 1) / BN, per_e = nk * ((a.N + BM - 1) / BM);
     int e, t;
     if (a.E <= 64) {
-        // few experts: the one with the most rows first, each one's tiles dealt to all XCDs
         t = blockIdx.x % per_e;
         e = blockIdx.x / per_e;
         if (e >= a.E) return;
@@ -321,9 +416,10 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a)
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    contract<OA, OB, BM, BN, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, (cd + GP_C - 1) / GP_C, m0, n0, true, acc);
-    store_tile<MT, NT2>((char *)a.C + ((int64_t)e * a.N + r0) * a.K * (a.c_bf16 ? 2 : 4), a.c_bf16, m0, min(a.N - r0, BM), k0 + n0,
-                        a.K, acc);
+    contract<ST, OA, OB, BM, BN, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, (cd + GP_C - 1) / GP_C, m0, n0,
+                                                true, acc);
+    store_tile<MT, NT2>((char *)a.C + ((int64_t)e * a.N + r0) * a.K * (a.c_bf16 ? 2 : 4), a.c_bf16, m0,
+                        min(a.N - r0, BM), k0 + n0, a.K, acc);
 }
 
 }  // namespace strata
