@@ -14,51 +14,65 @@ inline bool bad_dtype(int32_t t) { return t != STRATA_X_BF16 && t != STRATA_X_F3
 // A required row pointer: there and aligned.
 inline bool bad_rows(const void *p) { return !p || !aligned16(p); }
 
-// V consecutive values at p + i (elements of E), aligned to V elements (up
-// to 16 bytes at a time), as fp32.
-template <int V> __device__ __forceinline__ void load_values(const uint16_t *p, int64_t i, float (&v)[V]) {
+// V consecutive values at p + i, aligned to V elements (up to 16 bytes at a
+// time), as loaded.  Loads and conversions are apart so that a kernel can
+// issue all its loads before it waits for the first.
+template <typename E, int V> struct Raw;
+template <int V> struct Raw<float, V> { float w[V]; };
+template <int V> struct Raw<uint16_t, V> { uint32_t w[V >= 2 ? V / 2 : 1]; };
+
+template <int V> __device__ __forceinline__ void load_raw(const uint16_t *p, int64_t i, Raw<uint16_t, V> &r) {
     if constexpr (V == 8) {
         const uint4 q = *(const uint4 *)(p + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
+        r.w[0] = q.x;
+        r.w[1] = q.y;
+        r.w[2] = q.z;
+        r.w[3] = q.w;
     } else if constexpr (V == 4) {
         const uint2 q = *(const uint2 *)(p + i);
-        v[0] = __uint_as_float(q.x << 16);
-        v[1] = __uint_as_float(q.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(q.y << 16);
-        v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+        r.w[0] = q.x;
+        r.w[1] = q.y;
     } else if constexpr (V == 2) {
-        const uint32_t q = *(const uint32_t *)(p + i);
-        v[0] = __uint_as_float(q << 16);
-        v[1] = __uint_as_float(q & 0xFFFF0000u);
+        r.w[0] = *(const uint32_t *)(p + i);
     } else {
-        v[0] = bf16_to_float(p[i]);
+        r.w[0] = p[i];
     }
 }
-template <int V> __device__ __forceinline__ void load_values(const float *p, int64_t i, float (&v)[V]) {
+template <int V> __device__ __forceinline__ void load_raw(const float *p, int64_t i, Raw<float, V> &r) {
     if constexpr (V >= 4) {
 #pragma unroll
         for (int j = 0; j < V; j += 4) {
             const float4 q = *(const float4 *)(p + i + j);
-            v[j] = q.x;
-            v[j + 1] = q.y;
-            v[j + 2] = q.z;
-            v[j + 3] = q.w;
+            r.w[j] = q.x;
+            r.w[j + 1] = q.y;
+            r.w[j + 2] = q.z;
+            r.w[j + 3] = q.w;
         }
     } else if constexpr (V == 2) {
         const float2 q = *(const float2 *)(p + i);
-        v[0] = q.x;
-        v[1] = q.y;
+        r.w[0] = q.x;
+        r.w[1] = q.y;
     } else {
-        v[0] = p[i];
+        r.w[0] = p[i];
     }
 }
+template <typename E, int V> __device__ __forceinline__ void zero_raw(Raw<E, V> &r) {
+#pragma unroll
+    for (auto &w : r.w) w = 0;
+}
 
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) { return (uint32_t)f2bf(a) | ((uint32_t)f2bf(b) << 16); }
+// Value j of a loaded piece as fp32.
+template <int V> __device__ __forceinline__ float value(const Raw<float, V> &r, int j) { return r.w[j]; }
+template <int V> __device__ __forceinline__ float value(const Raw<uint16_t, V> &r, int j) {
+    return __uint_as_float(V == 1 || !(j & 1) ? r.w[j / 2] << 16 : r.w[j / 2] & 0xFFFF0000u);
+}
+
+// Two values rounded to bf16 in one word (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
 
 template <int V> __device__ __forceinline__ void store_values(uint16_t *p, int64_t i, const float (&v)[V]) {
     if constexpr (V == 8) {

@@ -22,17 +22,53 @@ template <int G> __device__ __forceinline__ bool row_group(int T, int &t, int &l
     return t < T;
 }
 
+// The positions (and weights) of up to PB picks r0.. of a token, -1 behind
+// the k-th.  Groups of whole waves read them once, a pick to a lane, and pass
+// them on as scalars; smaller groups read them lane by lane.
+template <int G> struct Picks {
+    int pos[PB];
+    float w[PB];
+    __device__ __forceinline__ void read(const int32_t *pt, const float *wt, int r0, int k, int rows) {
+        if constexpr (G >= 64) {
+            const int lane = threadIdx.x & 63;
+            const int r = r0 + (lane & (PB - 1));
+            const int p = r < k ? pt[r] : -1;
+            const int v = wt ? __builtin_bit_cast(int, r < k ? wt[r] : 0.f) : __builtin_bit_cast(int, 1.f);
+#pragma unroll
+            for (int q = 0; q < PB; ++q) {
+                const int c = __builtin_amdgcn_readlane(p, q);
+                pos[q] = (uint32_t)c < (uint32_t)rows ? c : -1;
+                w[q] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(v, q));
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < PB; ++q) {
+                pos[q] = -1;
+                w[q] = 1.f;
+                if (r0 + q < k) {
+                    const int c = pt[r0 + q];
+                    pos[q] = (uint32_t)c < (uint32_t)rows ? c : -1;
+                    if (wt) w[q] = wt[r0 + q];
+                }
+            }
+        }
+    }
+};
+
 template <typename P, int G>
 __global__ __launch_bounds__(256) void dispatch_kernel(const P *__restrict__ x, const int32_t *__restrict__ pos,
                                                        P *__restrict__ xs, int T, int k, int nc, int rows) {
     int t, lane;
     if (!row_group<G>(T, t, lane)) return;
-    const int32_t *pt = pos + (int64_t)t * k;
-    for (int c = lane; c < nc; c += G) {
-        const P v = x[(int64_t)t * nc + c];
-        for (int r = 0; r < k; ++r) {
-            const int p = pt[r];
-            if ((uint32_t)p < (uint32_t)rows) xs[(int64_t)p * nc + c] = v;
+    P v = lane < nc ? x[(int64_t)t * nc + lane] : P{};
+    for (int r0 = 0; r0 < k; r0 += PB) {
+        Picks<G> pk;
+        pk.read(pos + (int64_t)t * k, nullptr, r0, k, rows);
+        for (int c = lane; c < nc; c += G) {
+            if (c != lane || r0) v = x[(int64_t)t * nc + c];
+#pragma unroll
+            for (int r = 0; r < PB; ++r)
+                if (pk.pos[r] >= 0) xs[(int64_t)pk.pos[r] * nc + c] = v;
         }
     }
 }
@@ -45,32 +81,28 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const Y *__restrict__
     if (!row_group<G>(T, t, lane)) return;
     const int32_t *pt = pos + (int64_t)t * k;
     const float *wt = w ? w + (int64_t)t * k : nullptr;
+    Picks<G> pk;
+    pk.read(pt, wt, 0, k, rows);
     for (int i = lane * V; i < d; i += G * V) {
+        Raw<O, V> b;
+        zero_raw(b);
+        if (base) load_raw<V>(base, (int64_t)t * d + i, b);
         float s[V];
-        if (base) {
-            load_values<V>(base, (int64_t)t * d + i, s);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = 0.f;
-        }
         for (int r0 = 0; r0 < k; r0 += PB) {
-            float v[PB][V];
-            float g[PB];
-            bool has[PB];
+            if (k > PB) pk.read(pt, wt, r0, k, rows);
+            Raw<Y, V> v[PB];
 #pragma unroll
-            for (int r = 0; r < PB; ++r) {
-                const int p = r0 + r < k ? pt[r0 + r] : -1;
-                has[r] = (uint32_t)p < (uint32_t)rows;
-                if (has[r]) {
-                    g[r] = wt ? wt[r0 + r] : 1.f;
-                    load_values<V>(ys, (int64_t)p * d + i, v[r]);
-                }
+            for (int r = 0; r < PB; ++r)
+                if (pk.pos[r] >= 0) load_raw<V>(ys, (int64_t)pk.pos[r] * d + i, v[r]);
+            if (r0 == 0) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] = value<V>(b, j);
             }
 #pragma unroll
             for (int r = 0; r < PB; ++r) {
-                if (has[r]) {
+                if (pk.pos[r] >= 0) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) s[j] = fmaf(g[r], v[r][j], s[j]);
+                    for (int j = 0; j < V; ++j) s[j] = fmaf(pk.w[r], value<V>(v[r], j), s[j]);
                 }
             }
         }
@@ -95,32 +127,33 @@ __global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__
         const int32_t *pt = pos + (int64_t)t * k;
         const float *wt = w + (int64_t)t * k;
         for (int r0 = 0; r0 < k; r0 += PB) {
+            Picks<G> pk;
+            pk.read(pt, wt, r0, k, rows);
             float dot[PB];
 #pragma unroll
             for (int r = 0; r < PB; ++r) dot[r] = 0.f;
             for (int i = lane * V; i < d; i += G * V) {
+                Raw<O, V> oraw;
+                load_raw<V>(dout, (int64_t)t * d + i, oraw);
+                Raw<Y, V> v[PB];
+#pragma unroll
+                for (int r = 0; r < PB; ++r)
+                    if (dots && pk.pos[r] >= 0) load_raw<V>(ys, (int64_t)pk.pos[r] * d + i, v[r]);
                 float o[V];
-                load_values<V>(dout, (int64_t)t * d + i, o);
-                float v[PB][V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) o[j] = value<V>(oraw, j);
 #pragma unroll
                 for (int r = 0; r < PB; ++r) {
-                    const int p = r0 + r < k ? pt[r0 + r] : -1;
-                    if (dots && (uint32_t)p < (uint32_t)rows) load_values<V>(ys, (int64_t)p * d + i, v[r]);
-                }
-#pragma unroll
-                for (int r = 0; r < PB; ++r) {
-                    const int p = r0 + r < k ? pt[r0 + r] : -1;
-                    if ((uint32_t)p < (uint32_t)rows) {
+                    if (pk.pos[r] >= 0) {
                         if (dots) {
 #pragma unroll
-                            for (int j = 0; j < V; ++j) dot[r] = fmaf(o[j], v[r][j], dot[r]);
+                            for (int j = 0; j < V; ++j) dot[r] = fmaf(o[j], value<V>(v[r], j), dot[r]);
                         }
                         if (dys) {
-                            const float gw = wt[r0 + r];
                             float q[V];
 #pragma unroll
-                            for (int j = 0; j < V; ++j) q[j] = gw * o[j];
-                            store_values<V>(dys, (int64_t)p * d + i, q);
+                            for (int j = 0; j < V; ++j) q[j] = pk.w[r] * o[j];
+                            store_values<V>(dys, (int64_t)pk.pos[r] * d + i, q);
                         }
                     }
                 }
