@@ -6,7 +6,10 @@
 // Bound by HBM: every row is read once and written once, so a row lives in
 // the registers of G threads (VALS values each) from its first load to its
 // last store, and the two norms are two sums over those registers (a wave
-// sum by lane exchanges, then the waves' sums through LDS).
+// sum by lane exchanges, then the waves' sums through LDS).  r and u are
+// stored with the streaming hint: 4096 rows of 2048 bf16 20.0 -> 15.4 us (5.5
+// TB/s), and a reader right behind loses as much as it gains; the gradient's
+// stores are plain (76.5 us against 81.5 over 8191 rows, 4.8 TB/s).
 //
 // Gradient, with rr = rstd_r, ry = rstd_y, <,> over the row's d elements:
 //   dR = dr + rr (g_pre du - r rr^2 <g_pre du, r> / d)
@@ -72,11 +75,11 @@ template <int V, int VALS, int G> struct Row<Any, V, VALS, G> {
     }
 };
 
-template <typename E, int V, int VALS, int G>
+template <typename E, int V, int VALS, int G, bool STREAM = false>
 __device__ __forceinline__ void row_store(void *p, int bf16, int64_t row, int d, int lane, const float (&v)[VALS]) {
     if constexpr (__is_same(E, Any)) {
-        if (bf16) row_store<uint16_t, V, VALS, G>(p, 1, row, d, lane, v);
-        else row_store<float, V, VALS, G>(p, 0, row, d, lane, v);
+        if (bf16) row_store<uint16_t, V, VALS, G, STREAM>(p, 1, row, d, lane, v);
+        else row_store<float, V, VALS, G, STREAM>(p, 0, row, d, lane, v);
     } else {
 #pragma unroll
         for (int q = 0; q < VALS / V; ++q) {
@@ -84,7 +87,7 @@ __device__ __forceinline__ void row_store(void *p, int bf16, int64_t row, int d,
             float e[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) e[j] = v[q * V + j];
-            if (i < d) store_values<V>((E *)p, row + i, e);
+            if (i < d) store_values<V, STREAM>((E *)p, row + i, e);
         }
     }
 }
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a) {
             x[j] = fmaf(c, n, x[j]);
         }
     }
-    if (a.r) row_store<X, V, VALS, G>(a.r, a.x_bf16, row, d, lane, x);
+    if (a.r) row_store<X, V, VALS, G, true>(a.r, a.x_bf16, row, d, lane, x);
     if (!pre) return;
     float ss = 0.f;
 #pragma unroll
@@ -187,7 +190,7 @@ __global__ __launch_bounds__(256) void block_norm_kernel(NormArgs a) {
         x[j] *= rr;
         if (a.g_pre) x[j] *= gp[j];
     }
-    row_store<U, V, VALS, G>(a.u, a.u_bf16, row, d, lane, x);
+    row_store<U, V, VALS, G, true>(a.u, a.u_bf16, row, d, lane, x);
 }
 
 // 256 / G rows at a time per block; the waves of a G = 64 block keep partial

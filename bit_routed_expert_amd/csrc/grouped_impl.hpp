@@ -94,7 +94,6 @@ template <int R, int ACROSS, int NT> struct Operand {
 
 // The 8 values a lane feeds to one 32x32x16 product: tile rows r0 + lane%32,
 // contraction 16 kk + 8 (lane/32) .. +8 of the staged step.
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 template <int R, int ACROSS>
 __device__ __forceinline__ bf16x8_t read_frag(const uint8_t *__restrict__ t, int r0, int kk) {

@@ -21,37 +21,49 @@ template <typename E, int V> struct Raw;
 template <int V> struct Raw<float, V> { float w[V]; };
 template <int V> struct Raw<uint16_t, V> { uint32_t w[V >= 2 ? V / 2 : 1]; };
 
-template <int V> __device__ __forceinline__ void load_raw(const uint16_t *p, int64_t i, Raw<uint16_t, V> &r) {
+// Vector types of whole accesses, with the streaming hint (STREAM: what is
+// read or written once and not soon again stays out of the caches' way).
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+template <bool STREAM, typename T> __device__ __forceinline__ T get(const T *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    return *p;
+}
+template <bool STREAM, typename T> __device__ __forceinline__ void put(T *p, T v) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
+template <int V, bool STREAM = false>
+__device__ __forceinline__ void load_raw(const uint16_t *p, int64_t i, Raw<uint16_t, V> &r) {
     if constexpr (V == 8) {
-        const uint4 q = *(const uint4 *)(p + i);
-        r.w[0] = q.x;
-        r.w[1] = q.y;
-        r.w[2] = q.z;
-        r.w[3] = q.w;
+        const u32x4_t q = get<STREAM>((const u32x4_t *)(p + i));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.w[j] = q[j];
     } else if constexpr (V == 4) {
-        const uint2 q = *(const uint2 *)(p + i);
-        r.w[0] = q.x;
-        r.w[1] = q.y;
+        const u32x2_t q = get<STREAM>((const u32x2_t *)(p + i));
+        r.w[0] = q[0];
+        r.w[1] = q[1];
     } else if constexpr (V == 2) {
-        r.w[0] = *(const uint32_t *)(p + i);
+        r.w[0] = get<STREAM>((const uint32_t *)(p + i));
     } else {
         r.w[0] = p[i];
     }
 }
-template <int V> __device__ __forceinline__ void load_raw(const float *p, int64_t i, Raw<float, V> &r) {
+template <int V, bool STREAM = false>
+__device__ __forceinline__ void load_raw(const float *p, int64_t i, Raw<float, V> &r) {
     if constexpr (V >= 4) {
 #pragma unroll
         for (int j = 0; j < V; j += 4) {
-            const float4 q = *(const float4 *)(p + i + j);
-            r.w[j] = q.x;
-            r.w[j + 1] = q.y;
-            r.w[j + 2] = q.z;
-            r.w[j + 3] = q.w;
+            const f32x4_t q = get<STREAM>((const f32x4_t *)(p + i + j));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) r.w[j + c] = q[c];
         }
     } else if constexpr (V == 2) {
-        const float2 q = *(const float2 *)(p + i);
-        r.w[0] = q.x;
-        r.w[1] = q.y;
+        const f32x2_t q = get<STREAM>((const f32x2_t *)(p + i));
+        r.w[0] = q[0];
+        r.w[1] = q[1];
     } else {
         r.w[0] = p[i];
     }
@@ -69,29 +81,30 @@ template <int V> __device__ __forceinline__ float value(const Raw<uint16_t, V> &
 
 // Two values rounded to bf16 in one word (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    typedef float f32x2_t __attribute__((ext_vector_type(2)));
     typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
-template <int V> __device__ __forceinline__ void store_values(uint16_t *p, int64_t i, const float (&v)[V]) {
+template <int V, bool STREAM = false>
+__device__ __forceinline__ void store_values(uint16_t *p, int64_t i, const float (&v)[V]) {
     if constexpr (V == 8) {
-        *(uint4 *)(p + i) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                                       bf16_pair(v[6], v[7]));
+        put<STREAM>((u32x4_t *)(p + i), u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                                                bf16_pair(v[6], v[7])});
     } else if constexpr (V == 4) {
-        *(uint2 *)(p + i) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+        put<STREAM>((u32x2_t *)(p + i), u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
     } else if constexpr (V == 2) {
-        *(uint32_t *)(p + i) = bf16_pair(v[0], v[1]);
+        put<STREAM>((uint32_t *)(p + i), bf16_pair(v[0], v[1]));
     } else {
         p[i] = f2bf(v[0]);
     }
 }
-template <int V> __device__ __forceinline__ void store_values(float *p, int64_t i, const float (&v)[V]) {
+template <int V, bool STREAM = false>
+__device__ __forceinline__ void store_values(float *p, int64_t i, const float (&v)[V]) {
     if constexpr (V >= 4) {
 #pragma unroll
-        for (int j = 0; j < V; j += 4) *(float4 *)(p + i + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        for (int j = 0; j < V; j += 4) put<STREAM>((f32x4_t *)(p + i + j), f32x4_t{v[j], v[j + 1], v[j + 2], v[j + 3]});
     } else if constexpr (V == 2) {
-        *(float2 *)(p + i) = make_float2(v[0], v[1]);
+        put<STREAM>((f32x2_t *)(p + i), f32x2_t{v[0], v[1]});
     } else {
         p[i] = v[0];
     }

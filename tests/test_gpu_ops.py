@@ -70,7 +70,8 @@ def run_sort(idx, T, k, E):
 @pytest.mark.parametrize("T,k,E,drop", [
     (0, 4, 8, 0.0), (1, 1, 1, 0.0), (1, 1, 1, 1.0), (5, 10, 512, 0.0), (7, 3, 5, 0.4), (64, 1, 1024, 0.0),
     (100, 32, 3, 0.2), (128, 32, 1024, 0.1), (4095, 1, 63, 0.1), (1025, 4, 64, 0.0), (1366, 3, 1, 0.5),
-    (4096, 10, 512, 0.0), (3001, 7, 1024, 0.9), (40000, 7, 33, 0.1), (2000, 3, 17, 1.0)])
+    (4096, 10, 512, 0.0), (3001, 7, 1024, 0.9), (21845, 3, 512, 0.0), (16384, 4, 1024, 0.1), (13107, 5, 2, 0.0),
+    (65535, 1, 1, 0.0), (40000, 7, 33, 0.1), (2000, 3, 17, 1.0)])
 def test_sort(T, k, E, drop):
     print(f"case sort T={T} k={k} E={E} drop={drop}", flush=True)
     idx = draw_idx(T, k, E, drop, seed=T + k + E)

@@ -21,10 +21,10 @@ def lib():
 
 def test_sort_refusals():
     f, ws = lib().strata_moe_sort, lib().strata_moe_sort_workspace_bytes
-    need = ws(5000, 10, 512)
-    assert need >= 4 * 512 * 49 and ws(5, 10, 512) > 0 and ws(0, 1, 1) > 0
+    need = ws(50000, 10, 512)
+    assert need >= 4 * 512 * 200 and ws(5, 10, 512) > 0 and ws(0, 1, 1) > 0
 
-    def call(idx=P, T=5000, k=10, E=512, w=P, wb=need):
+    def call(idx=P, T=50000, k=10, E=512, w=P, wb=need):
         return f(idx, T, k, E, P, P, P, P, w, wb, None)
     assert call(idx=None) == EINVAL and call(w=None) == EINVAL and call(w=P + 8) == EINVAL
     for bad in (dict(T=-1), dict(k=0), dict(k=33), dict(E=0), dict(E=1025)):
