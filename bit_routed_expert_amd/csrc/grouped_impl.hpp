@@ -77,8 +77,10 @@ template <int R, int ACROSS, int NT> struct Operand {
         const uint16_t *p = ACROSS ? base + (int64_t)s * GP_C * ld : base + (int64_t)s * GP_C;
         const uint32_t bytes = ACROSS ? (uint32_t)min(left, GP_C) * (uint32_t)ld * 2u
                                       : left ? ((uint32_t)(count - 1) * (uint32_t)ld + (uint32_t)left) * 2u : 0u;
-        const __amdgpu_buffer_rsrc_t r =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p), 0, (int)bytes, 0x00020000);
+        // the size in a scalar register whatever unit computed it: a resource in vector registers makes
+        // every load a loop over the lanes
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t *>(p), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             uint32_t o = off[i];
@@ -169,13 +171,12 @@ __device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *__re
                                          int steps, int m0, int n0, bool active, f32x16_t (&acc)[MT][NT2]) {
     constexpr int L = OA::LOADS + OB::LOADS;   // a wave's loads per step
     if (steps == 0) return;
-#define STEP(S, AR, BR, AW, BW)                                                                     \
+#define STEP(S, MORE, AR, BR, AW, BW)                                                                  \
     {                                                                                               \
         wait_and_meet<(ST - 2) * L>();                                                              \
         step_product<BM, BN, MT, NT2, TA, TB>(AR, BR, m0, n0, active, acc, [&](int kk) {            \
-            const bool more = ST > 2 || (S) + 1 < steps;                                            \
-            if (kk == 0 && more) A.load((S) + ST - 1, AW);                                          \
-            if (kk == 1 && more) B.load((S) + ST - 1, BW);                                          \
+            if (kk == 0 && (MORE)) A.load((S) + ST - 1, AW);                                        \
+            if (kk == 1 && (MORE)) B.load((S) + ST - 1, BW);                                        \
         });                                                                                         \
     }
     A.load(0, a0);
@@ -188,27 +189,35 @@ __device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *__re
         A.load(2, a2);
         B.load(2, b2);
     }
+    const auto none = [](int) {};
     int s = 0;
+    if constexpr (ST == 2) {
+        for (; s + 2 <= steps; s += 2) {
+            STEP(s, true, a0, b0, a1, b1)
+            STEP(s + 1, s + 2 < steps, a1, b1, a0, b0)
+        }
+        if (s < steps) {
+            wait_and_meet<0>();
+            step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, none);
+        }
+        return;
+    }
     for (; s + ST <= steps; s += ST) {
-        if constexpr (ST == 2) {
-            STEP(s, a0, b0, a1, b1)
-            STEP(s + 1, a1, b1, a0, b0)
-        } else if constexpr (ST == 3) {
-            STEP(s, a0, b0, a2, b2)
-            STEP(s + 1, a1, b1, a0, b0)
-            STEP(s + 2, a2, b2, a1, b1)
+        if constexpr (ST == 3) {
+            STEP(s, true, a0, b0, a2, b2)
+            STEP(s + 1, true, a1, b1, a0, b0)
+            STEP(s + 2, true, a2, b2, a1, b1)
         } else {
-            STEP(s, a0, b0, a3, b3)
-            STEP(s + 1, a1, b1, a0, b0)
-            STEP(s + 2, a2, b2, a1, b1)
-            STEP(s + 3, a3, b3, a2, b2)
+            STEP(s, true, a0, b0, a3, b3)
+            STEP(s + 1, true, a1, b1, a0, b0)
+            STEP(s + 2, true, a2, b2, a1, b1)
+            STEP(s + 3, true, a3, b3, a2, b2)
         }
     }
 #undef STEP
-    const auto none = [](int) {};
     wait_and_meet<0>();   // the last steps, and no load outlives the loop
     if (s < steps) step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, none);
-    if (ST > 2 && s + 1 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, active, acc, none);
+    if (s + 1 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, active, acc, none);
     if (ST > 3 && s + 2 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a2, b2, m0, n0, active, acc, none);
 }
 
@@ -400,7 +409,9 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a)
     } else if (!group_tile(per_e, a.E, e, t)) {
         return;
     }
-    const int lo = min(max(a.offsets[e], 0), a.rows), hi = min(max(a.offsets[e + 1], 0), a.rows);
+    e = __builtin_amdgcn_readfirstlane(e);
+    const int lo = __builtin_amdgcn_readfirstlane(min(max(a.offsets[e], 0), a.rows));
+    const int hi = __builtin_amdgcn_readfirstlane(min(max(a.offsets[e + 1], 0), a.rows));
     const int cd = max(hi - lo, 0), r0 = (t / nk) * BM, k0 = (t % nk) * BN;
     OA A;
     OB B;
