@@ -243,14 +243,18 @@ template <int TB> strata_status grouped_rows(GroupArgs &a, hipStream_t s) {
 
 // The gradient's tiles: 256 square where there are enough for the 256 CUs,
 // else 128 square.
+int64_t weight_blocks(const GroupArgs &a, int t) {
+    const int64_t nn = (a.N + t - 1) / t, nk = (a.K + t - 1) / t;
+    if (a.E <= GP_RANKED) return ((int64_t)a.E * 4 + 7) / 8 * 8 * ((nn + 1) / 2) * ((nk + 1) / 2);
+    return (a.E * nn * nk + 7) / 8 * 8;
+}
+
 strata_status grouped_weights(const GroupArgs &a, hipStream_t s) {
     const int64_t large = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-    if (large >= 192 && a.N > 128 && a.K > 128) {
-        STRATA_LAUNCH((grouped_wgrad_kernel<256, 256, 2, 4, 2>), dim3((unsigned)((large + 7) / 8 * 8)), dim3(512), 0, s, a);
-    } else {
-        const int64_t blocks = ((int64_t)a.E * ((a.N + 127) / 128) * ((a.K + 127) / 128) + 7) / 8 * 8;
-        STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-    }
+    if (large >= 192 && a.N > 128 && a.K > 128)
+        STRATA_LAUNCH((grouped_wgrad_kernel<256, 256, 2, 4, 2>), dim3((unsigned)weight_blocks(a, 256)), dim3(512), 0, s, a);
+    else
+        STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 2>), dim3((unsigned)weight_blocks(a, 128)), dim3(256), 0, s, a);
     return hip_status(hipGetLastError());
 }
 
