@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void grouped_few_kernel(GroupArgs a, int slabs
     const int e = found[0] + found[1] + found[2] + found[3];
     if (e >= a.E) return;   // behind the last expert
     const int lo = max(a.offsets[e], 0), hi = min(a.offsets[e + 1], a.rows);
-    if (row < lo || ((row - lo) & (GV_R - 1))) return;   // its group's first row has it
+    if (row < lo || row >= hi || ((row - lo) & (GV_R - 1))) return;   // its group's first row has it
     const int n = min(hi - row, GV_R);
     const int K = a.K;
     for (int i = th; i < n * K / 8; i += 256)
@@ -182,6 +182,8 @@ strata_status check_grouped(int32_t rows, int32_t E, int32_t N, int32_t K) {
     if (rows < 0) return STRATA_EINVAL;
     if (E < 1 || E > GP_E || N < 8 || K < 8 || N > 65536 || K > 65536 || N % 8 || K % 8 || (int64_t)N * K > (1 << 29))
         return STRATA_EUNSUPPORTED;
+    // grids of fewer than 2^32 threads
+    if (rows > (1 << 22) || (int64_t)E * N * K > ((int64_t)1 << 37)) return STRATA_EUNSUPPORTED;
     return STRATA_OK;
 }
 

@@ -8,6 +8,7 @@ namespace strata {
 
 // Most tokens of a call: one 256-thread block each stays inside a grid's 2^32 threads.
 constexpr int32_t MAX_ROWS = 1 << 23;
+constexpr int32_t MAX_COLS = 1 << 24;   // longest row of dispatch and combine
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool bad_dtype(int32_t t) { return t != STRATA_X_BF16 && t != STRATA_X_F32; }

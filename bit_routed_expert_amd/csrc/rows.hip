@@ -89,17 +89,20 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const Y *__restrict__
     const float *wt = w ? w + (int64_t)t * k : nullptr;
     Picks<G> pk;
     pk.read(pt, wt, 0, k, rows);
-    for (int i = lane * V; i < d; i += G * V) {
+    // the trip count is the group's, so that a second batch of picks is read by whole waves
+    for (int i0 = 0; i0 < d; i0 += G * V) {
+        const int i = i0 + lane * V;
+        const bool in = i < d;
         Raw<O, V> b;
         zero_raw(b);
-        if (base) load_raw<V, true>(base, (int64_t)t * d + i, b);
+        if (base && in) load_raw<V, true>(base, (int64_t)t * d + i, b);
         float s[V];
         for (int r0 = 0; r0 < k; r0 += PB) {
             if (k > PB) pk.read(pt, wt, r0, k, rows);
             Raw<Y, V> v[PB];
 #pragma unroll
             for (int r = 0; r < PB; ++r)
-                if (pk.pos[r] >= 0) load_raw<V, true>(ys, (int64_t)pk.pos[r] * d + i, v[r]);
+                if (pk.pos[r] >= 0 && in) load_raw<V, true>(ys, (int64_t)pk.pos[r] * d + i, v[r]);
             if (r0 == 0) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) s[j] = value<V>(b, j);
@@ -112,7 +115,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const Y *__restrict__
                 }
             }
         }
-        store_values<V, true>(out, (int64_t)t * d + i, s);
+        if (in) store_values<V, true>(out, (int64_t)t * d + i, s);
     }
 }
 
@@ -221,7 +224,7 @@ strata_status check_rows(const void *a, const void *b, const int32_t *pos, int32
     if (T == 0) return STRATA_OK;
     if (!pos || bad_rows(b)) return STRATA_EINVAL;
     if (rows > 0 ? bad_rows(a) : (a && !aligned16(a))) return STRATA_EINVAL;
-    if (T > MAX_ROWS || (int64_t)T * k > INT32_MAX) return STRATA_EUNSUPPORTED;
+    if (T > MAX_ROWS || (int64_t)T * k > INT32_MAX || d > MAX_COLS) return STRATA_EUNSUPPORTED;
     return STRATA_OK;
 }
 

@@ -59,7 +59,7 @@ strata_status strata_moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t 
  *   pos [dev] [T*k] int32; entries outside 0..rows-1 copy nothing.
  * Rows of xs without a pick are left as they were.  T = 0: no-op.  EINVAL: a
  * null or misaligned pointer, T, rows < 0, d < 1, k outside 1..32, a bad
- * dtype; EUNSUPPORTED: T > 2^23 or T*k > 2^31 - 1; EHIP. */
+ * dtype; EUNSUPPORTED: T > 2^23, d > 2^24 or T*k > 2^31 - 1; EHIP. */
 strata_status strata_moe_dispatch(const void *x, strata_xdtype xdtype, int32_t T, int32_t k, int32_t d,
                                   const int32_t *pos, void *xs, int32_t rows, void *stream);
 
@@ -100,7 +100,7 @@ strata_status strata_moe_combine_backward(const void *dout, strata_xdtype odtype
  * outside the buffers is touched.  Matrix-core products of bf16 operands,
  * summed in fp32.
  * Limits: N % 8 == 0, K % 8 == 0, 8 <= N, K <= 65536, N*K <= 2^29, 1 <= E <=
- * 1024, else EUNSUPPORTED.  EINVAL: a null or misaligned pointer, rows < 0, a
+ * 1024, E*N*K <= 2^37, rows <= 2^22, else EUNSUPPORTED.  EINVAL: a null or misaligned pointer, rows < 0, a
  * bad dtype; EWORKSPACE; EHIP.  Rows behind the last expert's are not read
  * and their outputs are left as they were.
  */

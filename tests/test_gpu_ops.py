@@ -109,7 +109,8 @@ def test_sort_outputs_may_be_left_out():
 # ---------------------------------------------------- dispatch and combine
 
 ROWS = [(1, 1, 1, 1, 0.0), (3, 2, 2, 3, 0.5), (5, 10, 512, 2048, 0.0), (37, 4, 8, 130, 0.3), (19, 32, 40, 264, 0.1),
-        (50, 3, 6, 1000, 0.2), (9, 17, 20, 2052, 0.2), (21, 5, 4, 5001, 0.1), (6, 3, 4, 64, 1.0), (300, 8, 16, 24, 0.1)]
+        (50, 3, 6, 1000, 0.2), (9, 17, 20, 2052, 0.2), (21, 5, 4, 5001, 0.1), (6, 3, 4, 64, 1.0), (300, 8, 16, 24, 0.1),
+        (7, 32, 9, 2056, 0.1), (5, 20, 40, 1028, 0.0)]
 
 
 def positions(T, k, E, drop, seed):
@@ -281,10 +282,15 @@ def test_grouped_without_rows():
 
 
 @pytest.mark.parametrize("off", [[5, 2, 9, 9], [-7, 4, 99, 3], [0, 0, 0, 0], [30, 30, 30, 30], [12, 0, 12, 0]])
-def test_grouped_offsets_that_do_not_ascend_stay_inside(off):
-    """Which rows such offsets mean is not specified; nothing outside the buffers is written."""
-    E, N, K, rows = 3, 72, 64, 20
+@pytest.mark.parametrize("pad", [0, 100])
+def test_grouped_offsets_that_do_not_ascend_stay_inside(off, pad):
+    """Which rows such offsets mean is not specified; nothing outside the
+    buffers is written.  With 100 experts more the product takes its path for
+    few rows."""
+    N, K, rows = 72, 64, 20
     _, _, x, dy, W = group_inputs([20], N, K, 0)
+    off = off[:2] + [off[1]] * (pad // 2) + off[2:] + [off[3]] * (pad // 2)
+    E = len(off) - 1
     W = W.repeat(E, 1, 1)
     nb = brx.grouped_workspace_bytes(rows, E, N, K)
     wsb = torch.full((nb + GUARD,), 0x5A, dtype=torch.uint8, device="cuda")
@@ -296,6 +302,94 @@ def test_grouped_offsets_that_do_not_ascend_stay_inside(off):
     for q in (y, dx, dW):
         q.guarded()
     assert bool((wsb[nb:] == 0x5A).all())
+
+
+def test_grouped_experts_do_not_touch_each_other():
+    """NaN in one expert's rows or weights stays with it, in every tile size."""
+    for ns in ([5, 7, 40, 9], [130, 70, 300, 90], [600, 500, 700, 800], [1, 2, 0, 1] + [0] * 30):
+        N, K, E, bad = 264, 136, len(ns), 1
+        rows, off, x, dy, W = group_inputs(ns, N, K, 0)
+        a, b = int(off[bad]), int(off[bad + 1])
+        x[a:b], dy[a:b], W[bad] = float("nan"), float("inf"), float("nan")
+        nb = brx.grouped_workspace_bytes(rows, E, N, K)
+        ws = ws_of(nb)
+        y, dx, dW = Out(rows, N, dtype=F32), Out(rows, K, dtype=F32), Out(E, N, K, dtype=F32)
+        xc, yc, Wc, oc = x.cuda(), dy.cuda(), W.cuda(), off.cuda()
+        brx.grouped_product(xc, Wc, oc, rows, E, N, K, y.t, 1, ws, nb)
+        brx.grouped_dgrad(yc, Wc, oc, rows, E, N, K, dx.t, 1, ws, nb)
+        brx.grouped_wgrad(yc, xc, oc, rows, E, N, K, dW.t, 1, ws, nb)
+        others = torch.ones(rows, dtype=torch.bool)
+        others[a:b] = False
+        for q in (y, dx):
+            got = q.guarded().cpu()
+            assert bool(torch.isfinite(got[others]).all()) and not bool(torch.isfinite(got[a:b]).any())
+        got = dW.guarded().cpu()
+        assert bool(torch.isfinite(got[[e for e in range(E) if e != bad]]).all())
+
+
+# ------------------------------------------------------ past 32-bit offsets
+
+def test_rows_past_32_bit_offsets():
+    """Slots, experts' rows, weights and norm rows whose element offsets pass 2^31."""
+    d, rows = 2048, 1_100_000
+    assert rows * d > 2**31
+    print("case dispatch and combine past 2^31 elements", flush=True)
+    T, k = 3, 2
+    pos = torch.tensor([rows - 1, 0, rows - 2, 7, 2**20 + 5, rows - 3], dtype=torch.int32, device="cuda")
+    x = rand(T, d, seed=1, dtype=BF).cuda()
+    xs = torch.zeros(rows, d, dtype=BF, device="cuda")
+    brx.dispatch(x, 0, T, k, d, pos, xs, rows)
+    assert torch.equal(xs[pos.long()], x.repeat_interleave(k, 0)) and int((xs != 0).any(1).sum()) == T * k
+    out = torch.empty(T, d, dtype=F32, device="cuda")
+    brx.combine(xs, 0, rows, pos, None, T, k, d, out, 1)
+    assert torch.equal(out, 2 * x.float())
+    print("case products past 2^31 elements", flush=True)
+    N = 64
+    W = rand(2, N, d, seed=2, dtype=BF, scale=d ** -0.5).cuda()
+    off = torch.tensor([0, rows - 3, rows], dtype=torch.int32, device="cuda")
+    xs[-3:] = rand(3, d, seed=3, dtype=BF).cuda()
+    nb = brx.grouped_workspace_bytes(rows, 2, N, d)
+    ws, y = ws_of(nb), torch.empty(rows, N, dtype=F32, device="cuda")
+    brx.grouped_product(xs, W, off, rows, 2, N, d, y, 1, ws, nb)
+    tail, Wd = xs[-3:].double().cpu(), W.double().cpu()
+    R.check(y[-3:], tail @ Wd[1].t(), 2 * d * U * (tail.abs() @ Wd[1].abs().t()), "y")
+    dy = torch.zeros(rows, N, dtype=BF, device="cuda")
+    dy[-3:] = rand(3, N, seed=4, dtype=BF).cuda()
+    dx = torch.empty(rows, d, dtype=BF, device="cuda")
+    brx.grouped_dgrad(dy, W, off, rows, 2, N, d, dx, 0, ws, nb)
+    gt = dy[-3:].double().cpu()
+    R.check(dx[-3:], gt @ Wd[1], 2 * N * U * (gt.abs() @ Wd[1].abs()), "dx")
+    dW = torch.empty(2, N, d, dtype=F32, device="cuda")
+    brx.grouped_wgrad(dy, xs, off, rows, 2, N, d, dW, 1, ws, nb)
+    R.check(dW[1], gt.t() @ tail, 6 * U * (gt.abs().t() @ tail.abs()), "dW")
+    assert bool((dW[0] == 0).all())   # its dy are zeros
+    del dx, dy, y
+    print("case block norm past 2^31 elements", flush=True)
+    u = torch.empty(rows, d, dtype=BF, device="cuda")
+    xs[1] = 1.5
+    brx.block_norm(brx.block_norm_args(rows, d, 0, 0, 0, brx.PRE_NORM), xs, None, u=u)
+    want = R.norm_rows(xs[-3:].double().cpu(), None, f32(1e-6))
+    R.check(u[-3:], want, (d + 8) * U * want.abs(), "u")
+    del xs, u
+    print("case weights past 2^31 elements", flush=True)
+    E, N, K = 700, 1536, 2048
+    W = torch.zeros(E, N, K, dtype=BF, device="cuda")
+    W[-1] = rand(N, K, seed=5, dtype=BF, scale=K ** -0.5).cuda()
+    for n in (2, 800):   # the path for few rows, and the tiles
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[-1] = n
+        x = rand(n, K, seed=6, dtype=BF).cuda()
+        y = torch.empty(n, N, dtype=F32, device="cuda")
+        nb = brx.grouped_workspace_bytes(n, E, N, K)
+        brx.grouped_product(x, W, off, n, E, N, K, y, 1, ws_of(nb), nb)
+        xd, Wd = x.double().cpu(), W[-1].double().cpu()
+        R.check(y, xd @ Wd.t(), 2 * K * U * (xd.abs() @ Wd.abs().t()), "y")
+    dW = torch.empty(E, N, K, dtype=BF, device="cuda")
+    dy = rand(n, N, seed=7, dtype=BF).cuda()
+    brx.grouped_wgrad(dy, x, off, n, E, N, K, dW, 0, ws_of(nb), nb)
+    gd = dy.double().cpu()
+    R.check(dW[-1], gd.t() @ xd, 2 * n * U * (gd.abs().t() @ xd.abs()), "dW")
+    assert not bool(dW[:-1].any())
 
 
 # ------------------------------------------------------------- block norms
@@ -460,6 +554,28 @@ def test_block_norm_in_place_and_outputs_apart():
     brx.block_norm_backward(a, torch.zeros_like(dr), du, r, g["y"], **ins, rstd_y=sy, rstd_r=sr, dx=zero)
     brx.block_norm_backward(a, None, du, r, g["y"], **ins, rstd_y=sy, rstd_r=sr, dx=none)   # no gradient of r itself
     assert torch.equal(zero, none)
+
+
+def test_block_norm_gains_of_one():
+    """A null gain is a gain of 1, forward and backward."""
+    for d in (264, 2048, 3001):
+        T = 9
+        a, t = norm_case(T, d, F32, F32, F32, True, True, "token", False)
+        g = {n: cu(v) for n, v in t.items()}
+        one = torch.ones(d, device="cuda")
+        outs = []
+        for gp, gq in ((None, None), (one, one)):
+            r, u, sy, sr = (torch.empty(T, d, device="cuda"), torch.empty(T, d, device="cuda"),
+                            torch.empty(T, device="cuda"), torch.empty(T, device="cuda"))
+            brx.block_norm(a, g["x"], g["y"], gate=g["gate"], g_post=gp, g_pre=gq, r=r, u=u, rstd_y=sy, rstd_r=sr)
+            o = [torch.empty(T, d, device="cuda"), torch.empty(T, d, device="cuda"), torch.empty(T, device="cuda"),
+                 torch.empty(d, device="cuda"), torch.empty(d, device="cuda")]
+            nb = brx.block_norm_backward_workspace_bytes(a)
+            brx.block_norm_backward(a, g["x"], g["y"], r, g["y"], gate=g["gate"], g_post=gp, g_pre=gq, rstd_y=sy,
+                                    rstd_r=sr, dx=o[0], dy=o[1], dgate=o[2], dg_post=o[3], dg_pre=o[4], ws=ws_of(nb),
+                                    ws_bytes=nb)
+            outs.append([r, u, sy, sr] + o)
+        assert same(*outs)
 
 
 def test_block_norm_without_rows():

@@ -47,7 +47,7 @@ def test_dispatch_and_combine_refusals():
     for bad in (dict(a=None), dict(b=None), dict(pos=None), dict(a=P + 2), dict(b=P + 4), dict(rows=-1), dict(T=-1),
                 dict(k=0), dict(k=33), dict(dd=0), dict(xt=2)):
         assert calls(**bad) == [EINVAL] * 4, bad
-    assert calls(T=2**23 + 1) == [EUNSUP] * 4
+    assert calls(T=2**23 + 1) == [EUNSUP] * 4 and calls(dd=2**24 + 1) == [EUNSUP] * 4
     assert calls(T=0, a=None, b=None, pos=None) == [OK] * 4
     assert cb(P, 0, P, 0, 20, P, None, 5, 4, 64, P, P, P, None) == EINVAL          # no weights
     assert cb(P, 0, P, 0, 20, P, P, 5, 4, 64, P + 8, P, P, None) == EINVAL
@@ -66,10 +66,11 @@ def test_grouped_refusals(name):
     for bad in (dict(a=None), dict(b=None), dict(off=None), dict(c=None), dict(w=None), dict(a=P + 8),
                 dict(b=P + 2), dict(c=P + 4), dict(w=P + 8), dict(t=3), dict(rows=-1)):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(E=0), dict(E=1025), dict(N=60), dict(K=4), dict(N=0), dict(K=65544), dict(N=65536, K=16384)):
+    for bad in (dict(E=0), dict(E=1025), dict(N=60), dict(K=4), dict(N=0), dict(K=65544), dict(N=65536, K=16384),
+                dict(E=1024, N=32768, K=8192), dict(rows=2**22 + 1)):
         assert call(**bad, wb=1 << 40) == EUNSUP, bad
-        a = dict(E=8, N=64, K=128) | bad
-        assert ws(100, a["E"], a["N"], a["K"]) == 0
+        a = dict(rows=100, E=8, N=64, K=128) | bad
+        assert ws(a["rows"], a["E"], a["N"], a["K"]) == 0
     assert call(wb=need - 1) == EWS
     if name != "wgrad":
         assert call(rows=0, a=None, b=None, off=None, c=None, w=None) == OK
