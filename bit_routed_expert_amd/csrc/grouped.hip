@@ -243,20 +243,28 @@ template <int TB> strata_status grouped_rows(GroupArgs &a, hipStream_t s) {
     return launch_rows<256, 256, 2, 4, 2, TB>(a, s);
 }
 
-// The gradient's tiles: 256 square where there are enough for the 256 CUs,
-// else 128 square.
 int64_t weight_blocks(const GroupArgs &a, int t) {
     const int64_t nn = (a.N + t - 1) / t, nk = (a.K + t - 1) / t;
     if (a.E <= GP_RANKED) return ((int64_t)a.E * 4 + 7) / 8 * 8 * ((nn + 1) / 2) * ((nk + 1) / 2);
     return (a.E * nn * nk + 7) / 8 * 8;
 }
 
+// Tiles of the weights' gradient.  256 square where there are many (512
+// experts, 16 to 256 rows each, 1536 x 2048 bf16: 0.74 to 1.37 ms against 0.81
+// to 1.63 with 128 square) or some with long contractions (16 experts of 1024
+// rows: 99 against 109 us; of 256 rows: 50 against 46).  Else 128 square, two
+// blocks to a CU (4 experts of 1024 rows, 2048 x 768: 20 us, 64 square 27),
+// and 64 square where even those are fewer than the CUs (4 experts of 4096
+// rows, 128 x 128: 21 against 31 us).
 strata_status grouped_weights(const GroupArgs &a, hipStream_t s) {
     const int64_t large = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-    if (large >= 192 && a.N > 128 && a.K > 128)
+    const int64_t small = (int64_t)a.E * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+    if (large >= 1024 || (large >= 512 && a.rows >= 512 * (int64_t)a.E))
         STRATA_LAUNCH((grouped_wgrad_kernel<256, 256, 2, 4, 2>), dim3((unsigned)weight_blocks(a, 256)), dim3(512), 0, s, a);
-    else
+    else if (small >= 256)
         STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 2>), dim3((unsigned)weight_blocks(a, 128)), dim3(256), 0, s, a);
+    else
+        STRATA_LAUNCH((grouped_wgrad_kernel<64, 64, 1, 2, 2>), dim3((unsigned)weight_blocks(a, 64)), dim3(128), 0, s, a);
     return hip_status(hipGetLastError());
 }
 

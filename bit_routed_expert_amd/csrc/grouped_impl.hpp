@@ -42,6 +42,10 @@ struct GroupArgs {
     int rows, E, N, K, tile_rows, c_bf16;
 };
 
+// Permutation of the 16-byte chunks of staged row c (R values, a power of two
+// of at least 64), across: the 64-byte pieces by the low bits of c.
+template <int R> __device__ __forceinline__ int across_swz(int c) { return ((c & 3) << 2) & (R / 8 - 1); }
+
 // One operand: R rows of it in the tile (m or n), NT threads stage it.
 template <int R, int ACROSS, int NT> struct Operand {
     static constexpr int BYTES = R * GP_C * 2, LOADS = R * 8 / NT;
@@ -64,7 +68,7 @@ template <int R, int ACROSS, int NT> struct Operand {
             const int q = i * NT + th;
             if (ACROSS) {
                 const int c = q / (R / 8), at = q % (R / 8);
-                off[i] = (uint32_t)c * (uint32_t)ld * 2u + (uint32_t)(r0 + 8 * (at ^ ((c & 3) << 2))) * 2u;
+                off[i] = (uint32_t)c * (uint32_t)ld * 2u + (uint32_t)(r0 + 8 * (at ^ across_swz<R>(c))) * 2u;
             } else {
                 const int r = q >> 3, at = q & 7;
                 off[i] = (uint32_t)r * (uint32_t)ld * 2u + (uint32_t)(8 * (at ^ ((r ^ (r >> 3)) & 7))) * 2u;
@@ -108,7 +112,7 @@ __device__ __forceinline__ bf16x8_t read_frag(const uint8_t *__restrict__ t, int
         const int i = lane & 15, g = lane >> 4;
         const int c = 16 * kk + 8 * (g >> 1) + (i >> 2);   // second read: c + 4, the same low bits
         const int chunk = (r0 >> 3) + 2 * (g & 1) + ((i >> 1) & 1);
-        const uint8_t *p = t + c * (R * 2) + 16 * (chunk ^ ((c & 3) << 2)) + 8 * (i & 1);
+        const uint8_t *p = t + c * (R * 2) + 16 * (chunk ^ across_swz<R>(c)) + 8 * (i & 1);
         typedef __attribute__((address_space(3))) s16x4_t lds4;
         const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
         const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 4 * R * 2));

@@ -227,7 +227,10 @@ GROUPS = [  # rows per expert, N, K, rows behind the last
     ([16, 17, 31, 32, 48], 2048, 768, 0), ([700, 3], 200, 24, 0), ([90, 70, 0, 110], 512, 1032, 2),
     # few rows against the experts: one to nine rows of the experts that have any
     ([0, 1, 2, 0, 3, 4, 5] + [0] * 62 + [1], 200, 1032, 1), ([0] * 40 + [9], 72, 24, 0), ([0, 2] + [0] * 6, 1536, 2048, 0),
-    ([1] + [0] * 19 + [3], 88, 8192, 1), ([1] + [0] * 3, 8, 8, 0), ([0] * 9, 16, 16, 2)]
+    ([1] + [0] * 19 + [3], 88, 8192, 1), ([1] + [0] * 3, 8, 8, 0), ([0] * 9, 16, 16, 2),
+    # the largest tiles and grids whose tiles an earlier launch lists; more than 64 experts
+    ([5000, 131, 7769], 1000, 904, 2), ([39000, 900], 1000, 136, 0), ([20, 0, 41, 19] * 32 + [300], 520, 1032, 1),
+    ([3, 1, 5] * 67, 520, 264, 0), ([(7 * i) % 90 for i in range(40)], 1288, 1288, 3), ([0] * 30 + [700] * 2, 136, 1000, 0)]
 
 
 def group_inputs(ns, N, K, tail, seed=1):
