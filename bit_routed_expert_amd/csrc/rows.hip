@@ -5,9 +5,8 @@
 // row once.  The work is token-major: a group of G threads takes one token,
 // keeps a V-element piece of its row in registers and meets the k picked
 // rows, so x and dout are read once however many picks a token has and
-// every sum runs over r in order in one thread.  G is the power of two from
-// 16 to 256 that leaves the fewest threads without a piece, V the widest
-// vector up to 16 bytes that divides the row.
+// every sum runs over r in order in one thread.  G is a power of two from 16
+// to 256, V the widest vector up to 16 bytes that divides the row.
 //
 // Rows are read and written with the streaming hint: each once, and a prompt
 // chunk's slots (168 MB) are most of what the caches hold.  4096 tokens of
@@ -66,12 +65,13 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const P *__restrict__ x, 
                                                        P *__restrict__ xs, int T, int k, int nc, int rows) {
     int t, lane;
     if (!row_group<G>(T, t, lane)) return;
-    P v = lane < nc ? x[(int64_t)t * nc + lane] : P{};
+    const int c0 = blockIdx.y * G + lane, step = gridDim.y * G;   // the blocks of a token share its row
+    P v = c0 < nc ? x[(int64_t)t * nc + c0] : P{};
     for (int r0 = 0; r0 < k; r0 += PB) {
         Picks<G> pk;
         pk.read(pos + (int64_t)t * k, nullptr, r0, k, rows);
-        for (int c = lane; c < nc; c += G) {
-            if (c != lane || r0) v = x[(int64_t)t * nc + c];
+        for (int c = c0; c < nc; c += step) {
+            if (c != c0 || r0) v = x[(int64_t)t * nc + c];
 #pragma unroll
             for (int r = 0; r < PB; ++r)
                 if (pk.pos[r] >= 0) put<true>(xs + (int64_t)pk.pos[r] * nc + c, v);
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(const Y *__restrict__
     Picks<G> pk;
     pk.read(pt, wt, 0, k, rows);
     // the trip count is the group's, so that a second batch of picks is read by whole waves
-    for (int i0 = 0; i0 < d; i0 += G * V) {
+    for (int i0 = blockIdx.y * (G * V); i0 < d; i0 += gridDim.y * (G * V)) {
         const int i = i0 + lane * V;
         const bool in = i < d;
         Raw<O, V> b;
@@ -204,18 +204,31 @@ __global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__
 
 namespace {
 
-// Threads per token for nc pieces: fewest idle threads, the larger of equals.
-int row_threads(int64_t nc, int least) {
-    int best = 256;
-    int64_t cost = (nc + 255) / 256 * 256;
-    for (int g = 128; g >= least; g /= 2) {
-        const int64_t c = (nc + g - 1) / g * g;
-        if (c < cost) {
-            cost = c;
-            best = g;
+// Threads per token for nc pieces, and how many blocks share a token's row.
+// Many tokens fill the chip by themselves: the largest group that leaves at
+// most a quarter more threads idle than the best.  Few tokens: a thread per
+// piece as far as a block goes, and the rest of the row to other blocks (7
+// tokens of 1927 values in 121 trips of 16 threads: 72 us, else 4).
+struct RowGroups {
+    int threads, shares;
+};
+constexpr int ROW_BLOCKS = 1024;   // blocks that fill the chip
+RowGroups row_groups(int T, int64_t nc, int least) {
+    int g = least;
+    if (T >= ROW_BLOCKS) {
+        int64_t best = INT64_MAX;
+        for (int q = least; q <= 256; q *= 2) {
+            const int64_t c = (nc + q - 1) / q * q;
+            if (c < best) best = c;
         }
+        for (int q = least; q <= 256; q *= 2)
+            if ((nc + q - 1) / q * q * 4 <= best * 5) g = q;
+    } else {
+        while (g < 256 && g < nc) g *= 2;
     }
-    return best;
+    const int64_t blocks = ((int64_t)T * g + 255) / 256, trips = (nc + g - 1) / g;
+    const int64_t want = (ROW_BLOCKS + blocks - 1) / blocks;
+    return RowGroups{g, (int)(want < trips ? want : trips)};
 }
 
 strata_status check_rows(const void *a, const void *b, const int32_t *pos, int32_t rows, int32_t T, int32_t k,
@@ -228,17 +241,19 @@ strata_status check_rows(const void *a, const void *b, const int32_t *pos, int32
     return STRATA_OK;
 }
 
-dim3 row_grid(int T, int g) { return dim3((unsigned)(((int64_t)T + 256 / g - 1) / (256 / g))); }
+dim3 row_grid(int T, int g, int shares) {
+    return dim3((unsigned)(((int64_t)T + 256 / g - 1) / (256 / g)), (unsigned)shares);
+}
 
 template <typename P>
 void launch_dispatch(const void *x, const int32_t *pos, void *xs, int T, int k, int nc, int rows, hipStream_t s) {
-    const int g = row_threads(nc, 16);
+    const RowGroups q = row_groups(T, nc, 16);
 #define DISPATCH(G)                                                                                                  \
     case G:                                                                                                          \
-        STRATA_LAUNCH((dispatch_kernel<P, G>), row_grid(T, G), dim3(256), 0, s, (const P *)x, pos, (P *)xs, T, k, nc, \
+        STRATA_LAUNCH((dispatch_kernel<P, G>), row_grid(T, G, q.shares), dim3(256), 0, s, (const P *)x, pos, (P *)xs, T, k, nc, \
                       rows);                                                                                         \
         break;
-    switch (g) { DISPATCH(16) DISPATCH(32) DISPATCH(64) DISPATCH(128) DISPATCH(256) }
+    switch (q.threads) { DISPATCH(16) DISPATCH(32) DISPATCH(64) DISPATCH(128) DISPATCH(256) }
 #undef DISPATCH
 }
 
@@ -254,12 +269,13 @@ struct RowCall {
 
 struct Combine {
     template <typename Y, typename O, int V> static void run(const RowCall &c) {
+        const RowGroups q = row_groups(c.T, c.d / V, 16);
 #define COMBINE(G)                                                                                                 \
     case G:                                                                                                        \
-        STRATA_LAUNCH((combine_rows_kernel<Y, O, V, G>), row_grid(c.T, G), dim3(256), 0, c.s, (const Y *)c.ys, c.pos, \
+        STRATA_LAUNCH((combine_rows_kernel<Y, O, V, G>), row_grid(c.T, G, q.shares), dim3(256), 0, c.s, (const Y *)c.ys, c.pos, \
                       c.w, (const O *)c.in, (O *)c.out, c.T, c.k, c.d, c.rows);                                    \
         break;
-        switch (row_threads(c.d / V, 16)) { COMBINE(16) COMBINE(32) COMBINE(64) COMBINE(128) COMBINE(256) }
+        switch (q.threads) { COMBINE(16) COMBINE(32) COMBINE(64) COMBINE(128) COMBINE(256) }
 #undef COMBINE
     }
 };
@@ -268,10 +284,10 @@ struct CombineBack {
     template <typename Y, typename O, int V> static void run(const RowCall &c) {
 #define BACK(G)                                                                                                    \
     case G:                                                                                                        \
-        STRATA_LAUNCH((combine_back_kernel<Y, O, V, G>), row_grid(c.T, G), dim3(256), 0, c.s, (const O *)c.in,     \
+        STRATA_LAUNCH((combine_back_kernel<Y, O, V, G>), row_grid(c.T, G, 1), dim3(256), 0, c.s, (const O *)c.in,     \
                       (const Y *)c.ys, c.pos, c.w, (Y *)c.out, c.dw, c.dz, c.T, c.k, c.d, c.rows);                 \
         break;
-        switch (row_threads(c.d / V, 64)) { BACK(64) BACK(128) BACK(256) }
+        switch (row_groups(c.T, c.d / V, 64).threads) { BACK(64) BACK(128) BACK(256) }
 #undef BACK
     }
 };
