@@ -254,8 +254,8 @@ int64_t weight_blocks(const GroupArgs &a, int t) {
 // to 1.63 with 128 square) or some with long contractions (16 experts of 1024
 // rows: 99 against 109 us; of 256 rows: 50 against 46).  Else 128 square, two
 // blocks to a CU (4 experts of 1024 rows, 2048 x 768: 20 us, 64 square 27),
-// and 64 square where even those are fewer than the CUs (4 experts of 4096
-// rows, 128 x 128: 21 against 31 us).
+// and 64 square, four buffers, where even those are fewer than the CUs (4
+// experts of 4096 rows, 128 x 128: 17 against 31 us, 21 with two buffers).
 strata_status grouped_weights(const GroupArgs &a, hipStream_t s) {
     const int64_t large = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
     const int64_t small = (int64_t)a.E * ((a.N + 127) / 128) * ((a.K + 127) / 128);
@@ -264,7 +264,7 @@ strata_status grouped_weights(const GroupArgs &a, hipStream_t s) {
     else if (small >= 256)
         STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 2>), dim3((unsigned)weight_blocks(a, 128)), dim3(256), 0, s, a);
     else
-        STRATA_LAUNCH((grouped_wgrad_kernel<64, 64, 1, 2, 2>), dim3((unsigned)weight_blocks(a, 64)), dim3(128), 0, s, a);
+        STRATA_LAUNCH((grouped_wgrad_kernel<64, 64, 1, 2, 4>), dim3((unsigned)weight_blocks(a, 64)), dim3(128), 0, s, a);
     return hip_status(hipGetLastError());
 }
 
