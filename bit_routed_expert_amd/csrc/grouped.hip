@@ -231,14 +231,17 @@ template <int BM, int BN, int WM, int WN, int ST, int TB> strata_status launch_r
 // Tile by the average rows of an expert.  Up to 16, 32-row tiles: the weights
 // bound it and more, smaller blocks keep more of them in flight (E = 16, 16
 // rows each, 1536 x 2048: 22 us against 26 us for 128-row tiles; E = 512, 2
-// rows: 400 against 412).  Then 128 x 256 with three buffers (E = 512, 64
+// rows: 400 against 412); the same where fewer than 64 of the next tiles
+// exist (4 experts of 64 rows, 1536 x 2048: 16 against 24 us; 8 of 256 rows,
+// 512 x 512: 12 against 11).  Then 128 x 256 with three buffers (E = 512, 64
 // rows: 647 us, 5.0 TB/s, against 826 us).  From 384 rows on, and with tiles
 // enough for the 256 CUs, 256 x 256, whose operands are read half as often
 // (E = 16, 4096 rows: 406 against 438 us; with 256 rows 53 against 37 us).
 template <int TB> strata_status grouped_rows(GroupArgs &a, hipStream_t s) {
     const int64_t rows = a.rows, E = a.E;
     const int Nn = TB ? a.K : a.N;
-    if (rows <= 16 * E) return launch_rows<GP_MIN_ROWS, 128, 1, 4, 4, TB>(a, s);
+    if (rows <= 16 * E || (rows / 128 + E) * ((Nn + 255) / 256) < 64)
+        return launch_rows<GP_MIN_ROWS, 128, 1, 4, 4, TB>(a, s);
     if (rows < 384 * E || rows / 256 * ((Nn + 255) / 256) < 192) return launch_rows<128, 256, 2, 4, 3, TB>(a, s);
     return launch_rows<256, 256, 2, 4, 2, TB>(a, s);
 }

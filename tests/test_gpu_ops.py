@@ -230,7 +230,8 @@ GROUPS = [  # rows per expert, N, K, rows behind the last
     ([1] + [0] * 19 + [3], 88, 8192, 1), ([1] + [0] * 3, 8, 8, 0), ([0] * 9, 16, 16, 2),
     # the largest tiles and grids whose tiles an earlier launch lists; more than 64 experts
     ([5000, 131, 7769], 1000, 904, 2), ([39000, 900], 1000, 136, 0), ([20, 0, 41, 19] * 32 + [300], 520, 1032, 1),
-    ([3, 1, 5] * 67, 520, 264, 0), ([(7 * i) % 90 for i in range(40)], 1288, 1288, 3), ([0] * 30 + [700] * 2, 136, 1000, 0)]
+    ([3, 1, 5] * 67, 520, 264, 0), ([(7 * i) % 90 for i in range(40)], 1288, 1288, 3), ([0] * 30 + [700] * 2, 136, 1000, 0),
+    ([40, 39, 0, 161] * 10, 520, 600, 2)]
 
 
 def group_inputs(ns, N, K, tail, seed=1):
