@@ -705,6 +705,20 @@ def test_calls_on_another_stream(which):
     assert same(bits(outs), want)
 
 
+def test_addresses_beside_tensors():
+    """Raw addresses may stand for any of the tensors, or for all of them."""
+    T, k, E, d = 9, 4, 6, 64
+    pos, rows = positions(T, k, E, 0.2, 3).cuda(), T * k
+    x = rand(T, d, seed=1).cuda()
+    want = torch.zeros(rows, d, device="cuda")
+    brx.dispatch(x, 1, T, k, d, pos, want, rows)
+    for give in range(8):
+        xs = torch.zeros(rows, d, device="cuda")
+        a = [t.data_ptr() if give >> i & 1 else t for i, t in enumerate((x, pos, xs))]
+        brx.dispatch(a[0], 1, T, k, d, a[1], a[2], rows)
+        assert torch.equal(xs, want), give
+
+
 # ------------------------------------------------------------- all together
 
 def test_a_trainable_sparse_block():

@@ -154,6 +154,49 @@ def test_binding_checks_tensors():
         brx.block_norm_backward_workspace_bytes(_args(eps=0.0))
 
 
+SIZES = {   # every entry point's sizes, and the positions of its tensors
+    "sort_picks": (lambda T, *t: brx.sort_picks(t[0], T, 4, 8, *t[1:6], 256), 6),
+    "dispatch": (lambda T, *t: brx.dispatch(t[0], 1, T, 4, 64, t[1], t[2], 20), 3),
+    "dispatch_backward": (lambda T, *t: brx.dispatch_backward(t[0], 1, T, t[1], 5, 4, 64, t[2]), 3),
+    "combine": (lambda T, *t: brx.combine(t[0], 1, T, t[1], t[2], 5, 4, 64, t[3], 1, base=t[4]), 5),
+    "combine_backward": (lambda T, *t: brx.combine_backward(t[0], 1, t[1], 1, T, t[2], t[3], 5, 4, 64, *t[4:7]), 7),
+    "grouped_product": (lambda T, *t: brx.grouped_product(t[0], t[1], t[2], T, 8, 64, 64, t[3], 1, t[4], 1 << 20), 5),
+    "grouped_dgrad": (lambda T, *t: brx.grouped_dgrad(t[0], t[1], t[2], T, 8, 64, 64, t[3], 1, t[4], 1 << 20), 5),
+    "grouped_wgrad": (lambda T, *t: brx.grouped_wgrad(t[0], t[1], t[2], T, 8, 64, 64, t[3], 1, t[4], 1 << 20), 5),
+    "block_norm": (lambda T, *t: brx.block_norm(_args(T=T, flags=31 - brx.GATE_TOKEN), *t[:9]), 9),
+    "block_norm_backward": (lambda T, *t: brx.block_norm_backward(_args(T=T, flags=31 - brx.GATE_TOKEN), *t[:15], 1 << 20),
+                            15),
+}
+
+
+@pytest.mark.parametrize("name", sorted(SIZES))
+def test_binding_takes_no_host_tensor_among_addresses(name):
+    """One tensor in host memory among raw addresses: refused by the binding wherever it stands, the workspace too."""
+    call, n = SIZES[name]
+    for i in range(n):
+        t = [P] * n
+        t[i] = torch.zeros(1 << 20, dtype=torch.uint8)
+        with pytest.raises(brx.StrataError) as e:
+            call(5, *t)
+        assert e.value.status == EINVAL and "device memory" in str(e.value), (i, str(e.value))
+
+
+@pytest.mark.parametrize("name", sorted(SIZES))
+def test_binding_takes_no_size_past_32_bits(name):
+    """A size that a C int32 would cut to a smaller, valid one."""
+    call, n = SIZES[name]
+    for T in (2**32, 2**32 + 5, 2**31):
+        with pytest.raises(brx.StrataError) as e:
+            call(T, *[P + 8] * n)      # misaligned addresses: nothing is launched either way
+        assert e.value.status == EINVAL and "32 bits" in str(e.value)
+    with pytest.raises(brx.StrataError):
+        brx.sort_workspace_bytes(2**32 + 5, 4, 8)
+    with pytest.raises(brx.StrataError):
+        brx.grouped_workspace_bytes(2**32 + 5, 8, 64, 64)
+    with pytest.raises(brx.StrataError):
+        brx.grouped_product(P, P, P, 5, 8, 64, 64, P, 1, P, -1)
+
+
 def _leaf(*shape, seed):
     return torch.randn(*shape, dtype=torch.float64, generator=torch.Generator().manual_seed(seed)).requires_grad_(True)
 
