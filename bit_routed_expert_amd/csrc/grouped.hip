@@ -7,19 +7,19 @@
 //
 // Each is C[m][n] = sum_c A[m][c] B[n][c] over one expert's rows; what
 // differs is whether an operand's c runs along memory or across it.  The
-// expert's row count is only known on the device, so a first launch cuts the
-// experts' rows into tiles and lists them (product and dgrad; wgrad's tiles
-// are those of the weights).
+// expert's row count is only known on the device: in product and dgrad a
+// first launch cuts the experts' rows into tiles and lists them, or, in a
+// small grid, each block finds its own; wgrad's tiles are those of the
+// weights.
 #include "grouped_impl.hpp"
 
 namespace strata {
-
 
 // One block: the rows of every expert (cut to 0..rows and made to ascend by
 // a running maximum, so tiles never overlap and their number is bounded),
 // then the list of tiles.
 __global__ __launch_bounds__(1024) void grouped_plan_kernel(GroupArgs a) {
-    __shared__ int32_t first[GP_E + 1];   // first tile of each expert
+    __shared__ int32_t first[GP_E];   // first tile of each expert
     __shared__ int32_t seg0[GP_E], seg1[GP_E];
     __shared__ int32_t wave[16];
     const int th = threadIdx.x, lane = th & 63, w = th >> 6;
@@ -56,10 +56,7 @@ __global__ __launch_bounds__(1024) void grouped_plan_kernel(GroupArgs a) {
         total += wave[q];
     }
     first[th] = s - tiles;
-    if (th == 0) {
-        first[GP_E] = total;
-        *a.n_items = total;
-    }
+    if (th == 0) *a.n_items = total;
     __syncthreads();
     for (int i = th; i < total; i += 1024) {
         int e = 0;   // the last expert whose first tile is at or before i

@@ -53,13 +53,11 @@ template <int R, int ACROSS, int NT> struct Operand {
     const uint16_t *base;       // along: first row's first value; across: first contraction row
     int ld, count, cd;          // row length in memory, rows of the tile in range (along), contraction
     uint32_t off[LOADS];        // byte offset of this thread's chunks at step 0
-    int col0;
 
     // p: the operand's first value; tile rows r0.. of `total`.
     __device__ __forceinline__ void init(const uint16_t *p, int ld_, int r0, int total, int cd_) {
         ld = ld_;
         cd = cd_;
-        col0 = r0;
         count = ACROSS ? 0 : min(total - r0, R);
         base = ACROSS ? p : p + (int64_t)r0 * ld;
         const int th = threadIdx.x;

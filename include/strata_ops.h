@@ -57,7 +57,8 @@ strata_status strata_moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t 
 /* xs[pos[t*k + r]] = x[t]: the token rows copied to their picks' slots.
  *   x   [dev] [T][d], xs [dev] [rows][d], both xdtype.
  *   pos [dev] [T*k] int32; entries outside 0..rows-1 copy nothing.
- * Rows of xs without a pick are left as they were.  T = 0: no-op.  EINVAL: a
+ * Rows of xs without a pick are left as they were; where two picks name the
+ * same row, which token's values it gets is not specified.  T = 0: no-op.  EINVAL: a
  * null or misaligned pointer, T, rows < 0, d < 1, k outside 1..32, a bad
  * dtype; EUNSUPPORTED: T > 2^23, d > 2^24 or T*k > 2^31 - 1; EHIP. */
 strata_status strata_moe_dispatch(const void *x, strata_xdtype xdtype, int32_t T, int32_t k, int32_t d,
@@ -100,9 +101,9 @@ strata_status strata_moe_combine_backward(const void *dout, strata_xdtype odtype
  * outside the buffers is touched.  Matrix-core products of bf16 operands,
  * summed in fp32.
  * Limits: N % 8 == 0, K % 8 == 0, 8 <= N, K <= 65536, N*K <= 2^29, 1 <= E <=
- * 1024, E*N*K <= 2^37, rows <= 2^22, else EUNSUPPORTED.  EINVAL: a null or misaligned pointer, rows < 0, a
- * bad dtype; EWORKSPACE; EHIP.  Rows behind the last expert's are not read
- * and their outputs are left as they were.
+ * 1024, E*N*K <= 2^37, rows <= 2^22, else EUNSUPPORTED.  EINVAL: a null or
+ * misaligned pointer, rows < 0, a bad dtype; EWORKSPACE; EHIP.  Rows behind
+ * the last expert's are not read and their outputs are left as they were.
  */
 
 /* Bytes of workspace each of the three calls needs; 0 for arguments they refuse. */
