@@ -225,15 +225,16 @@ template <int BM, int BN, int WM, int WN, int ST, int TB> strata_status launch_r
     return hip_status(hipGetLastError());
 }
 
-// Tile by the average rows of an expert.  Up to 16, 32-row tiles: the weights
-// bound it and more, smaller blocks keep more of them in flight (E = 16, 16
-// rows each, 1536 x 2048: 22 us against 26 us for 128-row tiles; E = 512, 2
-// rows: 400 against 412); the same where fewer than 64 of the next tiles
-// exist (4 experts of 64 rows, 1536 x 2048: 16 against 24 us; 8 of 256 rows,
-// 512 x 512: 12 against 11).  Then 128 x 256 with three buffers (E = 512, 64
-// rows: 647 us, 5.0 TB/s, against 826 us).  From 384 rows on, and with tiles
-// enough for the 256 CUs, 256 x 256, whose operands are read half as often
-// (E = 16, 4096 rows: 406 against 438 us; with 256 rows 53 against 37 us).
+// Tile by the average rows of an expert (1536 x 2048 unless said).  Up to 16,
+// 32-row tiles: the weights bound it and more, smaller blocks keep more of
+// them in flight (E = 16, 16 rows each: 18 us against 19 us for 128-row tiles;
+// E = 512, 2 rows: 521 against 537); the same where fewer than 64 of the next
+// tiles exist (4 experts of 64 rows: 12 against 18 us; 8 of 256 rows, 512 x
+// 512: 7.5 against 10).  Then 128 x 256 with three buffers (E = 512, 64 rows:
+// 620 us, 5.6 TB/s, against 734 with 32 rows and 676 with 256).  From 384 rows
+// on, and with tiles enough for the 256 CUs, 256 x 256, whose operands are read
+// half as often (E = 16, 4096 rows: 362 against 398 us, 512 rows: 56 against
+// 65; with 256 rows 46 against 30 us).
 template <int TB> strata_status grouped_rows(GroupArgs &a, hipStream_t s) {
     const int64_t rows = a.rows, E = a.E;
     const int Nn = TB ? a.K : a.N;
@@ -249,22 +250,25 @@ int64_t weight_blocks(const GroupArgs &a, int t) {
     return (a.E * nn * nk + 7) / 8 * 8;
 }
 
-// Tiles of the weights' gradient.  256 square where there are many (512
-// experts, 16 to 256 rows each, 1536 x 2048 bf16: 0.74 to 1.37 ms against 0.81
-// to 1.63 with 128 square) or some with long contractions (16 experts of 1024
-// rows: 99 against 109 us; of 256 rows: 50 against 46).  Else 128 square, two
-// blocks to a CU (4 experts of 1024 rows, 2048 x 768: 20 us, 64 square 27),
-// and 64 square, four buffers, where even those are fewer than the CUs (4
-// experts of 4096 rows, 128 x 128: 17 against 31 us, 21 with two buffers).
+// Tiles of the weights' gradient (1536 x 2048 bf16 unless said).  256 square
+// where there are many (512 experts of 16, 80 and 256 rows: 0.68, 0.88 and 1.36
+// ms against 0.73, 1.05 and 1.51 with 128 square) or some with long
+// contractions (16 experts of 1024 rows, fp32: 115 against 129 us; of 256 rows:
+// 64 against 53).  Else 128 square, three blocks to a CU (4 experts of 1024
+// rows, 2048 x 768: 20 us, 64 square 27), and 64 square where even those are
+// fewer than the CUs (4 experts of 4096 rows, 128 x 128: 17 against 28 us).
+// Steps of 32 in three buffers but for the smallest, of 64 in four: 32768 rows of
+// 16 uneven experts in 256 square 210 us, with steps of 64 in two buffers 225;
+// 16 experts of 256 rows in 128 square 46 against 53 us.
 strata_status grouped_weights(const GroupArgs &a, hipStream_t s) {
     const int64_t large = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
     const int64_t small = (int64_t)a.E * ((a.N + 127) / 128) * ((a.K + 127) / 128);
     if (large >= 1024 || (large >= 512 && a.rows >= 512 * (int64_t)a.E))
-        STRATA_LAUNCH((grouped_wgrad_kernel<256, 256, 2, 4, 2>), dim3((unsigned)weight_blocks(a, 256)), dim3(512), 0, s, a);
+        STRATA_LAUNCH((grouped_wgrad_kernel<256, 256, 2, 4, 3, 32>), dim3((unsigned)weight_blocks(a, 256)), dim3(512), 0, s, a);
     else if (small >= 256)
-        STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 2>), dim3((unsigned)weight_blocks(a, 128)), dim3(256), 0, s, a);
+        STRATA_LAUNCH((grouped_wgrad_kernel<128, 128, 2, 2, 3, 32>), dim3((unsigned)weight_blocks(a, 128)), dim3(256), 0, s, a);
     else
-        STRATA_LAUNCH((grouped_wgrad_kernel<64, 64, 1, 2, 4>), dim3((unsigned)weight_blocks(a, 64)), dim3(128), 0, s, a);
+        STRATA_LAUNCH((grouped_wgrad_kernel<64, 64, 1, 2, 4, 64>), dim3((unsigned)weight_blocks(a, 64)), dim3(128), 0, s, a);
     return hip_status(hipGetLastError());
 }
 

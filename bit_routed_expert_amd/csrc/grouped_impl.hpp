@@ -1,17 +1,18 @@
 // Tile products of the experts' grouped products on the gfx950 matrix cores.
 //
 // One block computes a tile C[BM][BN] = sum_c A[m][c] B[n][c] of one expert.
-// The contraction is cut into steps of 64; a step's tiles of A and B come
-// into LDS by direct global->LDS loads (16 bytes a lane, no registers) while
-// earlier steps run on the matrix cores: 2 to 4 buffers in turn, one barrier
-// a step.
+// The contraction is cut into steps of C = 64 or 32; a step's tiles of A and B
+// come into LDS by direct global->LDS loads (16 bytes a lane, no registers)
+// while earlier steps run on the matrix cores: 2 to 4 buffers in turn, one
+// barrier a step, met while the matrix cores still have the step's last 16 of
+// the contraction ahead of them.
 //
 // An operand whose contraction runs along memory (x and W in the product)
 // lies in LDS as it does in memory, 64 values (128 bytes) to a row; a lane's
 // 8 values of a 32x32x16 product are one 16-byte read, and the row's chunks
 // are permuted by the row number so that 32 rows' reads meet no bank twice.
 // An operand whose contraction runs across memory (W in dgrad, both in wgrad)
-// lies as 64 rows of BM or BN values; the transposing LDS reads of gfx950
+// lies as C rows of BM or BN values; the transposing LDS reads of gfx950
 // (four 16-bit rows of 16 columns per 16 lanes) hand each lane 4 values down
 // a column, two of them make its 8.  There the 64-byte pieces of a row are
 // permuted by the low two bits of the row number, so the four rows of a read
@@ -25,7 +26,6 @@
 
 namespace strata {
 
-constexpr int GP_C = 64;          // contraction per step
 constexpr int GP_E = 1024;        // most experts
 constexpr int GP_RANKED = 64;     // experts up to which the weights' gradient orders them by rows
 
@@ -46,10 +46,14 @@ struct GroupArgs {
 // of at least 64), across: the 64-byte pieces by the low bits of c.
 template <int R> __device__ __forceinline__ int across_swz(int c) { return ((c & 3) << 2) & (R / 8 - 1); }
 
-// One operand: R rows of it in the tile (m or n), NT threads stage it.
-template <int R, int ACROSS, int NT> struct Operand {
-    static constexpr int BYTES = R * GP_C * 2, LOADS = R * 8 / NT;
-    static_assert(LOADS * NT == R * 8, "whole chunks per thread");
+// The same of row r of an operand that lies along: 8 chunks.
+__device__ __forceinline__ int along_swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+// One operand: R rows of it in the tile (m or n), NT threads stage C of the contraction.
+template <int R, int ACROSS, int NT, int C> struct Operand {
+    static constexpr int BYTES = R * C * 2, CH = C / 8, LOADS = R * CH / NT;
+    static_assert(LOADS * NT == R * CH, "whole chunks per thread");
+    static_assert(ACROSS || C == 64, "along_swz is for rows of 128 bytes");
     const uint16_t *base;       // along: first row's first value; across: first contraction row
     int ld, count, cd;          // row length in memory, rows of the tile in range (along), contraction
     uint32_t off[LOADS];        // byte offset of this thread's chunks at step 0
@@ -68,17 +72,17 @@ template <int R, int ACROSS, int NT> struct Operand {
                 const int c = q / (R / 8), at = q % (R / 8);
                 off[i] = (uint32_t)c * (uint32_t)ld * 2u + (uint32_t)(r0 + 8 * (at ^ across_swz<R>(c))) * 2u;
             } else {
-                const int r = q >> 3, at = q & 7;
-                off[i] = (uint32_t)r * (uint32_t)ld * 2u + (uint32_t)(8 * (at ^ ((r ^ (r >> 3)) & 7))) * 2u;
+                const int r = q / CH, at = q % CH;
+                off[i] = (uint32_t)r * (uint32_t)ld * 2u + (uint32_t)(8 * (at ^ along_swz(r))) * 2u;
             }
         }
     }
 
-    __device__ __forceinline__ void load(int s, uint8_t *__restrict__ dst) const {
+    __device__ __forceinline__ void load(int s, uint8_t *dst) const {
         const int th = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(th >> 6);
-        const int left = max(cd - s * GP_C, 0);   // contraction from this step on (0: a load behind the end, all zeros)
-        const uint16_t *p = ACROSS ? base + (int64_t)s * GP_C * ld : base + (int64_t)s * GP_C;
-        const uint32_t bytes = ACROSS ? (uint32_t)min(left, GP_C) * (uint32_t)ld * 2u
+        const int left = max(cd - s * C, 0);   // contraction from this step on (0: a load behind the end, all zeros)
+        const uint16_t *p = ACROSS ? base + (int64_t)s * C * ld : base + (int64_t)s * C;
+        const uint32_t bytes = ACROSS ? (uint32_t)min(left, C) * (uint32_t)ld * 2u
                                       : left ? ((uint32_t)(count - 1) * (uint32_t)ld + (uint32_t)left) * 2u : 0u;
         // the size in a scalar register whatever unit computed it: a resource in vector registers makes
         // every load a loop over the lanes
@@ -87,9 +91,9 @@ template <int R, int ACROSS, int NT> struct Operand {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             uint32_t o = off[i];
-            if (!ACROSS && left < GP_C) {   // a last short step: chunks behind the end
-                const int q = i * NT + th, row = q >> 3;
-                if (8 * ((q & 7) ^ ((row ^ (row >> 3)) & 7)) >= left) o = 0x80000000u;
+            if (!ACROSS && left < C) {   // a last short step: chunks behind the end
+                const int q = i * NT + th;
+                if (8 * ((q % CH) ^ along_swz(q / CH)) >= left) o = 0x80000000u;
             }
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (__attribute__((address_space(3))) void *)(dst + (i * NT + wv * 64) * 16), 16, o, 0, 0, 0);
@@ -100,20 +104,20 @@ template <int R, int ACROSS, int NT> struct Operand {
 // The 8 values a lane feeds to one 32x32x16 product: tile rows r0 + lane%32,
 // contraction 16 kk + 8 (lane/32) .. +8 of the staged step.
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
-template <int R, int ACROSS>
-__device__ __forceinline__ bf16x8_t read_frag(const uint8_t *__restrict__ t, int r0, int kk) {
+template <int R, int ACROSS, int C>
+__device__ __forceinline__ bf16x8_t read_frag(const uint8_t *t, int r0, int kk) {
     const int lane = threadIdx.x & 63;
     if constexpr (!ACROSS) {
         const int r = r0 + (lane & 31), c = 2 * kk + (lane >> 5);
-        return __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(t + r * 128 + 16 * (c ^ ((r ^ (r >> 3)) & 7))));
+        return __builtin_bit_cast(bf16x8_t, *(const u32x4_t *)(t + (r * C * 2 + 16 * (c ^ along_swz(r)))));
     } else {
         const int i = lane & 15, g = lane >> 4;
         const int c = 16 * kk + 8 * (g >> 1) + (i >> 2);   // second read: c + 4, the same low bits
         const int chunk = (r0 >> 3) + 2 * (g & 1) + ((i >> 1) & 1);
-        const uint8_t *p = t + c * (R * 2) + 16 * (chunk ^ across_swz<R>(c)) + 8 * (i & 1);
+        const int p = c * (R * 2) + 16 * (chunk ^ across_swz<R>(c)) + 8 * (i & 1);
         typedef __attribute__((address_space(3))) s16x4_t lds4;
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
-        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 4 * R * 2));
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(t + p));
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(t + (p + 4 * R * 2)));
         return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 }
@@ -126,102 +130,131 @@ template <int N> __device__ __forceinline__ void wait_and_meet() {
     asm volatile("" ::: "memory");
 }
 
-// One staged step on the wave's MT x NT2 subtiles of 32x32.  The fragments of
-// the next 16 are read while the current 16 are multiplied; the scheduling
-// barriers keep the compiler from reading the whole step ahead, which costs
-// more registers than the accumulators leave.  next(kk) issues the next
-// step's loads behind the reads, among the products (256 square, 32768 rows
-// of 16 experts, 2048 x 2048: dgrad 302 -> 268 us, wgrad 286 -> 256 us against
-// loads ahead of the step).  A wave without rows only stages.
-template <int BM, int BN, int MT, int NT2, int TA, int TB, typename Next>
-__device__ __forceinline__ void step_product(const uint8_t *__restrict__ ta, const uint8_t *__restrict__ tb, int m0,
-                                             int n0, bool active, f32x16_t (&acc)[MT][NT2], Next next) {
-    if (!active) {
-#pragma unroll
-        for (int kk = 0; kk < GP_C / 16; ++kk) next(kk);
-        return;
-    }
+// What a wave feeds to 16 of the contraction on its MT x NT2 subtiles of
+// 32x32, twice: the next 16 are read while the current 16 are multiplied.
+template <int MT, int NT2> struct Frags {
     bf16x8_t a[2][MT], b[2][NT2];
-#define READ_FRAGS(KK)                                                                                  \
-    {                                                                                                   \
-        _Pragma("unroll") for (int j = 0; j < NT2; ++j) b[(KK)&1][j] = read_frag<BN, TB>(tb, n0 + 32 * j, KK); \
-        _Pragma("unroll") for (int i = 0; i < MT; ++i) a[(KK)&1][i] = read_frag<BM, TA>(ta, m0 + 32 * i, KK);  \
-    }
-    READ_FRAGS(0)
+};
+template <int BM, int BN, int C, int MT, int NT2, int TA, int TB>
+__device__ __forceinline__ void read_frags(const uint8_t *ta, const uint8_t *tb, int m0,
+                                           int n0, int kk, int set, Frags<MT, NT2> &f) {
 #pragma unroll
-    for (int kk = 0; kk < GP_C / 16; ++kk) {
+    for (int j = 0; j < NT2; ++j) f.b[set][j] = read_frag<BN, TB, C>(tb, n0 + 32 * j, kk);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) f.a[set][i] = read_frag<BM, TA, C>(ta, m0 + 32 * i, kk);
+}
+
+// Step s, whose first 16 are in set 0 of f already; leaves the next step's
+// there.  Ahead of the step's last products every wave has read all of the
+// step's buffers and the next step's loads are done: the barrier stands there,
+// so its wait and the next step's first LDS reads hide behind products, and
+// A's buffer is loaded again right behind it (step s + ST), B's at the start of
+// the step after it.  Against a barrier at the start of a step (1536 x 2048):
+// 32768 rows of 16 uneven experts, product 220 -> 212 us, dgrad 220 -> 215 us,
+// wgrad 226 -> 208 us; 40960 rows of 512 experts, product 680 -> 666 us; 512
+// experts of 16 rows, wgrad 740 -> 677 us.
+// The scheduling barrier keeps the compiler from reading the whole step ahead,
+// which costs more registers than the accumulators leave.  WAIT: a wave's loads
+// that may still be under way at the barrier.  TAIL 1: no more steps to load
+// but B's last; 2: none.  A wave that is not ACTIVE has no rows and only stages.
+template <int ST, int BM, int BN, int C, int MT, int NT2, int TA, int TB, int WAIT, int TAIL, bool ACTIVE, typename OA,
+          typename OB>
+__device__ __forceinline__ void step_product(const OA &A, const OB &B, int s, int steps, uint8_t *ta, const uint8_t *tb,
+                                             const uint8_t *na, const uint8_t *nb, uint8_t *wb, int m0, int n0,
+                                             f32x16_t (&acc)[MT][NT2], Frags<MT, NT2> &f) {
+    constexpr int KS = C / 16;
+    const bool more = !TAIL || s + 1 < steps;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
         __builtin_amdgcn_sched_barrier(0);
-        if (kk + 1 < GP_C / 16) READ_FRAGS(kk + 1)
-        next(kk);
+        if (ACTIVE && kk + 1 < KS) read_frags<BM, BN, C, MT, NT2, TA, TB>(ta, tb, m0, n0, kk + 1, (kk + 1) & 1, f);
+        if (kk == 0 && TAIL < 2) B.load(s + ST - 1, wb);
+        if (kk + 1 == KS && more) {
+            wait_and_meet<WAIT>();
+            if (ACTIVE) read_frags<BM, BN, C, MT, NT2, TA, TB>(na, nb, m0, n0, 0, 0, f);
+            if (!TAIL) A.load(s + ST, ta);
+        }
+        if (ACTIVE) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < NT2; ++j) acc[i][j] = mfma(b[kk & 1][j], a[kk & 1][i], acc[i][j]);
+                for (int j = 0; j < NT2; ++j) acc[i][j] = mfma(f.b[kk & 1][j], f.a[kk & 1][i], acc[i][j]);
+        }
     }
-#undef READ_FRAGS
 }
 
 // The contraction with ST buffers: step s is multiplied while the ST - 1
-// behind it come in, A's loads issued with the first 16, B's with the second.
-// The buffers are distinct restrict pointers so that the compiler sees that a
-// read does not wait for the loads into the others.  With more than two
-// buffers, loads behind the end fetch nothing and keep the count of loads in
-// flight the same.
-template <int ST, typename OA, typename OB, int BM, int BN, int MT, int NT2, int TA, int TB>
-__device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *__restrict__ a0, uint8_t *__restrict__ b0,
-                                         uint8_t *__restrict__ a1, uint8_t *__restrict__ b1, uint8_t *__restrict__ a2,
-                                         uint8_t *__restrict__ b2, uint8_t *__restrict__ a3, uint8_t *__restrict__ b3,
-                                         int steps, int m0, int n0, bool active, f32x16_t (&acc)[MT][NT2]) {
+// behind it come in.  Loads behind the end fetch nothing and keep the count of
+// loads in flight the same.  The compiler waits for a direct load ahead of an
+// LDS read that it cannot tell from the load's target, which would undo the
+// buffering: it can where both are the kernel's own distinct arrays, no
+// pointer here is restrict (those scopes would hide the arrays'), reads are
+// one addition away from their array, and the loop has one exit.
+template <int ST, bool ACTIVE, int BM, int BN, int C, int MT, int NT2, int TA, int TB, typename OA, typename OB>
+__device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *a0, uint8_t *b0, uint8_t *a1, uint8_t *b1,
+                                         uint8_t *a2, uint8_t *b2, uint8_t *a3, uint8_t *b3, int steps, int m0, int n0,
+                                         f32x16_t (&acc)[MT][NT2]) {
     constexpr int L = OA::LOADS + OB::LOADS;   // a wave's loads per step
+    constexpr int W = (ST - 2) * L;
     if (steps == 0) return;
-#define STEP(S, MORE, AR, BR, AW, BW)                                                                  \
-    {                                                                                               \
-        wait_and_meet<(ST - 2) * L>();                                                              \
-        step_product<BM, BN, MT, NT2, TA, TB>(AR, BR, m0, n0, active, acc, [&](int kk) {            \
-            if (kk == 0 && (MORE)) A.load((S) + ST - 1, AW);                                        \
-            if (kk == 1 && (MORE)) B.load((S) + ST - 1, BW);                                        \
-        });                                                                                         \
-    }
+    Frags<MT, NT2> f;
+#define STEP(S, WAIT, TAIL, AR, BR, AN, BN_, BP) \
+    step_product<ST, BM, BN, C, MT, NT2, TA, TB, WAIT, TAIL, ACTIVE>(A, B, S, steps, AR, BR, AN, BN_, BP, m0, n0, acc, f);
     A.load(0, a0);
     B.load(0, b0);
-    if constexpr (ST > 2) {
-        A.load(1, a1);
-        B.load(1, b1);
-    }
-    if constexpr (ST > 3) {
-        A.load(2, a2);
-        B.load(2, b2);
-    }
-    const auto none = [](int) {};
-    int s = 0;
-    if constexpr (ST == 2) {
-        for (; s + 2 <= steps; s += 2) {
-            STEP(s, true, a0, b0, a1, b1)
-            STEP(s + 1, s + 2 < steps, a1, b1, a0, b0)
-        }
-        if (s < steps) {
-            wait_and_meet<0>();
-            step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, none);
+    if (steps == 1) {   // on its own: nothing to wait for but its loads
+        wait_and_meet<0>();
+        if (!ACTIVE) return;
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk) {
+            read_frags<BM, BN, C, MT, NT2, TA, TB>(a0, b0, m0, n0, kk, 0, f);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT2; ++j) acc[i][j] = mfma(f.b[0][j], f.a[0][i], acc[i][j]);
         }
         return;
     }
-    for (; s + ST <= steps; s += ST) {
-        if constexpr (ST == 3) {
-            STEP(s, true, a0, b0, a2, b2)
-            STEP(s + 1, true, a1, b1, a0, b0)
-            STEP(s + 2, true, a2, b2, a1, b1)
+    A.load(1, a1);
+    if constexpr (ST > 2) {
+        B.load(1, b1);
+        A.load(2, a2);
+    }
+    if constexpr (ST > 3) {
+        B.load(2, b2);
+        A.load(3, a3);
+    }
+    wait_and_meet<W + OA::LOADS>();
+    if (ACTIVE) read_frags<BM, BN, C, MT, NT2, TA, TB>(a0, b0, m0, n0, 0, 0, f);
+    int s = 0;
+    for (; s + ST < steps; s += ST) {
+        if constexpr (ST == 2) {
+            STEP(s, W, 0, a0, b0, a1, b1, b1)
+            STEP(s + 1, W, 0, a1, b1, a0, b0, b0)
+        } else if constexpr (ST == 3) {
+            STEP(s, W, 0, a0, b0, a1, b1, b2)
+            STEP(s + 1, W, 0, a1, b1, a2, b2, b0)
+            STEP(s + 2, W, 0, a2, b2, a0, b0, b1)
         } else {
-            STEP(s, true, a0, b0, a3, b3)
-            STEP(s + 1, true, a1, b1, a0, b0)
-            STEP(s + 2, true, a2, b2, a1, b1)
-            STEP(s + 3, true, a3, b3, a2, b2)
+            STEP(s, W, 0, a0, b0, a1, b1, b3)
+            STEP(s + 1, W, 0, a1, b1, a2, b2, b0)
+            STEP(s + 2, W, 0, a2, b2, a3, b3, b1)
+            STEP(s + 3, W, 0, a3, b3, a0, b0, b2)
         }
     }
+    // the last one to ST steps; B of the last is the only load not issued yet
+    if constexpr (ST == 2) STEP(s, W, 1, a0, b0, a1, b1, b1)
+    else if constexpr (ST == 3) STEP(s, W, 1, a0, b0, a1, b1, b2)
+    else STEP(s, W, 1, a0, b0, a1, b1, b3)
+    if (s + 1 < steps) {
+        constexpr int W1 = ST > 3 ? (ST - 3) * L : 0;
+        if constexpr (ST == 2) STEP(s + 1, 0, 2, a1, b1, a0, b0, b0)
+        else STEP(s + 1, W1, 2, a1, b1, a2, b2, b0)
+    }
+    if (ST > 2 && s + 2 < steps) STEP(s + 2, 0, 2, a2, b2, ST > 3 ? a3 : a0, ST > 3 ? b3 : b0, b1)
+    if (ST > 3 && s + 3 < steps) STEP(s + 3, 0, 2, a3, b3, a0, b0, b2)
 #undef STEP
-    wait_and_meet<0>();   // the last steps, and no load outlives the loop
-    if (s < steps) step_product<BM, BN, MT, NT2, TA, TB>(a0, b0, m0, n0, active, acc, none);
-    if (s + 1 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a1, b1, m0, n0, active, acc, none);
-    if (ST > 3 && s + 2 < steps) step_product<BM, BN, MT, NT2, TA, TB>(a2, b2, m0, n0, active, acc, none);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // no load outlives the block
 }
 
 // The ST buffers of a block's two operands.
@@ -338,9 +371,9 @@ template <int NT> struct FindItem {
 // (product, dgrad).  LIST: the row tiles were listed by an earlier launch.
 template <int BM, int BN, int WM, int WN, int ST, int TB, int LIST>
 __global__ __launch_bounds__(64 * WM *WN) void grouped_rows_kernel(GroupArgs a) {
-    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
-    typedef Operand<BM, 0, NT> OA;
-    typedef Operand<BN, TB, NT> OB;
+    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN, C = 64;
+    typedef Operand<BM, 0, NT, C> OA;
+    typedef Operand<BN, TB, NT, C> OB;
     GROUP_BUFFERS(ST, OA, OB)
     const int Cd = TB ? a.N : a.K, Nn = TB ? a.K : a.N;
     int item, ct;
@@ -372,8 +405,12 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_rows_kernel(GroupArgs a) 
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    contract<ST, OA, OB, BM, BN, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, (Cd + GP_C - 1) / GP_C, m0, n0,
-                                                 m0 < it.n, acc);
+    const int steps = (Cd + C - 1) / C;
+    if (m0 >= it.n) {   // no rows for this wave: it only stages
+        contract<ST, false, BM, BN, C, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+        return;
+    }
+    contract<ST, true, BM, BN, C, MT, NT2, 0, TB>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
     store_tile<MT, NT2>((char *)a.C + (int64_t)it.row0 * Nn * (a.c_bf16 ? 2 : 4), a.c_bf16, m0, it.n, ct * BN + n0, Nn,
                         acc);
 }
@@ -398,11 +435,11 @@ __device__ __forceinline__ int expert_by_rows(const GroupArgs &a, int r) {
 // tile dealt on its own 281, 223 and 235 us; even experts, 2048 x 2048: 263
 // against 275 us.  With more experts they even out, and an expert's tiles
 // stay on one XCD.
-template <int BM, int BN, int WM, int WN, int ST>
+template <int BM, int BN, int WM, int WN, int ST, int C>
 __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;
-    typedef Operand<BM, 1, NT> OA;
-    typedef Operand<BN, 1, NT> OB;
+    typedef Operand<BM, 1, NT, C> OA;
+    typedef Operand<BN, 1, NT, C> OB;
     GROUP_BUFFERS(ST, OA, OB)
     const int nk = (a.K + BN - 1) / BN, per_e = nk * ((a.N + BM - 1) / BM);
     int e, tn, tk;
@@ -438,8 +475,8 @@ __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a)
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    contract<ST, OA, OB, BM, BN, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, (cd + GP_C - 1) / GP_C, m0, n0,
-                                                true, acc);
+    contract<ST, true, BM, BN, C, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, (cd + C - 1) / C, m0,
+                                                      n0, acc);
     store_tile<MT, NT2>((char *)a.C + ((int64_t)e * a.N + r0) * a.K * (a.c_bf16 ? 2 : 4), a.c_bf16, m0,
                         min(a.N - r0, BM), k0 + n0, a.K, acc);
 }

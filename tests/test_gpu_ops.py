@@ -276,6 +276,54 @@ def test_grouped_products(ns, N, K, tail, ot):
     R.check(dW.guarded(), ref, mag, "dW")
 
 
+LENGTHS = [   # rows per expert, N, K, what is run: contractions of 1 to 13 whole and ragged steps in every tile
+    *[([7, 0, 50], 136, 64 * n + r, "product") for n in range(1, 10) for r in (0, -8)],                 # 32-row tiles
+    *[([7, 0, 50], 64 * n + r, 136, "dgrad") for n in range(1, 10) for r in (0, -8)],
+    *[([120] * 40, 520, 64 * n + r, "product") for n in range(1, 8) for r in (0, 8)],                   # 128-row tiles
+    *[([120] * 40, 64 * n + r, 520, "dgrad") for n in range(1, 8) for r in (0, 8)],
+    *[([25000, 24200], 256, 64 * n + r, "product") for n in range(1, 6) for r in (0, -56)],             # 256-row tiles
+    *[([25000, 24200], 64 * n + r, 256, "dgrad") for n in range(1, 6) for r in (0, -56)],
+    ([16 * i + i % 3 for i in range(25)], 128, 128, "wgrad"),                                           # 64 square
+    ([16 * i + i % 3 for i in range(25)], 512, 512, "wgrad"),                                           # 128 square
+    ([16 * i + i % 3 for i in range(25)] + [31, 32, 33] * 5, 1288, 1288, "wgrad"),                      # 256 square
+    ([16 * (i % 25) + i % 3 for i in range(70)], 1032, 776, "wgrad"),                                   # the same, not ranked
+]
+
+
+@pytest.mark.parametrize("ns,N,K,what", LENGTHS)
+def test_grouped_contractions_of_every_length(ns, N, K, what):
+    """The buffered contraction's start, turns and end: as test_grouped_products, fp32 outputs."""
+    print(f"case length {len(ns)} N={N} K={K} {what}", flush=True)
+    rows, off, x, dy, W = group_inputs(ns, N, K, 0, seed=4)
+    E = len(ns)
+    nb = brx.grouped_workspace_bytes(rows, E, N, K)
+    ws, oc = ws_of(nb), off.cuda()
+    xc, yc, Wc = x.cuda(), dy.cuda(), W.cuda()
+    first = None
+    for _ in range(2):
+        if what == "product":
+            out = Out(rows, N, dtype=F32)
+            brx.grouped_product(xc, Wc, oc, rows, E, N, K, out.t, 1, ws, nb)
+        elif what == "dgrad":
+            out = Out(rows, K, dtype=F32)
+            brx.grouped_dgrad(yc, Wc, oc, rows, E, N, K, out.t, 1, ws, nb)
+        else:
+            out = Out(E, N, K, dtype=F32)
+            brx.grouped_wgrad(yc, xc, oc, rows, E, N, K, out.t, 1, ws, nb)
+        got = out.guarded()
+        first = got if first is None else first
+        assert torch.equal(got, first)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if what == "wgrad":
+            a, b, n, g = yc[lo:hi].double().t().contiguous(), xc[lo:hi].double(), hi - lo, got[e]
+        elif what == "product":
+            a, b, n, g = xc[lo:hi].double(), Wc[e].double().t().contiguous(), K, got[lo:hi]
+        else:
+            a, b, n, g = yc[lo:hi].double(), Wc[e].double(), N, got[lo:hi]
+        R.check(g, (a @ b).cpu(), (2 * n * U * (a.abs() @ b.abs())).cpu(), f"{what} of expert {e}")
+
+
 def test_grouped_without_rows():
     E, N, K = 3, 64, 72
     nb = brx.grouped_workspace_bytes(0, E, N, K)
