@@ -58,14 +58,38 @@ def _compile_host_common() -> str:
     return obj
 
 
+# The operators' tensor checks: a CPython module against torch's headers.
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(HERE, "..", "include"), "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"host compile failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source (always) and link the shared library."""
+    """Compile every source (always), link the shared library and the binding's module."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
         futs = [ex.submit(_compile, src) for src in SOURCES]
         futs += [ex.submit(_compile_host, ns) for ns in HOST_ISAS]
         futs.append(ex.submit(_compile_host_common))
+        binding = ex.submit(_compile_binding)
         objs = [f.result() for f in futs]
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -5,6 +5,8 @@ guard bands behind every output; captured and replayed in graphs, on other
 streams, twice with the same bits, and together as one trainable block."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -765,6 +767,43 @@ def test_addresses_beside_tensors():
         a = [t.data_ptr() if give >> i & 1 else t for i, t in enumerate((x, pos, xs))]
         brx.dispatch(a[0], 1, T, k, d, a[1], a[2], rows)
         assert torch.equal(xs, want), give
+
+
+def test_a_call_whose_device_is_not_current():
+    """The call is made once more with its tensors' device current, and on a
+    stream that is given; what it returns and raises stays the same."""
+    brx.sort_workspace_bytes(1, 1, 1)
+    T, k, d, rows = 5, 4, 64, 20
+    pos = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    x, xs = rand(T, d, seed=1).cuda(), Out(rows, d, dtype=F32)
+    brx.dispatch(x, 1, T, k, d, pos, xs.t, rows)
+    native = brx.ops._native
+    seen = []
+
+    def elsewhere(dev, fn, *args):
+        seen.append(dev)
+        bind(lambda: 0)
+        brx.ops._elsewhere(dev, fn, *args)
+
+    def bind(device):
+        lib = brx.load_library()
+        native.bind(tuple(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in brx.ops._BOUND), brx.ops._raise,
+                    elsewhere, device, torch.cuda.current_device, torch._C._cuda_getCurrentRawStream)
+    try:
+        for stream in (None, torch.cuda.current_stream(), torch.cuda.current_stream().cuda_stream):
+            bind(lambda: 1)   # as if device 1 were current
+            out = Out(rows, d, dtype=F32)
+            brx.dispatch(x, 1, T, k, d, pos, out.t, rows, stream=stream)
+            assert torch.equal(out.guarded(), xs.guarded()) and seen.pop() == 0 and not seen
+        bind(lambda: 1)
+        with pytest.raises(brx.StrataError) as e:
+            brx.dispatch(x, 1, T, 33, d, pos.repeat(9)[:T * 33].contiguous(), xs.t, rows)
+        assert e.value.status == brx.STRATA_EINVAL
+    finally:
+        bind(torch._C._cuda_getDevice)
+        brx.ops._native = brx.ops._Unloaded()   # bound anew at the next call
+    brx.dispatch(x, 1, T, k, d, pos, xs.t, rows)
+    assert brx.ops._native is native
 
 
 # ------------------------------------------------------------- all together

@@ -4,6 +4,7 @@ reference's gradients against differences."""
 from __future__ import annotations
 
 import ctypes
+import sys
 
 import pytest
 import torch
@@ -195,6 +196,27 @@ def test_binding_takes_no_size_past_32_bits(name):
         brx.grouped_workspace_bytes(2**32 + 5, 8, 64, 64)
     with pytest.raises(brx.StrataError):
         brx.grouped_product(P, P, P, 5, 8, 64, 64, P, 1, P, -1)
+
+
+def test_binding_keeps_no_references():
+    """A refused call, however far it got, leaves its arguments' reference counts as they were."""
+    t, args = torch.zeros(20, dtype=torch.int32), _args(T=5, flags=31 - brx.GATE_TOKEN)
+    count = sys.getrefcount(t), sys.getrefcount(args)
+    for _ in range(50):
+        for call in (lambda: brx.sort_picks(t, 5, 4, 8, None, None, None, None, None, 0),
+                     lambda: brx.dispatch(P, 1, 5, 4, 64, "pos", P, 20),
+                     lambda: brx.block_norm(args, P, P, t),
+                     lambda: brx.block_norm(args, P, object()),
+                     lambda: brx.block_norm_backward(args, P, P, P, P, ws_bytes=-1)):
+            with pytest.raises(brx.StrataError):
+                call()
+    with pytest.raises(TypeError):
+        brx.dispatch(P, 1, "T", 4, 64, P, P, 20)
+    with pytest.raises(TypeError):
+        brx.block_norm(object(), P, P)
+    with pytest.raises(brx.StrataError):
+        brx.block_norm(bytearray(8), P, P)
+    assert (sys.getrefcount(t), sys.getrefcount(args)) == count
 
 
 def _leaf(*shape, seed):
