@@ -285,6 +285,9 @@ LENGTHS = [   # rows per expert, N, K, what is run: contractions of 1 to 13 whol
     *[([120] * 40, 64 * n + r, 520, "dgrad") for n in range(1, 8) for r in (0, 8)],
     *[([25000, 24200], 256, 64 * n + r, "product") for n in range(1, 6) for r in (0, -56)],             # 256-row tiles
     *[([25000, 24200], 64 * n + r, 256, "dgrad") for n in range(1, 6) for r in (0, -56)],
+    *[([25000, 24200, 130], 136, n, "dgrad") for n in (264, 328, 456)],                                 # waves without columns
+    *[([25000, 24200, 130], n, 136, "product") for n in (264, 328, 456)],
+    *[([300, 120, 7] * 14, n, 200, "product") for n in (264, 328, 392, 456)],
     ([16 * i + i % 3 for i in range(25)], 128, 128, "wgrad"),                                           # 64 square
     ([16 * i + i % 3 for i in range(25)], 512, 512, "wgrad"),                                           # 128 square
     ([16 * i + i % 3 for i in range(25)] + [31, 32, 33] * 5, 1288, 1288, "wgrad"),                      # 256 square
