@@ -132,6 +132,14 @@ __global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__
     const bool live = row_group<G>(T, t, lane);
     const int g = threadIdx.x / G, wv = (threadIdx.x % G) / 64;
     const bool dots = dw || dz;
+    // lane r of the group's first wave ends with pick r: its weight and position, read while the rows are
+    const int th = threadIdx.x % G;
+    float wr = 0.f;
+    int pr = -1;
+    if (dz && live && th < k) {
+        wr = w[(int64_t)t * k + th];
+        pr = pos[(int64_t)t * k + th];
+    }
     if (live) {
         const int32_t *pt = pos + (int64_t)t * k;
         const float *wt = w + (int64_t)t * k;
@@ -169,19 +177,17 @@ __global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__
             }
             if (dots) {
 #pragma unroll
-                for (int r = 0; r < PB; ++r) {
-                    if (r0 + r < k) {
-                        const float s = wave_sum_dpp(dot[r]);
-                        if ((threadIdx.x & 63) == 63) part[g][wv][r0 + r] = s;
-                    }
+                for (int r = 0; r < PB; ++r) dot[r] = wave_sum_dpp(dot[r]);   // side by side; zeros behind the k-th
+                if ((threadIdx.x & 63) == 63) {
+#pragma unroll
+                    for (int r = 0; r < PB; ++r) part[g][wv][r0 + r] = dot[r];
                 }
             }
         }
     }
     if (!dots) return;
     __syncthreads();
-    const int th = threadIdx.x % G;
-    if (live && th < 32) {   // lane r of the group's first wave: pick r
+    if (live && th < 32) {
         float s = 0.f;
         if (th < k) {
 #pragma unroll
@@ -189,9 +195,7 @@ __global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__
             if (dw) dw[(int64_t)t * k + th] = s;
         }
         if (dz) {
-            const float wr = th < k ? w[(int64_t)t * k + th] : 0.f;
-            const int p = th < k ? pos[(int64_t)t * k + th] : -1;
-            float q = (uint32_t)p < (uint32_t)rows ? wr * s : 0.f;   // a skipped pick's weight enters no sum
+            float q = (uint32_t)pr < (uint32_t)rows ? wr * s : 0.f;   // a skipped pick's weight enters no sum
             q += __shfl_xor(q, 16, 32);
             q += __shfl_xor(q, 8, 32);
             q += __shfl_xor(q, 4, 32);
