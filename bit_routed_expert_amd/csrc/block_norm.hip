@@ -82,8 +82,15 @@ NormArgs norm_args(const strata_block_norm_args *p) {
     return a;
 }
 
-int back_blocks(const strata_block_norm_args *p) {
-    const int64_t rows = wave_rows(p->d) ? ((int64_t)p->T + 3) / 4 : p->T;
+// Blocks of the gradient.  With gains' gradients asked for, one block takes up
+// to two trips of rows by itself and leaves the sums where they belong: the
+// second launch and its wait cost more than the second trip (2048 columns, 1
+// row: 5.6 -> 3.4 us, 2 rows: 5.7 -> 4.8, 4096 columns, 2 rows: 7.1 -> 6.7) but
+// for the longest rows (8192 columns, 2 rows: 10.1 -> 11.4 us, so one trip).
+int back_blocks(const strata_block_norm_args *p, bool gains) {
+    const int group = wave_rows(p->d) ? 4 : 1;
+    if (gains && p->T > 0 && p->T <= (p->d <= 4096 ? 2 : 1) * group) return 1;
+    const int64_t rows = ((int64_t)p->T + group - 1) / group;
     return (int)(rows < BN_BLOCKS ? rows : BN_BLOCKS);
 }
 
@@ -139,7 +146,7 @@ strata_status strata_block_norm(const strata_block_norm_args *args, const void *
 
 size_t strata_block_norm_backward_workspace_bytes(const strata_block_norm_args *args) {
     if (check_norm(args) != STRATA_OK) return 0;
-    const size_t n = (size_t)2 * back_blocks(args) * args->d * 4;
+    const size_t n = (size_t)2 * back_blocks(args, true) * args->d * 4;
     return n ? n : 256;
 }
 
@@ -181,15 +188,16 @@ strata_status strata_block_norm_backward(const strata_block_norm_args *args, con
     a.dgate = dgate;
     a.dg_post = dg_post;
     a.dg_pre = dg_pre;
-    a.blocks = back_blocks(args);
-    a.part_post = (float *)ws;
-    a.part_pre = (float *)ws + (size_t)a.blocks * a.d;
+    a.blocks = back_blocks(args, gains);
+    const bool alone = a.blocks == 1 && rows;
+    a.part_post = alone ? dg_post : (float *)ws;
+    a.part_pre = alone ? dg_pre : (float *)ws + (size_t)a.blocks * a.d;
     const hipStream_t s = (hipStream_t)stream;
     if (rows && (dx || dy || dgate || gains)) {
         const hipError_t e = launch_norm(a, true, s);
         if (e != hipSuccess) return hip_status(e);
     }
-    if (gains) {   // no rows: no partial sums, zeros
+    if (gains && !alone) {   // no rows: no partial sums, zeros
         STRATA_LAUNCH(block_norm_gains_kernel, dim3((a.d + 31) / 32, 2), dim3(1024), 0, s, a);
         return hip_status(hipGetLastError());
     }

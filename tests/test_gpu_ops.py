@@ -461,7 +461,11 @@ NORMS = [  # T, d, x, y, u types, post, pre, gate, sigmoid
     (2, 4097, BF, BF, BF, True, True, "channel", True), (2, 8192, F32, F32, BF, True, True, "channel", True),
     (2, 8191, F32, F32, F32, True, True, "token", False), (6, 256, F32, None, BF, False, True, None, False),
     (1100, 136, BF, BF, BF, True, True, "channel", True), (4500, 64, F32, F32, F32, True, True, "token", True),
-    (1500, 1160, BF, BF, F32, True, True, "token", False)]
+    (1500, 1160, BF, BF, F32, True, True, "token", False),
+    # around the rows that one block takes alone, gains' gradients and all
+    (8, 512, F32, BF, BF, True, True, "channel", False), (9, 520, BF, BF, F32, True, True, "token", True),
+    (8, 1024, BF, F32, BF, True, True, None, False), (2, 2048, F32, BF, BF, True, True, "token", False),
+    (1, 8192, BF, BF, BF, True, True, None, False), (3, 4096, BF, BF, BF, True, False, "channel", True)]
 
 
 def norm_case(T, d, xt, yt, ut, post, pre, gate, sig, seed=1):
