@@ -214,32 +214,40 @@ template <int BM, int BN, int WM, int WN, int ST, int TB> strata_status launch_r
     const int Nn = TB ? a.K : a.N;
     a.tile_rows = BM;
     const int64_t blocks = (max_tiles(a.rows, a.E, BM) * ((Nn + BN - 1) / BN) + 7) / 8 * 8;
-    if (blocks <= GP_FIND_BLOCKS) {
-        STRATA_LAUNCH((grouped_rows_kernel<BM, BN, WM, WN, ST, TB, 0>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
-        return hip_status(hipGetLastError());
+    if constexpr (BM != 64) {   // 64-row tiles are for small grids
+        if (blocks > GP_FIND_BLOCKS) {
+            STRATA_LAUNCH(grouped_plan_kernel, dim3(1), dim3(1024), 0, s, a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return hip_status(e);
+            STRATA_LAUNCH((grouped_rows_kernel<BM, BN, WM, WN, ST, TB, 1>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
+            return hip_status(hipGetLastError());
+        }
     }
-    STRATA_LAUNCH(grouped_plan_kernel, dim3(1), dim3(1024), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return hip_status(e);
-    STRATA_LAUNCH((grouped_rows_kernel<BM, BN, WM, WN, ST, TB, 1>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
+    STRATA_LAUNCH((grouped_rows_kernel<BM, BN, WM, WN, ST, TB, 0>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
     return hip_status(hipGetLastError());
 }
 
-// Tile by the average rows of an expert (1536 x 2048 unless said).  Up to 16,
-// 32-row tiles: the weights bound it and more, smaller blocks keep more of
-// them in flight (E = 16, 16 rows each: 18 us against 19 us for 128-row tiles;
-// E = 512, 2 rows: 521 against 537); the same where fewer than 64 of the next
-// tiles exist (4 experts of 64 rows: 12 against 18 us; 8 of 256 rows, 512 x
-// 512: 7.5 against 10).  Then 128 x 256 with three buffers (E = 512, 64 rows:
-// 620 us, 5.6 TB/s, against 734 with 32 rows and 676 with 256).  From 384 rows
-// on, and with tiles enough for the 256 CUs, 256 x 256, whose operands are read
-// half as often (E = 16, 4096 rows: 362 against 398 us, 512 rows: 56 against
-// 65; with 256 rows 46 against 30 us).
+// Tile by the rows an expert has on average, and by how many tiles there are
+// (1536 x 2048 unless said).  Up to 16 rows, 32-row tiles: the weights bound it
+// and more, smaller blocks keep more of them in flight (E = 16, 16 rows each:
+// 18 us against 19 us for 128-row tiles; E = 512, 2 rows: 521 against 537);
+// the same where 64 x 128 tiles would be fewer than 128 (4 experts of 64 rows:
+// 12 against 18 us; 8 of 64 rows, 512 x 512: 5.7 against 6.5 with 64 rows).
+// 64 x 128 where those are no more than the CUs, uneven experts counted with
+// half a tile each (7 experts, 4011 rows, 264 x 624: 7.8 us against 11 with
+// 32 and 128 rows; 16 of 64 rows, 1024 x 1024: 9.6 against 10 and 12; where
+// they are twice the CUs, 8 of 1024 rows, 512 x 512: 16 against 12 with 128).
+// Then 128 x 256 with three buffers (E = 512, 64 rows: 620 us, 5.6 TB/s,
+// against 734 with 32 rows and 676 with 256).  From 384 rows on, and with
+// tiles enough for the 256 CUs, 256 x 256, whose operands are read half as
+// often (E = 16, 4096 rows: 362 against 398 us, 512 rows: 56 against 65; with
+// 256 rows 46 against 30 us).
 template <int TB> strata_status grouped_rows(GroupArgs &a, hipStream_t s) {
     const int64_t rows = a.rows, E = a.E;
     const int Nn = TB ? a.K : a.N;
-    if (rows <= 16 * E || (rows / 128 + E) * ((Nn + 255) / 256) < 64)
-        return launch_rows<GP_MIN_ROWS, 128, 1, 4, 4, TB>(a, s);
+    const int64_t tiles64 = (rows / 64 + (E + 1) / 2) * ((Nn + 127) / 128);
+    if (rows <= 16 * E || tiles64 < 128) return launch_rows<GP_MIN_ROWS, 128, 1, 4, 4, TB>(a, s);
+    if (tiles64 <= 256) return launch_rows<64, 128, 2, 2, 4, TB>(a, s);
     if (rows < 384 * E || rows / 256 * ((Nn + 255) / 256) < 192) return launch_rows<128, 256, 2, 4, 3, TB>(a, s);
     return launch_rows<256, 256, 2, 4, 2, TB>(a, s);
 }

@@ -11,7 +11,7 @@
 // Rows are read and written with the streaming hint: each once, and a prompt
 // chunk's slots (168 MB) are most of what the caches hold.  4096 tokens of
 // 2048 bf16, 10 picks of 512 experts: combine 35.7 -> 31.2 us (5.7 TB/s),
-// its gradient 75.5 -> 71.5 us (4.9 TB/s), dispatch 33.5 -> 31.1 us (5.9
+// its gradient 75.5 -> 70 us (5.0 TB/s), dispatch 33.5 -> 31.1 us (5.9
 // TB/s); with the experts' product right behind, within 1% either way.
 #include "ops.hpp"
 

@@ -281,6 +281,8 @@ def test_grouped_products(ns, N, K, tail, ot):
 LENGTHS = [   # rows per expert, N, K, what is run: contractions of 1 to 13 whole and ragged steps in every tile
     *[([7, 0, 50], 136, 64 * n + r, "product") for n in range(1, 10) for r in (0, -8)],                 # 32-row tiles
     *[([7, 0, 50], 64 * n + r, 136, "dgrad") for n in range(1, 10) for r in (0, -8)],
+    *[([300, 200, 7, 0, 260], 1224, 64 * n + r, "product") for n in range(1, 10) for r in (0, -8)],     # 64-row tiles
+    *[([300, 200, 7, 0, 260], 64 * n + r, 1224, "dgrad") for n in range(1, 10) for r in (0, -8)],
     *[([120] * 40, 520, 64 * n + r, "product") for n in range(1, 8) for r in (0, 8)],                   # 128-row tiles
     *[([120] * 40, 64 * n + r, 520, "dgrad") for n in range(1, 8) for r in (0, 8)],
     *[([25000, 24200], 256, 64 * n + r, "product") for n in range(1, 6) for r in (0, -56)],             # 256-row tiles
