@@ -587,6 +587,33 @@ def test_block_norm_backward(case):
         R.check(out["dgate"].guarded(), grads["gate"], c * (m if gate == "channel" else m.sum(1)), "dgate")
 
 
+@pytest.mark.parametrize("gate,yt", [("token", F32), ("token", BF), ("channel", F32), ("channel", BF)])
+@pytest.mark.parametrize("d", [65, 130, 264, 1032, 2056, 4104])
+def test_block_norm_gradient_of_sigmoid_gates_far_from_zero(d, gate, yt):
+    """The gate's own gradient b D n s (1 - s), s = sigmoid(v), to its own
+    magnitude: 1 - s is not taken from an s that has rounded to 1.  Bounds: the
+    exponential is off by 2|v| + 2 steps (its argument by two roundings of v
+    log2 e, the instruction by two), so s (1 - s) by no more than 4|v| + 10; b D n
+    adds 3, a token's sum d."""
+    print(f"case sigmoid gates d={d} {gate} {yt}", flush=True)
+    vals = torch.tensor([0.0, 1.0, 4.0, 8.0, 10.0, 12.0, 15.0, 16.5, 17.0, 17.5, 20.0, 30.0, 60.0, 80.0, 100.0, 1000.0])
+    vals = torch.cat([vals, -vals])
+    T = 37
+    v = vals[torch.arange(T) % 32] if gate == "token" else vals[(torch.arange(T)[:, None] * 5 + torch.arange(d)) % 32].to(yt)
+    y, dr = rand(T, d, seed=1, dtype=yt), rand(T, d, seed=2)
+    a = brx.block_norm_args(T, d, CODE[F32], CODE[yt], CODE[F32],
+                            brx.GATE_SIGMOID | (brx.GATE_TOKEN if gate == "token" else brx.GATE_CHANNEL), 1.0, -1.25)
+    dg = Out(T, dtype=F32) if gate == "token" else Out(T, d, dtype=yt)
+    brx.block_norm_backward(a, dr.cuda(), None, None, y.cuda(), gate=v.cuda(), dgate=dg.t)
+    terms, vd = -1.25 * dr.double() * y.double(), v.double()
+    mag = terms.abs()
+    if gate == "token":
+        terms, mag = terms.sum(1), mag.sum(1)
+    der = torch.sigmoid(vd) * torch.sigmoid(-vd)
+    steps = 4 * vd.abs() + 16 + (d if gate == "token" else 0)
+    R.check(dg.guarded(), terms * der, steps * U * mag * der, "dgate")
+
+
 def test_block_norm_in_place_and_outputs_apart():
     T, d = 40, 768
     a, t = norm_case(T, d, F32, BF, BF, True, True, "channel", True)
