@@ -12,6 +12,10 @@ constexpr int32_t MAX_COLS = 1 << 24;   // longest row of dispatch and combine
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool bad_dtype(int32_t t) { return t != STRATA_X_BF16 && t != STRATA_X_F32; }
+// Two buffers of a and b bytes that share memory (null or empty: none does).
+inline bool overlap(const void *p, size_t a, const void *q, size_t b) {
+    return p && q && a && b && (uintptr_t)p < (uintptr_t)q + b && (uintptr_t)q < (uintptr_t)p + a;
+}
 // A required row pointer: there and aligned.
 inline bool bad_rows(const void *p) { return !p || !aligned16(p); }
 

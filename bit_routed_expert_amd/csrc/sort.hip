@@ -250,6 +250,17 @@ strata_status strata_moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t 
     if ((int64_t)T * k > INT32_MAX) return STRATA_EUNSUPPORTED;
     if (T > 0 && (!idx || !ws || !aligned16(ws))) return STRATA_EINVAL;
     if (T > 0 && ws_bytes < strata_moe_sort_workspace_bytes(T, k, n_experts)) return STRATA_EWORKSPACE;
+    // Blocks read the picks (and, in two launches, each other's counts) while others write: slots from counts that
+    // changed in between could lie outside perm.
+    const size_t n = (size_t)T * k * 4;
+    const size_t used = (int64_t)T * k > SORT_ONCE ? strata_moe_sort_workspace_bytes(T, k, n_experts) : 0;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } outs[] = {{counts, (size_t)n_experts * 4}, {offsets, (size_t)(n_experts + 1) * 4}, {perm, n}, {pos, n}};
+    for (const auto &o : outs)
+        if (overlap(o.p, o.bytes, idx, n) || overlap(o.p, o.bytes, ws, used)) return STRATA_EINVAL;
+    if (overlap(ws, used, idx, n)) return STRATA_EINVAL;
     SortArgs a{};
     a.idx = idx;
     a.counts = counts;

@@ -49,7 +49,8 @@ size_t strata_moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t n_experts);
 /* counts [E], offsets [E+1] (exclusive prefix sum; offsets[E] = kept picks),
  * perm [T*k], pos [T*k]: [dev] int32, each nullable.  idx: [dev] [T][k].
  * T = 0 writes zero counts and offsets.  EINVAL: a null idx or workspace with
- * T > 0, T < 0, k outside 1..32, E outside 1..1024, a misaligned workspace;
+ * T > 0, T < 0, k outside 1..32, E outside 1..1024, a misaligned workspace, an
+ * output that shares memory with idx, or with the workspace above 65535 picks;
  * EUNSUPPORTED: T*k > 2^31 - 1; EWORKSPACE; EHIP. */
 strata_status strata_moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t n_experts, int32_t *counts,
                               int32_t *offsets, int32_t *perm, int32_t *pos, void *ws, size_t ws_bytes, void *stream);

@@ -36,6 +36,26 @@ def test_sort_refusals():
     assert call(T=2**31 - 1, k=2, wb=1 << 40) == EUNSUP and ws(2**31 - 1, 2, 512) == 0
 
 
+def test_sort_refuses_outputs_over_its_inputs():
+    """Blocks read all the picks while others already write, so no output may
+    lie over idx; nor over the workspace where it carries counts between launches."""
+    f, wsb = lib().strata_moe_sort, lib().strata_moe_sort_workspace_bytes
+    G = 1 << 30   # apart
+
+    def call(T, k=10, E=512, idx=G, counts=2 * G, offsets=3 * G, perm=4 * G, pos=5 * G, w=6 * G):
+        return f(idx, T, k, E, counts, offsets, perm, pos, w, wsb(T, k, E), None)
+    for T in (5, 400, 50000):
+        n, need = T * 10 * 4, wsb(T, 10, 512)
+        for name, size in (("counts", 512 * 4), ("offsets", 513 * 4), ("perm", n), ("pos", n)):
+            for at in (G, G + n - 4, G - size + 4):
+                assert call(T, **{name: at}) == EINVAL, (T, name, at - G)
+            if n > 65535 * 4:
+                for at in (6 * G, 6 * G + need - 4, 6 * G - size + 4):
+                    assert call(T, **{name: at}) == EINVAL, (T, name, at - 6 * G)
+        if n > 65535 * 4:
+            assert call(T, w=G) == EINVAL and call(T, w=G + n - 16) == EINVAL and call(T, idx=6 * G + need - 4) == EINVAL
+
+
 def test_dispatch_and_combine_refusals():
     d, db, c, cb = (lib().strata_moe_dispatch, lib().strata_moe_dispatch_backward, lib().strata_moe_combine,
                     lib().strata_moe_combine_backward)
