@@ -185,12 +185,16 @@ strata_status check_grouped(int32_t rows, int32_t E, int32_t N, int32_t K) {
 }
 
 strata_status grouped_call(const void *A, const void *B, const int32_t *offsets, int32_t rows, int32_t E, int32_t N,
-                           int32_t K, void *C, strata_xdtype dtype, void *ws, size_t ws_bytes, GroupArgs &a) {
+                           int32_t K, void *C, int64_t c_values, strata_xdtype dtype, void *ws, size_t ws_bytes,
+                           GroupArgs &a) {
     if (bad_dtype(dtype)) return STRATA_EINVAL;
     const strata_status st = check_grouped(rows, E, N, K);
     if (st != STRATA_OK) return st;
     if (bad_rows(A) || bad_rows(B) || bad_rows(C) || bad_rows(ws) || !offsets) return STRATA_EINVAL;
-    if (ws_bytes < strata_moe_grouped_workspace_bytes(rows, E, N, K)) return STRATA_EWORKSPACE;
+    const size_t need = strata_moe_grouped_workspace_bytes(rows, E, N, K);
+    if (ws_bytes < need) return STRATA_EWORKSPACE;
+    // Blocks take their rows from the list in the workspace while others already store.
+    if (overlap(C, (size_t)c_values * (dtype == STRATA_X_BF16 ? 2 : 4), ws, need)) return STRATA_EINVAL;
     a.A = (const uint16_t *)A;
     a.B = (const uint16_t *)B;
     a.C = C;
@@ -299,7 +303,7 @@ strata_status strata_moe_grouped_product(const void *x, const void *W, const int
     GroupArgs a{};
     const strata_status st =
         rows == 0 ? check_grouped(rows, n_experts, N, K)
-                  : grouped_call(x, W, offsets, rows, n_experts, N, K, y, ydtype, ws, ws_bytes, a);
+                  : grouped_call(x, W, offsets, rows, n_experts, N, K, y, (int64_t)rows * N, ydtype, ws, ws_bytes, a);
     if (st != STRATA_OK || rows == 0) return st;
     if (few_rows_path(rows, n_experts, K)) {
         const int slabs = (N + GV_N - 1) / GV_N;
@@ -316,7 +320,7 @@ strata_status strata_moe_grouped_dgrad(const void *dy, const void *W, const int3
     GroupArgs a{};
     const strata_status st =
         rows == 0 ? check_grouped(rows, n_experts, N, K)
-                  : grouped_call(dy, W, offsets, rows, n_experts, N, K, dx, xdtype, ws, ws_bytes, a);
+                  : grouped_call(dy, W, offsets, rows, n_experts, N, K, dx, (int64_t)rows * K, xdtype, ws, ws_bytes, a);
     if (st != STRATA_OK || rows == 0) return st;
     return grouped_rows<1>(a, (hipStream_t)stream);
 }
@@ -327,8 +331,8 @@ strata_status strata_moe_grouped_wgrad(const void *dy, const void *x, const int3
     GroupArgs a{};
     // without rows dy and x may be null: dW stands in for them and is not read
     const bool none = rows == 0;
-    const strata_status st = grouped_call(none ? dW : dy, none ? dW : x, offsets, rows, n_experts, N, K, dW, wdtype,
-                                          ws, ws_bytes, a);
+    const strata_status st = grouped_call(none ? dW : dy, none ? dW : x, offsets, rows, n_experts, N, K, dW,
+                                          (int64_t)n_experts * N * K, wdtype, ws, ws_bytes, a);
     if (st != STRATA_OK) return st;
     return grouped_weights(a, (hipStream_t)stream);
 }

@@ -103,7 +103,8 @@ strata_status strata_moe_combine_backward(const void *dout, strata_xdtype odtype
  * summed in fp32.
  * Limits: N % 8 == 0, K % 8 == 0, 8 <= N, K <= 65536, N*K <= 2^29, 1 <= E <=
  * 1024, E*N*K <= 2^37, rows <= 2^22, else EUNSUPPORTED.  EINVAL: a null or
- * misaligned pointer, rows < 0, a bad dtype; EWORKSPACE; EHIP.  Rows behind
+ * misaligned pointer, rows < 0, a bad dtype, an output that shares memory with
+ * the workspace; EWORKSPACE; EHIP.  Rows behind
  * the last expert's are not read and their outputs are left as they were.
  */
 

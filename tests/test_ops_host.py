@@ -97,6 +97,19 @@ def test_grouped_refusals(name):
         assert call(rows=0, a=None, b=None, off=None, c=None, w=None) == OK
 
 
+@pytest.mark.parametrize("name", ["product", "dgrad", "wgrad"])
+def test_grouped_refuses_an_output_over_its_workspace(name):
+    """Blocks take their rows from a list in the workspace while others already store."""
+    f, G, rows, E, N, K = getattr(lib(), f"strata_moe_grouped_{name}"), 1 << 30, 1683, 40, 1288, 264
+    need = lib().strata_moe_grouped_workspace_bytes(rows, E, N, K)
+    for t, step in ((0, 2), (1, 4)):
+        size = step * {"product": rows * N, "dgrad": rows * K, "wgrad": E * N * K}[name]
+        for c in (5 * G, 5 * G + need // 16 * 16, 5 * G - size // 16 * 16 + 16):
+            if not 5 * G - size < c < 5 * G + need:
+                continue
+            assert f(G, 2 * G, 3 * G, rows, E, N, K, c, t, 5 * G, need, None) == EINVAL, (t, c - 5 * G)
+
+
 def _args(**kw):
     a = dict(T=5, d=64, x_dtype=1, y_dtype=0, u_dtype=0, flags=brx.POST_NORM | brx.PRE_NORM)
     a.update(kw)
