@@ -184,6 +184,11 @@ strata_status check_grouped(int32_t rows, int32_t E, int32_t N, int32_t K) {
     return STRATA_OK;
 }
 
+// A call without rows: nothing to do, whatever the pointers are.
+strata_status check_no_rows(int32_t E, int32_t N, int32_t K, strata_xdtype dtype) {
+    return bad_dtype(dtype) ? STRATA_EINVAL : check_grouped(0, E, N, K);
+}
+
 strata_status grouped_call(const void *A, const void *B, const int32_t *offsets, int32_t rows, int32_t E, int32_t N,
                            int32_t K, void *C, int64_t c_values, strata_xdtype dtype, void *ws, size_t ws_bytes,
                            GroupArgs &a) {
@@ -302,7 +307,7 @@ strata_status strata_moe_grouped_product(const void *x, const void *W, const int
                                          void *ws, size_t ws_bytes, void *stream) {
     GroupArgs a{};
     const strata_status st =
-        rows == 0 ? check_grouped(rows, n_experts, N, K)
+        rows == 0 ? check_no_rows(n_experts, N, K, ydtype)
                   : grouped_call(x, W, offsets, rows, n_experts, N, K, y, (int64_t)rows * N, ydtype, ws, ws_bytes, a);
     if (st != STRATA_OK || rows == 0) return st;
     if (few_rows_path(rows, n_experts, K)) {
@@ -319,7 +324,7 @@ strata_status strata_moe_grouped_dgrad(const void *dy, const void *W, const int3
                                        void *ws, size_t ws_bytes, void *stream) {
     GroupArgs a{};
     const strata_status st =
-        rows == 0 ? check_grouped(rows, n_experts, N, K)
+        rows == 0 ? check_no_rows(n_experts, N, K, xdtype)
                   : grouped_call(dy, W, offsets, rows, n_experts, N, K, dx, (int64_t)rows * K, xdtype, ws, ws_bytes, a);
     if (st != STRATA_OK || rows == 0) return st;
     return grouped_rows<1>(a, (hipStream_t)stream);

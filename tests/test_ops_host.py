@@ -110,6 +110,15 @@ def test_grouped_refuses_an_output_over_its_workspace(name):
             assert f(G, 2 * G, 3 * G, rows, E, N, K, c, t, 5 * G, need, None) == EINVAL, (t, c - 5 * G)
 
 
+@pytest.mark.parametrize("name", ["product", "dgrad"])
+def test_grouped_without_rows_checks_the_rest(name):
+    """A call without rows does nothing whatever its pointers are, but a bad dtype or shape stays an error."""
+    f = getattr(lib(), f"strata_moe_grouped_{name}")
+    for t, E, N, want in ((0, 8, 64, OK), (1, 8, 64, OK), (2, 8, 64, EINVAL), (-1, 8, 64, EINVAL), (0, 0, 64, EUNSUP),
+                          (1, 8, 60, EUNSUP)):
+        assert f(None, None, None, 0, E, N, 128, None, t, None, 0, None) == want, (t, E, N)
+
+
 def _args(**kw):
     a = dict(T=5, d=64, x_dtype=1, y_dtype=0, u_dtype=0, flags=brx.POST_NORM | brx.PRE_NORM)
     a.update(kw)
