@@ -4,6 +4,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import os
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -66,7 +67,7 @@ def _compile_binding() -> str:
     import sysconfig
     try:
         import torch
-    except ImportError:   # the operators' binding is for torch's tensors
+    except (ImportError, OSError):   # the operators' binding is for torch's tensors
         return ""
     base = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
@@ -83,7 +84,12 @@ def _compile_binding() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source (always), link the shared library and the binding's module."""
+    """Compile every source (always), link the shared library and the binding's module.
+
+    The library needs neither Python's headers nor torch's: where the module
+    does not compile against them the library is built all the same, with a
+    warning, and the operators say so when they are called from Python.
+    """
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
         futs = [ex.submit(_compile, src) for src in SOURCES]
@@ -91,13 +97,16 @@ def build(verbose: bool = False) -> str:
         futs.append(ex.submit(_compile_host_common))
         binding = ex.submit(_compile_binding)
         objs = [f.result() for f in futs]
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if binding.exception() is not None:
+        if os.path.exists(BINDING):   # of an earlier build: its calls need not fit this library
+            os.remove(BINDING)
+        warnings.warn(f"the operators cannot be called from Python: {binding.exception()}", RuntimeWarning)
     if verbose:
         print("built", LIB)
     return LIB
