@@ -12,11 +12,6 @@ from __future__ import annotations
 
 import ctypes
 
-try:
-    import torch
-except ImportError:  # pragma: no cover -- the rest of the package imports without it
-    torch = None
-
 POST_NORM, PRE_NORM, GATE_TOKEN, GATE_CHANNEL, GATE_SIGMOID = 1, 2, 4, 8, 16
 
 _EINVAL = 1
@@ -67,6 +62,7 @@ def _raise(what):
 
 def _elsewhere(dev: int, fn, *args):
     """fn(*args) with device dev current."""
+    import torch
     with torch.cuda.device(dev):
         fn(*args)
 
@@ -87,13 +83,12 @@ class _Unloaded:
 
     def __getattr__(self, name):
         global _native
-        if torch is None:  # pragma: no cover
-            raise RuntimeError("the operators' binding needs torch")
         lib = _lib()
         try:
+            import torch   # here and not above: the package is imported without it, and sooner
             from . import _binding
         except ImportError as e:
-            raise RuntimeError("_binding.so is missing or was built against another torch: build it with "
+            raise RuntimeError("the operators need torch and a _binding.so built against it: build it with "
                                "`python -m bit_routed_expert_amd.build`") from e
         fns = tuple(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in _BOUND)
         # torch's direct accessors where it has them: a Stream object costs as much host time as the launch

@@ -4,6 +4,8 @@ reference's gradients against differences."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
 import sys
 
 import pytest
@@ -259,6 +261,22 @@ def test_binding_keeps_no_references():
     with pytest.raises(brx.StrataError):
         brx.block_norm(bytearray(8), P, P)
     assert (sys.getrefcount(t), sys.getrefcount(args)) == count
+
+
+def test_the_package_imports_without_torch():
+    """Shapes, the build and the host's entry points need no torch: the import neither loads it nor fails with it."""
+    code = ("import sys, importlib.abc\n"
+            "class No(importlib.abc.MetaPathFinder):\n"
+            "    def find_spec(self, name, path=None, target=None):\n"
+            "        if name.split('.')[0] == 'torch':\n"
+            "            raise OSError('a torch whose libraries do not load')\n"
+            "sys.meta_path.insert(0, No())\n"
+            "import bit_routed_expert_amd as brx, bit_routed_expert_amd.build\n"
+            "assert 'torch' not in sys.modules and brx.shape(8, 2, 64, 64, 3).n_experts == 8\n"
+            "assert brx.block_norm_args(1, 8, 0, 0, 0, 0).d == 8\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
 
 
 def _leaf(*shape, seed):
