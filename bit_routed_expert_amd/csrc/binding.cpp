@@ -142,7 +142,7 @@ struct Call {
         }
         PyObject *s = a[n - 1], *own = nullptr;
         if (s == Py_None) own = s = PyObject_CallOneArg(g_stream, d);
-        else if (!PyLong_Check(s)) own = s = PyObject_GetAttrString(s, "cuda_stream");
+        else if (!PyLong_Check(s)) own = s = stream_on(s, current);
         Py_DECREF(d);
         if (!s) return nullptr;
         void *stream = (void *)(uintptr_t)PyLong_AsUnsignedLongLong(s);
@@ -158,6 +158,23 @@ struct Call {
         PyObject *r = PyObject_CallOneArg(g_raise, c);
         Py_DECREF(c);
         return r;
+    }
+    // A stream object's address; one of another device would run the kernels there, on memory of this one.
+    PyObject *stream_on(PyObject *s, long long current) {
+        PyObject *d = PyObject_GetAttrString(s, "device_index");
+        if (!d) {
+            if (!PyErr_ExceptionMatches(PyExc_AttributeError)) return nullptr;
+            PyErr_Clear();   // not torch's: its address is all there is to know
+        } else {
+            const long long on = PyLong_AsLongLong(d);
+            Py_DECREF(d);
+            if (PyErr_Occurred()) return nullptr;
+            if (on != current) {
+                bad("stream is on device %lld, not %lld", on, current);
+                return nullptr;
+            }
+        }
+        return PyObject_GetAttrString(s, "cuda_stream");
     }
     // The same call once more with the tensors' device current.
     PyObject *elsewhere() {

@@ -3,9 +3,9 @@
 Tensors are checked before a call (device, type, contiguity, element count)
 and a mismatch raises StrataError with STRATA_EINVAL; everything else is
 checked by the library.  A call runs on the current stream of its tensors'
-device unless one is given, with that device current.  Raw device addresses
-(ints) are passed on unchecked, beside tensors or alone (then on the current
-device).  The checks are compiled (csrc/binding.cpp, the module _binding): a
+device unless one is given, with that device current; a stream of another
+device is refused.  Raw device addresses (ints) are passed on unchecked, beside
+tensors or alone (then on the current device), and so is a raw stream.  The checks are compiled (csrc/binding.cpp, the module _binding): a
 small call's time is the host's.
 """
 from __future__ import annotations

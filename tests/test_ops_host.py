@@ -263,6 +263,34 @@ def test_binding_keeps_no_references():
     assert (sys.getrefcount(t), sys.getrefcount(args)) == count
 
 
+def test_binding_takes_no_stream_of_another_device():
+    """Kernels would run on the stream's device, on memory of the tensors'.  The addresses are misaligned, so that
+    the library refuses what the binding lets pass."""
+    class Stream:
+        def __init__(self, device_index, cuda_stream=0):
+            self.device_index, self.cuda_stream = device_index, cuda_stream
+
+    class Plain:
+        cuda_stream = 0
+    native, library = brx.ops._native, lib()
+    if isinstance(native, brx.ops._Unloaded):
+        native.bind   # loads the module
+        native = brx.ops._native
+    try:
+        native.bind(tuple(ctypes.cast(getattr(library, f), ctypes.c_void_p).value for f in brx.ops._BOUND), brx.ops._raise,
+                    brx.ops._elsewhere, lambda: 2, lambda: 2, lambda dev: 0)
+        for stream, refused in ((Stream(1), True), (Stream(2), False), (Plain(), False), (0, False), (None, False)):
+            with pytest.raises(brx.StrataError) as e:
+                brx.dispatch(P + 8, 1, 5, 4, 64, P + 8, P + 8, 20, stream=stream)
+            assert e.value.status == EINVAL and ("stream is on device 1, not 2" in str(e.value)) == refused, stream
+        with pytest.raises(AttributeError):
+            brx.dispatch(P + 8, 1, 5, 4, 64, P + 8, P + 8, 20, stream=object())
+        with pytest.raises(TypeError):
+            brx.dispatch(P + 8, 1, 5, 4, 64, P + 8, P + 8, 20, stream=Stream("one"))
+    finally:
+        brx.ops._native = brx.ops._Unloaded()   # bound anew at the next call
+
+
 def test_the_package_imports_without_torch():
     """Shapes, the build and the host's entry points need no torch: the import neither loads it nor fails with it."""
     code = ("import sys, importlib.abc\n"
