@@ -107,16 +107,17 @@ template <int G> __device__ __forceinline__ float group_sum(float v, float *red)
 }
 
 // The gate as it multiplies the branch (g) and the derivative of that (dg).
-// Of the sigmoid, with e = exp(-v): g = 1 / (1 + e), g' = g (1 - g) = e g^2.
-// For v > 0 1 - g has lost its digits to g's rounding (0 from 17 on), for v < 0
-// e may be past the largest number: each form where it is exact to a few steps.
+// Of the sigmoid, with e = exp(-v): g = 1 / (1 + e), and g' = g (1 - g) as e g^2,
+// since for v > 0 the digits of 1 - g are lost to g's rounding (all from 17 on).
+// Below -87, where g is next to the smallest number, e is held at 2^126 so that
+// the product stays finite.
 __device__ __forceinline__ void gate_value(float v, bool sigmoid, float &g, float &dg) {
     g = v;
     dg = 1.f;
     if (sigmoid) {
         const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * v);
         g = 1.f / (1.f + e);
-        dg = g * (v > 0.f ? e * g : 1.f - g);
+        dg = fminf(e, 0x1p126f) * g * g;
     }
 }
 

@@ -614,6 +614,26 @@ def test_block_norm_gradient_of_sigmoid_gates_far_from_zero(d, gate, yt):
     R.check(dg.guarded(), terms * der, steps * U * mag * der, "dgate")
 
 
+@pytest.mark.parametrize("gate", ["token", "channel"])
+def test_block_norm_sigmoid_gates_at_infinity(gate):
+    """Gates of either infinity are 1 and 0 and have no gradient; one of NaN stays in its row."""
+    T, d = 4, 264
+    v = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0])
+    v = v if gate == "token" else v[:, None].expand(T, d).contiguous()
+    x, y, dr = rand(T, d, seed=1), rand(T, d, seed=2), rand(T, d, seed=3)
+    a = brx.block_norm_args(T, d, 1, 1, 1, brx.GATE_SIGMOID | (brx.GATE_TOKEN if gate == "token" else brx.GATE_CHANNEL))
+    r, dy, dg = Out(T, d, dtype=F32), Out(T, d, dtype=F32), Out(*v.shape, dtype=F32)
+    brx.block_norm(a, x.cuda(), y.cuda(), gate=v.cuda(), r=r.t)
+    brx.block_norm_backward(a, dr.cuda(), None, None, y.cuda(), gate=v.cuda(), dy=dy.t, dgate=dg.t)
+    got = r.guarded().cpu()
+    assert torch.equal(got[0], x[0] + y[0]) and torch.equal(got[1], x[1]) and bool(got[2].isnan().all())
+    assert torch.equal(got[3], torch.add(x[3], y[3], alpha=0.5))
+    got = dy.guarded().cpu()
+    assert torch.equal(got[0], dr[0]) and bool((got[1] == 0).all()) and torch.equal(got[3], 0.5 * dr[3])
+    got = dg.guarded().cpu()
+    assert bool((got[:2] == 0).all()) and bool(got[2].isnan().all()) and bool(got[3].isfinite().all())
+
+
 def test_block_norm_in_place_and_outputs_apart():
     T, d = 40, 768
     a, t = norm_case(T, d, F32, BF, BF, True, True, "channel", True)
