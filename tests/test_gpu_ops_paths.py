@@ -276,6 +276,27 @@ def test_the_same_on_another_stream(name):
     assert T.same(T.bits(outs), want)
 
 
+@pytest.mark.parametrize("name", CALLS)
+def test_two_at_once(name):
+    """Two calls under way together on two streams, each with its own workspace and outputs."""
+    print(f"case two at once {name}", flush=True)
+    pair = [CALLS[name](s) for s in (5, 77)]
+    want = [eager(run, outs) for run, _, outs in pair]
+    for _, _, outs in pair:
+        for o in outs:
+            o.zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for st, (run, _, _) in zip(streams, pair):
+            with torch.cuda.stream(st):
+                run()
+    torch.cuda.synchronize()
+    for (_, _, outs), w in zip(pair, want):
+        assert T.same(T.bits(outs), w)
+
+
 # --------------------------------- norms of every width, more rows than blocks
 
 WIDTHS = [  # widths that 8 does not divide, and all above 4096; T above the 512 blocks' rows
