@@ -374,7 +374,12 @@ template <typename X, typename Y, typename U> hipError_t block_norm_launch(const
     return hipGetLastError();
 }
 
-// The other lengths, in pieces of 2 or 1.
+// The other lengths, in pieces of 2 or 1, with types that the call names.  The
+// gradient holds so many registers that a SIMD has one wave, and above 4096
+// columns some in memory.  4096 bf16 rows with both norms and a channel gate,
+// forward and gradient, in us (and TB/s): 2048 columns 16 (5.1) and 29 (4.6),
+// 2046 21 (4.1) and 54 (2.5), 2047 22 (3.8) and 63 (2.1), 8192 61 (5.5) and 165
+// (3.3), 8190 73 (4.6) and 187 (2.9), 8191 176 (1.9) and 366 (1.5).
 template <int V> hipError_t block_norm_launch_any(const NormArgs &a, bool back, hipStream_t s) {
     if (back) NORM_SIZES(block_norm_back_kernel, Any, Any, Any, V, (unsigned)a.blocks, (unsigned)a.blocks);
     else NORM_SIZES(block_norm_kernel, Any, Any, Any, V, (unsigned)((a.T + 3) / 4), (unsigned)a.T);

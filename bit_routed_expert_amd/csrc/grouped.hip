@@ -76,8 +76,7 @@ __global__ __launch_bounds__(1024) void grouped_plan_kernel(GroupArgs a) {
 // columns, 16 to a wave.  The rows lie in LDS; a wave streams its 16 weight
 // rows in whole (64 lanes x 16 bytes) from memory, two of them in flight, and
 // sums each over its lanes.  No launch lists the units: a block finds the
-// expert of "its" row by counting the segment ends at or before it.  48 rows
-// of 48 of 512 experts, 1536 x 2048: 47.6 us, 6.3 TB/s (the tiles: 87 us).
+// expert of "its" row by counting the segment ends at or before it.
 constexpr int GV_R = 4, GV_N = 64, GV_MAX_K = 8192;
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
@@ -171,6 +170,10 @@ constexpr size_t GP_HEAD = 256;     // the tile count, then the list
 constexpr int GP_MIN_ROWS = 32;     // smallest row tile
 
 // Rows against experts up to which the product goes without the matrix cores.
+// Of 512 experts, 1536 x 2048, picked evenly: 50 rows 50 us (6.0 TB/s of the
+// picked weights), the tiles 54; 128 rows 127 and 130.  Only the device knows how
+// the rows fall: 128 rows that all pick one expert are 32 units that each stream
+// its matrix, 35 us where the tiles take 14; 64 rows 16 and 14.
 bool few_rows_path(int64_t rows, int E, int K) { return rows * 4 <= E && K <= GV_MAX_K; }
 
 int64_t max_tiles(int64_t rows, int E, int tile_rows) { return rows / tile_rows + (rows < E ? rows : E); }
@@ -215,8 +218,12 @@ strata_status grouped_call(const void *A, const void *B, const int32_t *offsets,
 }
 
 // Blocks of a grid up to which each finds its own row tile; above, a launch
-// before lists them.  The list costs a launch and about 5 us; the search
-// about 1 us in every block.
+// before lists them.  The list costs a small grid 2 to 3 us, the search every
+// round of blocks about 1, and 32-row tiles their second block on a CU (28 bytes
+// of LDS too many).  Found and listed, 32 rows: 384 blocks 8.5 and 10.1 us, 600
+// 14.3 and 14.5, 900 20.5 and 18.6, 1640 29 and 22; 128 rows: 348 blocks 10.6 and
+// 13.6, 696 21.7 and 23.6, 1024 40.5 and 41.4, 4992 648 and 650; 256 rows: 288
+// blocks 35 and 37, 864 219 and 219.
 constexpr int64_t GP_FIND_BLOCKS = 512;
 
 template <int BM, int BN, int WM, int WN, int ST, int TB> strata_status launch_rows(GroupArgs &a, hipStream_t s) {

@@ -442,11 +442,11 @@ __device__ __forceinline__ int expert_by_rows(const GroupArgs &a, int r) {
 // C is an expert's [N][K] weights' gradient.  Rows go unevenly to experts, so
 // a tile's work does too: with up to 64 experts each one's tiles are cut into
 // quarters (which share rows in an XCD's L2), and the quarters go to the XCDs
-// by falling row count.  16 unevenly picked experts over 32768 rows, 1536 x
-// 2048 (the largest with 9090, 6187 or 7363 rows): 278, 228 and 227 us; every
-// tile dealt on its own 281, 223 and 235 us; even experts, 2048 x 2048: 263
-// against 275 us.  With more experts they even out, and an expert's tiles
-// stay on one XCD.
+// by falling row count.  With more experts they even out, and an expert's
+// tiles stay on one XCD.  16 unevenly picked experts over 32768 rows, 1536 x
+// 2048 (the largest with 6769, 5626 or 6646 rows): 208, 200 and 199 us, in
+// order with an expert on one XCD 311, 288 and 330; even experts, 2048 x
+// 2048: 259 and 260 us.
 template <int BM, int BN, int WM, int WN, int ST, int C>
 __global__ __launch_bounds__(64 * WM *WN) void grouped_wgrad_kernel(GroupArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN;

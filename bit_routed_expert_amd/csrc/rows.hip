@@ -10,9 +10,11 @@
 //
 // Rows are read and written with the streaming hint: each once, and a prompt
 // chunk's slots (168 MB) are most of what the caches hold.  4096 tokens of
-// 2048 bf16, 10 picks of 512 experts: combine 35.7 -> 31.2 us (5.7 TB/s),
-// its gradient 75.5 -> 70 us (5.0 TB/s), dispatch 33.5 -> 31.1 us (5.9
-// TB/s); with the experts' product right behind, within 1% either way.
+// 2048 bf16, 10 picks of 512 experts, four sets of rows in turn: combine 40.0
+// -> 34.4 us (5.9 TB/s), its gradient 74.0 -> 70.7 us (5.0 TB/s), dispatch
+// 34.9 -> 34.5 us (5.4 TB/s); dispatch into the same slots over and over, which
+// the last-level cache holds, 28.8 -> 34.7 us; with the experts' product right
+// behind, within 1% either way.
 #include "ops.hpp"
 
 namespace strata {
@@ -211,8 +213,9 @@ namespace {
 // Threads per token for nc pieces, and how many blocks share a token's row.
 // Many tokens fill the chip by themselves: the largest group that leaves at
 // most a quarter more threads idle than the best.  Few tokens: a thread per
-// piece as far as a block goes, and the rest of the row to other blocks (7
-// tokens of 1927 values in 121 trips of 16 threads: 72 us, else 4).
+// piece as far as a block goes, and the rest of the row to other blocks
+// (combine of 7 tokens of 1927 values in 121 trips of 16 threads: 72 us, else
+// 2.5).
 struct RowGroups {
     int threads, shares;
 };

@@ -12,10 +12,13 @@
 // to SORT_ONCE picks every block counts all of them by itself (from the L2,
 // into LDS counters kept several times over so that lanes with equal ids meet
 // less), those before its own chunk in the upper half of the same counters:
-// one launch, no counts exchanged (E = 512: 50 picks 3.5 us, 4090 picks 5.0
-// us, 40960 picks 7.7 us; in two launches 40960 picks take 8.3 us and the
-// host a second launch).  Above, a first launch counts each block's picks and
-// the second adds up the counts of the blocks before it (327680 picks 17 us).
+// one launch, no counts exchanged.  Above, a first launch counts each block's
+// picks and the second adds up the counts of the blocks before it (327680 picks
+// 17 us).  One launch against two, E = 512: 6000 picks 5.4 and 7.4 us, 20480
+// picks 6.7 and 7.9, 40960 picks 8.0 and 8.2, 65530 picks 9.8 and 9.3; 40960
+// picks of 16 experts 8.0 and 7.1: with many picks each block's count of all
+// of them through LDS costs what the second launch does.  The border is where
+// the 16-bit halves end, since two launches also cost the host a second one.
 #include "ops.hpp"
 
 namespace strata {

@@ -3,8 +3,9 @@
  * gradient: tokens sorted by expert and back, the experts' products over the
  * sorted rows with dense bf16 weights, and the norms before and after a
  * block fused with its gate and residual scale.  With strata_moe_route they
- * make a sparse block that can be trained and then quantised into the packed
- * format of strata_moe.h.
+ * are the sparse parts of a trainable block; the activation between the
+ * products, the router's own gradient (from dz) and packing the trained weights
+ * into the format of strata_moe.h are the caller's.
  *
  * Conventions are those of strata_moe.h: [dev] and [host] pointers, memory
  * owned by the caller, kernels only on `stream` (so a call can be captured
@@ -14,7 +15,8 @@
  * and every row follows the one before it (no padding between rows); the
  * current HIP device must be the stream's.  A workspace needs no
  * initialisation; calls that may overlap need workspaces of their own (a
- * captured graph keeps using the one it was captured with).  Results are the
+ * captured graph keeps using the one it was captured with).  An output shares
+ * no memory with another argument unless the call says that it may.  Results are the
  * same bits on every run: no sum depends on the order in which blocks run.
  * All sums, norms and their statistics are fp32; a bf16 output is rounded
  * once (to nearest even) as it is stored.
@@ -85,8 +87,8 @@ strata_status strata_moe_combine(const void *ys, strata_xdtype ydtype, int32_t r
  *   dw[t][r] = <dout[t], ys[pos[t*k + r]]>, 0 for a skipped pick   [dev] [T][k] fp32
  *   dz[t][r] = w[t][r] * (dw[t][r] - sum_s w[t][s] dw[t][s])       [dev] [T][k] fp32
  * dz is the gradient of the picked logits when the weights are their softmax
- * over the k picks (the gates of strata_moe_route).  Each output is
- * nullable; rows of dys without a pick are left as they were.  dys may be
+ * over the k picks (the gates of strata_moe_route); a skipped pick's weight
+ * enters its own dz alone.  Each output is nullable; rows of dys without a pick are left as they were.  dys may be
  * ys.  pos must name no row twice.  Errors as above, and EINVAL for a null w. */
 strata_status strata_moe_combine_backward(const void *dout, strata_xdtype odtype, const void *ys,
                                           strata_xdtype ydtype, int32_t rows, const int32_t *pos, const float *w,
