@@ -9,7 +9,9 @@ The C ABI is declared in include/strata_moe.h; the names here mirror it:
 ``workspace_bytes``, ``route``, ``forward``, ``kernel_names``.  The operators
 around the layer (include/strata_ops.h) are bound in ``ops`` and reached from
 here: ``sort_picks``, ``dispatch``, ``combine``, ``grouped_product``,
-``block_norm`` and their gradients.
+``block_norm`` and their gradients; so are the ends of a training step
+(include/strata_train.h): ``balance_loss``, ``embed``, ``vocab_loss`` with their
+gradients, and ``orthogonalise``.
 """
 from __future__ import annotations
 
@@ -19,10 +21,13 @@ from dataclasses import dataclass
 from typing import Optional, Sequence
 
 from . import ops as _ops
-from .ops import (GATE_CHANNEL, GATE_SIGMOID, GATE_TOKEN, POST_NORM, PRE_NORM, BlockNormArgs,  # noqa: F401
-                  block_norm, block_norm_args, block_norm_backward, block_norm_backward_workspace_bytes, combine,
-                  combine_backward, dispatch, dispatch_backward, grouped_dgrad, grouped_product, grouped_wgrad,
-                  grouped_workspace_bytes, sort_picks, sort_workspace_bytes)
+from .ops import (ACCUMULATE, GATE_CHANNEL, GATE_SIGMOID, GATE_TOKEN, POST_NORM, PRE_NORM, BlockNormArgs,  # noqa: F401
+                  balance_loss, balance_loss_backward, balance_loss_workspace_bytes, block_norm, block_norm_args,
+                  block_norm_backward, block_norm_backward_workspace_bytes, combine, combine_backward, dispatch,
+                  dispatch_backward, embed, embed_backward, embed_backward_workspace_bytes, grouped_dgrad,
+                  grouped_product, grouped_wgrad, grouped_workspace_bytes, orthogonalise, orthogonalise_workspace_bytes,
+                  sort_picks, sort_workspace_bytes, vocab_loss, vocab_loss_backward, vocab_loss_backward_workspace_bytes,
+                  vocab_loss_workspace_bytes)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libstrata_moe.so")

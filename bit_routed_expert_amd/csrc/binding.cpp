@@ -13,11 +13,14 @@
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "strata_ops.h"
+#include "strata_train.h"
 
 namespace {
 
-enum Fn { SORT, DISPATCH, DISPATCH_BACK, COMBINE, COMBINE_BACK, PRODUCT, DGRAD, WGRAD, NORM, NORM_BACK, FNS };
+enum Fn {
+    SORT, DISPATCH, DISPATCH_BACK, COMBINE, COMBINE_BACK, PRODUCT, DGRAD, WGRAD, NORM, NORM_BACK,
+    BALANCE, BALANCE_BACK, EMBED, EMBED_BACK, VOCAB, VOCAB_BACK, ORTH, FNS
+};
 void *g_fn[FNS];         // the library's functions
 PyObject *g_self[FNS];   // this module's, for a call that has to move to another device
 PyObject *g_raise, *g_elsewhere, *g_device, *g_first_device, *g_stream;
@@ -81,6 +84,12 @@ struct Call {
         if (v < 0) bad("%s is negative", names[i]);
         return v;
     }
+    float number(int i) {
+        if (!ok) return 0.f;
+        const double v = PyFloat_AsDouble(a[i]);
+        if (v == -1.0 && PyErr_Occurred()) ok = false;
+        return (float)v;
+    }
     strata_xdtype code(long long c, const char *name) {
         if (c != STRATA_X_BF16 && c != STRATA_X_F32) bad("%s is not X_BF16 or X_F32", name);
         return (strata_xdtype)c;
@@ -117,6 +126,11 @@ struct Call {
             bad("%s has %lld elements, not %lld", names[i], (long long)t->numel(), (long long)want);
         else if (!t->is_contiguous()) bad("%s is not contiguous", names[i]);
         return ok ? (T *)t->data_ptr() : nullptr;
+    }
+    // The same of truth values or bytes.
+    uint8_t *truths(int i, int64_t want) {
+        const at::Tensor *t = ok ? tensor(i) : nullptr;
+        return ptr<uint8_t>(i, t && t->scalar_type() == at::ScalarType::Byte ? at::ScalarType::Byte : at::ScalarType::Bool, want);
     }
     void *rows(int i, strata_xdtype c, int64_t want) { return ptr(i, c == STRATA_X_BF16 ? BF16 : F32, want); }
     // Address of a workspace said to hold `need` bytes.
@@ -393,12 +407,135 @@ PyObject *block_norm_backward(ARGS) {
     });
 }
 
+PyObject *balance_loss(ARGS) {
+    static const char *const names[] = {"z",   "zdtype", "idx",    "T",  "k",        "n_experts", "losses", "counts",
+                                        "lse", "tokens", "ws", "ws_bytes", "prob",      "keep",   "stream"};
+    return entry(BALANCE, args, nargs, names, [](Call &c) {
+        const auto zt = c.code(1);
+        const int32_t T = c.size(3), k = c.size(4), E = c.size(5);
+        const int64_t wb = c.bytes(11);
+        const void *const z = c.rows(0, zt, count(T, E));
+        const auto idx = c.ptr<int32_t>(2, I32, count(T, k));
+        const auto losses = c.ptr<float>(6, F32, 2);
+        const auto counts = c.ptr<int32_t>(7, I32, E);
+        const auto lse = c.ptr<float>(8, F32, T);
+        const auto tokens = c.ptr<int32_t>(9, I32, 1);
+        void *const ws = c.workspace(10, wb);
+        const auto prob = c.ptr<float>(12, F32, E);
+        const auto keep = c.truths(13, T);
+        return c.run([=](void *f, void *stream) {
+            return AS(strata_moe_balance)(z, zt, idx, keep, T, k, E, losses, counts, prob, lse, tokens, ws, (size_t)wb, stream);
+        });
+    });
+}
+
+PyObject *balance_loss_backward(ARGS) {
+    static const char *const names[] = {"z",      "zdtype", "idx",     "T",  "k",    "n_experts", "lse",
+                                        "counts", "tokens", "dlosses", "dz", "keep", "dpicks",    "stream"};
+    return entry(BALANCE_BACK, args, nargs, names, [](Call &c) {
+        const auto zt = c.code(1);
+        const int32_t T = c.size(3), k = c.size(4), E = c.size(5);
+        const void *const z = c.rows(0, zt, count(T, E));
+        const auto idx = c.ptr<int32_t>(2, I32, count(T, k));
+        const auto lse = c.ptr<float>(6, F32, T);
+        const auto counts = c.ptr<int32_t>(7, I32, E), tokens = c.ptr<int32_t>(8, I32, 1);
+        const auto dlosses = c.ptr<float>(9, F32, 2);
+        void *const dz = c.rows(10, zt, count(T, E));
+        const auto keep = c.truths(11, T);
+        const auto dpicks = c.ptr<float>(12, F32, count(T, k));
+        return c.run([=](void *f, void *stream) {
+            return AS(strata_moe_balance_backward)(z, zt, idx, keep, T, k, E, lse, counts, tokens, dlosses, dpicks, dz, stream);
+        });
+    });
+}
+
+PyObject *embed(ARGS) {
+    static const char *const names[] = {"W", "wdtype", "V", "d", "ids", "T", "scale", "out", "odtype", "stream"};
+    return entry(EMBED, args, nargs, names, [](Call &c) {
+        const auto wt = c.code(1), ot = c.code(8);
+        const int32_t V = c.size(2), d = c.size(3), T = c.size(5);
+        const float scale = c.number(6);
+        const void *const W = c.rows(0, wt, count(V, d));
+        const auto ids = c.ptr<int32_t>(4, I32, T);
+        void *const out = c.rows(7, ot, count(T, d));
+        return c.run([=](void *f, void *stream) { return AS(strata_embed)(W, wt, V, d, ids, T, scale, out, ot, stream); });
+    });
+}
+
+PyObject *embed_backward(ARGS) {
+    static const char *const names[] = {"dout", "odtype", "ids", "T",        "V",     "d",     "scale",
+                                        "dW",   "wdtype", "ws",  "ws_bytes", "flags", "stream"};
+    return entry(EMBED_BACK, args, nargs, names, [](Call &c) {
+        const auto ot = c.code(1), wt = c.code(8);
+        const int32_t T = c.size(3), V = c.size(4), d = c.size(5), flags = c.size(11);
+        const float scale = c.number(6);
+        const int64_t wb = c.bytes(10);
+        const void *const dout = c.rows(0, ot, count(T, d));
+        const auto ids = c.ptr<int32_t>(2, I32, T);
+        void *const dW = c.rows(7, wt, count(V, d)), *const ws = c.workspace(9, wb);
+        return c.run([=](void *f, void *stream) {
+            return AS(strata_embed_backward)(dout, ot, ids, T, V, d, scale, dW, wt, (uint32_t)flags, ws, (size_t)wb, stream);
+        });
+    });
+}
+
+PyObject *vocab_loss(ARGS) {
+    static const char *const names[] = {"h", "W", "targets", "T", "V", "d", "loss", "lse", "ws", "ws_bytes", "stream"};
+    return entry(VOCAB, args, nargs, names, [](Call &c) {
+        const int32_t T = c.size(3), V = c.size(4), d = c.size(5);
+        const int64_t wb = c.bytes(9);
+        const void *const h = c.ptr(0, BF16, count(T, d)), *const W = c.ptr(1, BF16, count(V, d));
+        const auto targets = c.ptr<int32_t>(2, I32, T);
+        const auto loss = c.ptr<float>(6, F32, T), lse = c.ptr<float>(7, F32, T);
+        void *const ws = c.workspace(8, wb);
+        return c.run([=](void *f, void *stream) {
+            return AS(strata_vocab_loss)(h, W, targets, T, V, d, loss, lse, ws, (size_t)wb, stream);
+        });
+    });
+}
+
+PyObject *vocab_loss_backward(ARGS) {
+    static const char *const names[] = {"h",        "W",    "targets", "T",       "V",  "d",       "lse",   "dloss", "ws",
+                                        "ws_bytes", "dlse", "dh",      "dhdtype", "dW", "dwdtype", "flags", "stream"};
+    return entry(VOCAB_BACK, args, nargs, names, [](Call &c) {
+        const int32_t T = c.size(3), V = c.size(4), d = c.size(5), flags = c.size(15);
+        const auto ht = c.code(12), wt = c.code(14);
+        const int64_t wb = c.bytes(9);
+        const void *const h = c.ptr(0, BF16, count(T, d)), *const W = c.ptr(1, BF16, count(V, d));
+        const auto targets = c.ptr<int32_t>(2, I32, T);
+        const auto lse = c.ptr<float>(6, F32, T), dloss = c.ptr<float>(7, F32, T), dlse = c.ptr<float>(10, F32, T);
+        void *const ws = c.workspace(8, wb), *const dh = c.rows(11, ht, count(T, d)), *const dW = c.rows(13, wt, count(V, d));
+        return c.run([=](void *f, void *stream) {
+            return AS(strata_vocab_loss_backward)(h, W, targets, T, V, d, lse, dloss, dlse, dh, ht, dW, wt, (uint32_t)flags, ws,
+                                                  (size_t)wb, stream);
+        });
+    });
+}
+
+PyObject *orthogonalise(ARGS) {
+    static const char *const names[] = {"G",     "gdtype", "n", "N", "K", "out",   "ws", "ws_bytes",
+                                        "steps", "a",      "b", "c", "scale", "eps", "stream"};
+    return entry(ORTH, args, nargs, names, [](Call &c) {
+        const auto gt = c.code(1);
+        const int32_t n = c.size(2), N = c.size(3), K = c.size(4), steps = c.size(8);
+        const int64_t wb = c.bytes(7);
+        const float p[3] = {c.number(9), c.number(10), c.number(11)}, scale = c.number(12), eps = c.number(13);
+        const void *const G = c.rows(0, gt, count(n, N, K));
+        void *const out = c.ptr(5, BF16, count(n, N, K)), *const ws = c.workspace(6, wb);
+        return c.run([=](void *f, void *stream) {
+            return AS(strata_orthogonalise)(G, gt, n, N, K, steps, p, scale, eps, out, ws, (size_t)wb, stream);
+        });
+    });
+}
+
 #define METHOD(NAME) {#NAME, (PyCFunction)(void (*)())NAME, METH_FASTCALL, nullptr}
 PyObject *bind(PyObject *, PyObject *);
 PyMethodDef g_methods[] = {   // in the order of Fn
     METHOD(sort_picks),      METHOD(dispatch),      METHOD(dispatch_backward), METHOD(combine),
     METHOD(combine_backward), METHOD(grouped_product), METHOD(grouped_dgrad),     METHOD(grouped_wgrad),
-    METHOD(block_norm),      METHOD(block_norm_backward), {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
+    METHOD(block_norm),      METHOD(block_norm_backward), METHOD(balance_loss),   METHOD(balance_loss_backward),
+    METHOD(embed),           METHOD(embed_backward),  METHOD(vocab_loss),         METHOD(vocab_loss_backward),
+    METHOD(orthogonalise),   {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 
 // bind(addresses of the library's functions, raise, elsewhere, device, first device, stream)
 PyObject *bind(PyObject *module, PyObject *args) {

@@ -2,7 +2,7 @@
 // vector loads and stores of bf16 or fp32 rows as fp32 values.
 #pragma once
 #include "mfma.hpp"
-#include "strata_ops.h"
+#include "strata_train.h"
 
 namespace strata {
 

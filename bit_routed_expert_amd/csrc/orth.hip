@@ -1,0 +1,245 @@
+// Matrices orthogonalised by Newton-Schulz products (strata_orthogonalise).
+//
+//   A = X X^T,  B = b A + c A^2,  X' = a X + B X        (from the right where N > K)
+//
+// Three launches of tile products a step, over all matrices at once; b A, c,
+// a X and the last scale are epilogues.  A and B are symmetric: only the
+// tiles of their lower halves are computed.  The operands are fp16: the values
+// are in known ranges (|X| and |A| at most about 1, X kept times a power of
+// two), and 11 bits leave the result about 3e-4 off where bf16's 8 would leave
+// 5e-3.  X itself is hi + lo, 22 bits: with hi alone the rounding of X, a
+// matrix of full rank, would be multiplied by a at every step like the small
+// directions of G itself (3.4^5 = 485 in five steps; a gradient of 80 rows in
+// 1536 x 2048 came out 2% off).
+#include <cmath>
+
+#include "orth_impl.hpp"
+
+namespace strata {
+
+constexpr int ORTH_SIDE = 16384, ORTH_N = 1024, ORTH_PARTS = 64;
+
+template <int V, typename G> __device__ __forceinline__ void piece_values(const G *p, int64_t i, float (&v)[V]) {
+    Raw<G, V> r;
+    load_raw<V>(p, i, r);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = value<V>(r, j);
+}
+
+// Sum of squares of a part of a matrix, in 64 bits.  Pieces of V values do not cross rows.
+template <typename G, int V> __global__ __launch_bounds__(256) void orth_norm_kernel(OrthArgs a) {
+    __shared__ double sh[4];
+    const int e = blockIdx.y, part = blockIdx.x;
+    const int64_t pieces = (int64_t)a.N * a.K / V, per = (pieces + a.parts - 1) / a.parts;
+    const int64_t p0 = part * per, p1 = min(p0 + per, pieces);
+    const G *g = (const G *)a.G + (int64_t)e * a.N * a.K;
+    double s = 0.0;
+#pragma unroll 4
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += 256) {
+        float v[V];
+        piece_values<V, G>(g, p * V, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = fma((double)v[j], (double)v[j], s);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) a.norms[e * a.parts + part] = sh[0] + sh[1] + sh[2] + sh[3];
+}
+
+// X_0 = G / (|G| + eps), times size, in two pieces (or, without steps, times scale to out).
+template <typename G, int V> __global__ __launch_bounds__(256) void orth_start_kernel(OrthArgs a, int steps) {
+    const int e = blockIdx.y;
+    double s = 0.0;
+    for (int q = 0; q < a.parts; ++q) s += a.norms[e * a.parts + q];
+    const double r = 1.0 / (sqrt(s) + (double)a.eps);
+    const int nc = (steps ? a.ldx : a.K + V - 1) / V;   // pieces of a row, those of zeros behind its end too
+    const G *g = (const G *)a.G + (int64_t)e * a.N * a.K;
+    const int64_t all = (int64_t)a.N * nc;
+    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < all; p += (int64_t)gridDim.x * 256) {
+        const int64_t m = p / nc;
+        const int c = (int)(p - m * nc) * V;
+        float v[V], l[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = 0.f;
+        if (c < a.K) piece_values<V, G>(g, m * a.K + c, v);
+        if (!steps) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = (float)((double)v[j] * r * (double)a.scale);
+            store_values<V>(a.out + (int64_t)e * a.N * a.K, m * a.K + c, v);
+            continue;
+        }
+        uint16_t *hi = a.hi + ((int64_t)e * a.N + m) * a.ldx + c, *lo = a.lo + ((int64_t)e * a.N + m) * a.ldx + c;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float x = (float)((double)v[j] * r) * a.size;
+            v[j] = x;
+            l[j] = x - (float)(_Float16)x;
+        }
+        if constexpr (V == 1) {
+            *hi = (uint16_t)half_pair(v[0], 0.f);
+            *lo = (uint16_t)half_pair(l[0], 0.f);
+        } else {
+            uint32_t w[V / 2], x[V / 2];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                w[j] = half_pair(v[2 * j], v[2 * j + 1]);
+                x[j] = half_pair(l[2 * j], l[2 * j + 1]);
+            }
+            __builtin_memcpy(__builtin_assume_aligned(hi, 2 * V), w, 2 * V);
+            __builtin_memcpy(__builtin_assume_aligned(lo, 2 * V), x, 2 * V);
+        }
+    }
+}
+
+namespace {
+
+strata_status check_orth(int32_t n, int32_t N, int32_t K) {
+    if (n < 0 || N < 1 || K < 1) return STRATA_EINVAL;
+    if (N > ORTH_SIDE || K > ORTH_SIDE || n > ORTH_N || (int64_t)n * N * K > ((int64_t)1 << 33)) return STRATA_EUNSUPPORTED;
+    return STRATA_OK;
+}
+
+struct OrthPlan {
+    int side, ldx, lds;
+    size_t hi, next, lo, A, B, bytes;
+};
+
+OrthPlan orth_plan(int32_t n, int32_t N, int32_t K) {
+    OrthPlan p{};
+    p.side = N < K ? N : K;
+    p.ldx = (K + 7) / 8 * 8;
+    p.lds = (p.side + 7) / 8 * 8;
+    size_t at = (size_t)(n > 0 ? n : 1) * ORTH_PARTS * 8;
+    const auto take = [&](size_t values) {
+        const size_t q = at;
+        at += (values * 2 + 255) / 256 * 256;
+        return q;
+    };
+    const size_t x = (size_t)n * N * p.ldx, s = (size_t)n * p.side * p.lds;
+    p.hi = take(x);
+    p.next = take(x);
+    p.lo = take(x);
+    p.A = take(s);
+    p.B = take(s);
+    p.bytes = at;
+    return p;
+}
+
+template <typename G, int V> hipError_t orth_begin(const OrthArgs &a, int steps, hipStream_t s) {
+    STRATA_LAUNCH((orth_norm_kernel<G, V>), dim3(a.parts, a.n), dim3(256), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t pieces = (int64_t)a.N * a.ldx / V, blocks = (pieces + 1023) / 1024, most = 8192 / a.n + 1;
+    STRATA_LAUNCH((orth_start_kernel<G, V>), dim3((unsigned)(blocks < most ? blocks : most), a.n), dim3(256), 0, s, a, steps);
+    return hipGetLastError();
+}
+
+template <typename G> hipError_t orth_begin_width(const OrthArgs &a, int steps, hipStream_t s) {
+    if (a.K % 8 == 0) return orth_begin<G, 8>(a, steps, s);
+    if (a.K % 4 == 0) return orth_begin<G, 4>(a, steps, s);
+    if (a.K % 2 == 0) return orth_begin<G, 2>(a, steps, s);
+    return orth_begin<G, 1>(a, steps, s);
+}
+
+dim3 range_grid(int64_t tiles) { return dim3((unsigned)((tiles + 7) / 8 * 8)); }
+
+template <int BM, int WM, int WN, int ST, int SQUARE, int ACROSS> void square(const OrthArgs &a, hipStream_t s) {
+    const int64_t nt = (a.side + BM - 1) / BM;
+    STRATA_LAUNCH((orth_square_kernel<BM, WM, WN, ST, 64, SQUARE, ACROSS>), range_grid(a.n * (nt * (nt + 1) / 2)), dim3(64 * WM * WN),
+                  0, s, a);
+}
+
+template <int BM, int BN, int WM, int WN, int ST, int TALL> void step(const OrthArgs &a, hipStream_t s) {
+    const int64_t nr = (a.N + BM - 1) / BM, nk = (a.K + BN - 1) / BN;
+    STRATA_LAUNCH((orth_step_kernel<BM, BN, WM, WN, ST, TALL>), range_grid(a.n * nr * nk), dim3(64 * WM * WN), 0, s, a);
+}
+
+template <int SQUARE, int ACROSS> hipError_t squares(const OrthArgs &a, hipStream_t s) {
+    const auto tiles = [&](int64_t t) {
+        const int64_t nt = (a.side + t - 1) / t;
+        return a.n * (nt * (nt + 1) / 2);
+    };
+    if (tiles(256) >= 192) square<256, 2, 4, 2, SQUARE, ACROSS>(a, s);
+    else if (tiles(128) >= 192) square<128, 2, 2, 4, SQUARE, ACROSS>(a, s);
+    else square<64, 1, 2, 4, SQUARE, ACROSS>(a, s);
+    return hipGetLastError();
+}
+
+template <int TALL> hipError_t steps_of(const OrthArgs &a, hipStream_t s) {
+    const auto tiles = [&](int64_t r, int64_t c) { return a.n * ((a.N + r - 1) / r) * ((a.K + c - 1) / c); };
+    if (tiles(256, 256) >= 192) step<256, 256, 2, 4, 2, TALL>(a, s);
+    else if (tiles(128, 256) >= 192) step<128, 256, 2, 4, 3, TALL>(a, s);
+    else step<64, 128, 2, 2, 4, TALL>(a, s);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace strata
+
+using namespace strata;
+
+extern "C" {
+
+size_t strata_orthogonalise_workspace_bytes(int32_t n, int32_t N, int32_t K) {
+    return check_orth(n, N, K) == STRATA_OK ? orth_plan(n, N, K).bytes : 0;
+}
+
+strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t n, int32_t N, int32_t K, int32_t steps,
+                                   const float *coefficients, float scale, float eps, void *out, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    if (bad_dtype(gdtype) || steps < 0 || steps > 32 || !coefficients || !std::isfinite(scale) || !(eps > 0.f) || !std::isfinite(eps))
+        return STRATA_EINVAL;
+    for (int i = 0; i < 3; ++i)
+        if (!std::isfinite(coefficients[i])) return STRATA_EINVAL;
+    const strata_status st = check_orth(n, N, K);
+    if (st != STRATA_OK || n == 0) return st;
+    if (bad_rows(G) || bad_rows(out) || bad_rows(ws)) return STRATA_EINVAL;
+    const OrthPlan p = orth_plan(n, N, K);
+    if (ws_bytes < p.bytes) return STRATA_EWORKSPACE;
+    // Without steps blocks convert G while others still read it: only piece by piece in place.
+    const size_t values = (size_t)n * N * K;
+    if (steps == 0 && !(G == out && gdtype == STRATA_X_BF16) && overlap(G, values * (gdtype == STRATA_X_BF16 ? 2 : 4), out, values * 2))
+        return STRATA_EINVAL;
+    const hipStream_t s = (hipStream_t)stream;
+    char *const w = (char *)ws;
+    OrthArgs a{};
+    a.G = G;
+    a.out = (uint16_t *)out;
+    a.norms = (double *)w;
+    a.hi = (uint16_t *)(w + p.hi);
+    a.next = (uint16_t *)(w + p.next);
+    a.lo = (uint16_t *)(w + p.lo);
+    a.A = (uint16_t *)(w + p.A);
+    a.B = (uint16_t *)(w + p.B);
+    a.n = n;
+    a.N = N;
+    a.K = K;
+    a.side = p.side;
+    a.ldx = p.ldx;
+    a.lds = p.lds;
+    const int64_t parts = ((int64_t)N * K + 16383) / 16384;
+    a.parts = (int)(parts < ORTH_PARTS ? parts : ORTH_PARTS);
+    a.size = exp2f(roundf(0.5f * log2f((float)(N > K ? N : K))));
+    a.a = coefficients[0];
+    a.b = coefficients[1];
+    a.c = coefficients[2];
+    a.scale = scale;
+    a.eps = eps;
+    const bool tall = N > K;
+    hipError_t e = gdtype == STRATA_X_BF16 ? orth_begin_width<uint16_t>(a, steps, s) : orth_begin_width<float>(a, steps, s);
+    for (int i = 0; i < steps && e == hipSuccess; ++i) {
+        a.last = i + 1 == steps;
+        e = tall ? squares<0, 1>(a, s) : squares<0, 0>(a, s);
+        if (e == hipSuccess) e = squares<1, 0>(a, s);
+        if (e == hipSuccess) e = tall ? steps_of<1>(a, s) : steps_of<0>(a, s);
+        uint16_t *const hi = a.hi;
+        a.hi = a.next;
+        a.next = hi;
+    }
+    return hip_status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,238 @@
+// Kernels of the orthogonalised updates (orth.hip).
+#pragma once
+#include "tile_impl.hpp"
+
+namespace strata {
+
+// n matrices of N x K; side = min(N, K), the order of A and B.  X is kept
+// times `size` (a power of two near sqrt(max(N, K)), so that its values are
+// about 1 in size at the end), in rows of ldx values; A and B in rows of lds.
+// What lies in a row behind its last column is zero in all of them.
+struct OrthArgs {
+    const void *G;
+    uint16_t *out;              // bf16 [n][N][K]
+    double *norms;              // [n][parts] sums of squares
+    uint16_t *hi, *next, *lo;   // X = hi + lo, the next X's hi
+    uint16_t *A, *B;
+    int n, N, K, side, ldx, lds, parts, last;
+    float size, a, b, c, scale, eps;
+};
+
+__device__ __forceinline__ float half_value(uint32_t w, int high) { return half_to_float((uint16_t)(high ? w >> 16 : w)); }
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+    typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+}
+
+// Buffer of M rows of ld 16-bit values.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t half_rows(const void *p, int M, int ld) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, __builtin_amdgcn_readfirstlane((int)((uint32_t)M * (uint32_t)ld * 2u)),
+                                             0x00020000);
+}
+
+// This lane's 4 values of subtile (i, j), group q, at row m0 + 32 i + lane % 32, column n0 + 32 j + 8 q + 4 (lane / 32):
+// offset in bytes, past every buffer for columns behind ld.
+__device__ __forceinline__ uint32_t quad_at(int m0, int n0, int ld, int i, int j, int q) {
+    const int lane = threadIdx.x & 63, m = m0 + 32 * i + (lane & 31), n = n0 + 32 * j + 8 * q + 4 * (lane >> 5);
+    return n < ld ? ((uint32_t)m * (uint32_t)ld + n) * 2u : 0xFFFFFFF0u;
+}
+
+__device__ __forceinline__ f32x4_t load_quad(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    const u32x2_t w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+    return f32x4_t{half_value(w[0], 0), half_value(w[0], 1), half_value(w[1], 0), half_value(w[1], 1)};
+}
+
+// 16 values of a subtile as fp16 pairs to rows of ld: 16-byte stores after the wave's halves have exchanged groups.
+__device__ __forceinline__ void store_halves(__amdgpu_buffer_rsrc_t r, int m0, int n0, int ld, int i, int j, const uint32_t (&w)[8]) {
+    const int lane = threadIdx.x & 63, m = m0 + 32 * i + (lane & 31);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const auto s0 = __builtin_amdgcn_permlane32_swap(w[4 * q], w[4 * q + 2], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(w[4 * q + 1], w[4 * q + 3], false, false);
+        const int n = n0 + 32 * j + 16 * q + 8 * (lane >> 5);
+        const uint32_t at = n < ld ? ((uint32_t)m * (uint32_t)ld + n) * 2u : 0xFFFFFFF0u;
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{s0[0], s1[0], s0[1], s1[1]}, r, at, 0, 0);
+    }
+}
+
+// Tile (i, j), j <= i, number t of the lower half of a square of tiles.
+__device__ __forceinline__ void lower_tile(int t, int &i, int &j) {
+    i = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    j = t - i * (i + 1) / 2;
+}
+
+// Blocks dealt to the 8 XCDs in ranges.
+__device__ __forceinline__ bool range_tile(int64_t total, int64_t &t) {
+    const int64_t per = (total + 7) >> 3, q = blockIdx.x >> 3;
+    t = (int64_t)(blockIdx.x & 7) * per + q;
+    return q < per && t < total;
+}
+
+// SQUARE 0: A = X X^T (ACROSS 1: X^T X), else B = b A + c A A: symmetric, so
+// only the tiles of the lower half are computed; those off the diagonal are
+// stored a second time, transposed.
+template <int BM, int WM, int WN, int ST, int C, int SQUARE, int ACROSS>
+__global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
+    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BM / 32 / WN;
+    typedef Operand<BM, ACROSS, NT, C> OA;
+    typedef Operand<BM, ACROSS, NT, C> OB;
+    GROUP_BUFFERS(ST, OA, OB)
+    const int nt = (a.side + BM - 1) / BM, tri = nt * (nt + 1) / 2;
+    int64_t t;
+    if (!range_tile((int64_t)a.n * tri, t)) return;
+    const int e = __builtin_amdgcn_readfirstlane((int)(t / tri));
+    int ti, tj;
+    lower_tile(__builtin_amdgcn_readfirstlane((int)(t - (int64_t)e * tri)), ti, tj);
+    ti = __builtin_amdgcn_readfirstlane(ti);
+    tj = __builtin_amdgcn_readfirstlane(tj);
+    const int64_t squares = (int64_t)a.side * a.lds;
+    const uint16_t *A0 = a.A + e * squares;
+    const uint16_t *X = SQUARE ? A0 : a.hi + (int64_t)e * a.N * a.ldx;
+    const int ld = SQUARE ? a.lds : a.ldx, cd = ACROSS ? a.N : ld;
+    const int r0 = ti * BM, k0 = tj * BM, M = min(a.side - r0, BM);
+    OA A;
+    OB B;
+    A.init(X, ld, r0, a.side, cd);
+    B.init(X, ld, k0, a.side, cd);
+    int m0, n0;
+    wave_place<WM, WN, MT, NT2>(m0, n0);
+    f32x16_t acc[MT][NT2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int steps = (cd + C - 1) / C;
+    const bool active = m0 < M && k0 + n0 < a.lds;
+    if (!active) {
+        contract<ST, false, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+        return;
+    }
+    contract<ST, true, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+    uint16_t *to = (SQUARE ? a.B : a.A) + e * squares;
+    const auto old = half_rows(A0 + (int64_t)r0 * a.lds, M, a.lds), rows = half_rows(to + (int64_t)r0 * a.lds, M, a.lds);
+    const auto cols = half_rows(to + (int64_t)k0 * a.lds, min(a.side - k0, BM), a.lds);
+    const float r = SQUARE ? a.c : 1.f / (a.size * a.size);
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j) {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4_t v = {acc[i][j][4 * q] * r, acc[i][j][4 * q + 1] * r, acc[i][j][4 * q + 2] * r, acc[i][j][4 * q + 3] * r};
+                if (SQUARE) v += a.b * load_quad(old, quad_at(m0, k0 + n0, a.lds, i, j, q));
+                w[2 * q] = half_pair(v[0], v[1]);
+                w[2 * q + 1] = half_pair(v[2], v[3]);
+            }
+            if (ti != tj) {
+                const int m = r0 + m0 + 32 * i + (lane & 31);
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int n = n0 + 32 * j + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
+                    const uint32_t at = m < a.lds ? ((uint32_t)n * (uint32_t)a.lds + m) * 2u : 0xFFFFFFF0u;
+                    const uint32_t x = w[v / 2];
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v & 1 ? x >> 16 : x), cols, at, 0, 0);
+                }
+            }
+            store_halves(rows, m0, k0 + n0, a.lds, i, j, w);
+        }
+}
+
+// X' = a X + B X (TALL: a X + X B, B symmetric), the last one to out.
+template <int BM, int BN, int WM, int WN, int ST, int TALL>
+__global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
+    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN, C = 64;
+    typedef Operand<BM, 0, NT, C> OA;
+    typedef Operand<BN, !TALL, NT, C> OB;
+    GROUP_BUFFERS(ST, OA, OB)
+    const int nr = (a.N + BM - 1) / BM, nk = (a.K + BN - 1) / BN;
+    int64_t t;
+    if (!range_tile((int64_t)a.n * nr * nk, t)) return;
+    const int e = __builtin_amdgcn_readfirstlane((int)(t / (nr * nk))), at = (int)(t - (int64_t)e * nr * nk);
+    const int r0 = __builtin_amdgcn_readfirstlane(at / nk) * BM, k0 = __builtin_amdgcn_readfirstlane(at % nk) * BN;
+    const int M = min(a.N - r0, BM);
+    const int64_t xs = (int64_t)a.N * a.ldx;
+    const uint16_t *X = a.hi + e * xs, *S = a.B + (int64_t)e * a.side * a.lds;
+    OA A;
+    OB B;
+    if (TALL) {
+        A.init(X, a.ldx, r0, a.N, a.ldx);
+        B.init(S, a.lds, k0, a.side, a.lds);
+    } else {
+        A.init(S, a.lds, r0, a.side, a.lds);
+        B.init(X, a.ldx, k0, a.ldx, a.N);
+    }
+    int m0, n0;
+    wave_place<WM, WN, MT, NT2>(m0, n0);
+    f32x16_t acc[MT][NT2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int steps = (a.lds + C - 1) / C;
+    if (m0 >= M || k0 + n0 >= a.ldx) {
+        contract<ST, false, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+        return;
+    }
+    contract<ST, true, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+    const auto hi = half_rows(X + (int64_t)r0 * a.ldx, M, a.ldx), lo = half_rows(a.lo + e * xs + (int64_t)r0 * a.ldx, M, a.ldx);
+    const auto next = half_rows(a.next + e * xs + (int64_t)r0 * a.ldx, M, a.ldx);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        __builtin_amdgcn_sched_barrier(0);   // no more than a subtile row's loads ahead: registers
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t p = quad_at(m0, k0 + n0, a.ldx, i, j, q);
+                const f32x4_t x = load_quad(hi, p) + load_quad(lo, p);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][j][4 * q + c] = fmaf(a.a, x[c], acc[i][j][4 * q + c]);
+            }
+    }
+    if (a.last) {
+        const float r = a.scale / a.size;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] *= r;
+        uint16_t *to = a.out + ((int64_t)e * a.N + r0) * a.K;
+        if (a.K % 8 == 0) return store_tile<MT, NT2>(to, 1, m0, M, k0 + n0, a.K, acc);
+        const int lane = threadIdx.x & 63;   // rows that 16 bytes do not divide
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int m = m0 + 32 * i + (lane & 31), n = k0 + n0 + 32 * j + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
+                    if (m < M && n < a.K) to[(int64_t)m * a.K + n] = f2bf(acc[i][j][v]);
+                }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j) {
+            uint32_t w[8], l[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float x = acc[i][j][2 * q], y = acc[i][j][2 * q + 1];
+                w[q] = half_pair(x, y);
+                l[q] = half_pair(x - half_value(w[q], 0), y - half_value(w[q], 1));
+            }
+            store_halves(next, m0, k0 + n0, a.ldx, i, j, w);
+            store_halves(lo, m0, k0 + n0, a.ldx, i, j, l);
+        }
+}
+
+}  // namespace strata

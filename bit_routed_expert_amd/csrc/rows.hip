@@ -15,19 +15,11 @@
 // 34.9 -> 34.5 us (5.4 TB/s); dispatch into the same slots over and over, which
 // the last-level cache holds, 28.8 -> 34.7 us; with the experts' product right
 // behind, within 1% either way.
-#include "ops.hpp"
+#include "rows.hpp"
 
 namespace strata {
 
 constexpr int PB = 16;   // picked rows in flight per thread
-
-// Token of this thread's group and its place in the group.
-template <int G> __device__ __forceinline__ bool row_group(int T, int &t, int &lane) {
-    t = (int)blockIdx.x * (256 / G) + (int)(threadIdx.x / G);
-    if (G >= 64) t = __builtin_amdgcn_readfirstlane(t);
-    lane = threadIdx.x % G;
-    return t < T;
-}
 
 // The positions (and weights) of up to PB picks r0.. of a token, -1 behind
 // the k-th.  Groups of whole waves read them once, a pick to a lane, and pass
@@ -210,34 +202,6 @@ __global__ __launch_bounds__(256) void combine_back_kernel(const O *__restrict__
 
 namespace {
 
-// Threads per token for nc pieces, and how many blocks share a token's row.
-// Many tokens fill the chip by themselves: the largest group that leaves at
-// most a quarter more threads idle than the best.  Few tokens: a thread per
-// piece as far as a block goes, and the rest of the row to other blocks
-// (combine of 7 tokens of 1927 values in 121 trips of 16 threads: 72 us, else
-// 2.5).
-struct RowGroups {
-    int threads, shares;
-};
-constexpr int ROW_BLOCKS = 1024;   // blocks that fill the chip
-RowGroups row_groups(int T, int64_t nc, int least) {
-    int g = least;
-    if (T >= ROW_BLOCKS) {
-        int64_t best = INT64_MAX;
-        for (int q = least; q <= 256; q *= 2) {
-            const int64_t c = (nc + q - 1) / q * q;
-            if (c < best) best = c;
-        }
-        for (int q = least; q <= 256; q *= 2)
-            if ((nc + q - 1) / q * q * 4 <= best * 5) g = q;
-    } else {
-        while (g < 256 && g < nc) g *= 2;
-    }
-    const int64_t blocks = ((int64_t)T * g + 255) / 256, trips = (nc + g - 1) / g;
-    const int64_t want = (ROW_BLOCKS + blocks - 1) / blocks;
-    return RowGroups{g, (int)(want < trips ? want : trips)};
-}
-
 strata_status check_rows(const void *a, const void *b, const int32_t *pos, int32_t rows, int32_t T, int32_t k,
                          int32_t d) {
     if (T < 0 || rows < 0 || k < 1 || k > 32 || d < 1) return STRATA_EINVAL;
@@ -246,10 +210,6 @@ strata_status check_rows(const void *a, const void *b, const int32_t *pos, int32
     if (rows > 0 ? bad_rows(a) : (a && !aligned16(a))) return STRATA_EINVAL;
     if (T > MAX_ROWS || (int64_t)T * k > INT32_MAX || d > MAX_COLS) return STRATA_EUNSUPPORTED;
     return STRATA_OK;
-}
-
-dim3 row_grid(int T, int g, int shares) {
-    return dim3((unsigned)(((int64_t)T + 256 / g - 1) / (256 / g)), (unsigned)shares);
 }
 
 template <typename P>

@@ -1,4 +1,5 @@
-"""Binding of the operators around the layer (include/strata_ops.h).
+"""Binding of the operators around the layer (include/strata_ops.h) and of the
+ends of a training step (include/strata_train.h).
 
 Tensors are checked before a call (device, type, contiguity, element count)
 and a mismatch raises StrataError with STRATA_EINVAL; everything else is
@@ -13,6 +14,7 @@ from __future__ import annotations
 import ctypes
 
 POST_NORM, PRE_NORM, GATE_TOKEN, GATE_CHANNEL, GATE_SIGMOID = 1, 2, 4, 8, 16
+ACCUMULATE = 1   # STRATA_ACCUMULATE
 
 _EINVAL = 1
 
@@ -20,7 +22,10 @@ SYMBOLS = ("strata_moe_sort_workspace_bytes", "strata_moe_sort", "strata_moe_dis
            "strata_moe_dispatch_backward", "strata_moe_combine", "strata_moe_combine_backward",
            "strata_moe_grouped_workspace_bytes", "strata_moe_grouped_product", "strata_moe_grouped_dgrad",
            "strata_moe_grouped_wgrad", "strata_block_norm", "strata_block_norm_backward_workspace_bytes",
-           "strata_block_norm_backward")
+           "strata_block_norm_backward", "strata_moe_balance_workspace_bytes", "strata_moe_balance",
+           "strata_moe_balance_backward", "strata_embed", "strata_embed_backward_workspace_bytes", "strata_embed_backward",
+           "strata_vocab_loss_workspace_bytes", "strata_vocab_loss_backward_workspace_bytes", "strata_vocab_loss",
+           "strata_vocab_loss_backward", "strata_orthogonalise_workspace_bytes", "strata_orthogonalise")
 
 
 class BlockNormArgs(ctypes.Structure):
@@ -32,6 +37,7 @@ class BlockNormArgs(ctypes.Structure):
 def declare(lib):
     """Signatures of the functions above on a loaded library."""
     vp, i32, sz, it = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int
+    u32, fl = ctypes.c_uint32, ctypes.c_float
     norm = ctypes.POINTER(BlockNormArgs)
     for name, restype, argtypes in (
             ("strata_moe_sort_workspace_bytes", sz, [i32, i32, i32]),
@@ -46,7 +52,20 @@ def declare(lib):
             ("strata_moe_grouped_wgrad", it, [vp, vp, vp, i32, i32, i32, i32, vp, it, vp, sz, vp]),
             ("strata_block_norm", it, [norm, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             ("strata_block_norm_backward_workspace_bytes", sz, [norm]),
-            ("strata_block_norm_backward", it, [norm] + [vp] * 15 + [sz, vp])):
+            ("strata_block_norm_backward", it, [norm] + [vp] * 15 + [sz, vp]),
+            ("strata_moe_balance_workspace_bytes", sz, [i32, i32, i32]),
+            ("strata_moe_balance", it, [vp, it, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+            ("strata_moe_balance_backward", it, [vp, it, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+            ("strata_embed", it, [vp, it, i32, i32, vp, i32, fl, vp, it, vp]),
+            ("strata_embed_backward_workspace_bytes", sz, [i32, i32, i32]),
+            ("strata_embed_backward", it, [vp, it, vp, i32, i32, i32, fl, vp, it, u32, vp, sz, vp]),
+            ("strata_vocab_loss_workspace_bytes", sz, [i32, i32, i32]),
+            ("strata_vocab_loss_backward_workspace_bytes", sz, [i32, i32, i32]),
+            ("strata_vocab_loss", it, [vp, vp, vp, i32, i32, i32, vp, vp, vp, sz, vp]),
+            ("strata_vocab_loss_backward", it,
+             [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, it, vp, it, u32, vp, sz, vp]),
+            ("strata_orthogonalise_workspace_bytes", sz, [i32, i32, i32]),
+            ("strata_orthogonalise", it, [vp, it, i32, i32, i32, i32, ctypes.POINTER(fl), fl, fl, vp, vp, sz, vp])):
         f = getattr(lib, name)
         f.restype = restype
         f.argtypes = argtypes
@@ -102,7 +121,9 @@ class _Unloaded:
 _native = _Unloaded()
 _BOUND = ("strata_moe_sort", "strata_moe_dispatch", "strata_moe_dispatch_backward", "strata_moe_combine",
           "strata_moe_combine_backward", "strata_moe_grouped_product", "strata_moe_grouped_dgrad",
-          "strata_moe_grouped_wgrad", "strata_block_norm", "strata_block_norm_backward")   # in _binding's order
+          "strata_moe_grouped_wgrad", "strata_block_norm", "strata_block_norm_backward", "strata_moe_balance",
+          "strata_moe_balance_backward", "strata_embed", "strata_embed_backward", "strata_vocab_loss",
+          "strata_vocab_loss_backward", "strata_orthogonalise")   # in _binding's order
 
 
 def _int32(bits: int):
@@ -197,3 +218,75 @@ def block_norm_backward(args: BlockNormArgs, dr, du, r, y, gate=None, g_post=Non
     """Gradients of block_norm's rows, gate and gains (see strata_block_norm_backward)."""
     _native.block_norm_backward(args, dr, du, r, y, gate, g_post, g_pre, rstd_y, rstd_r, dx, dy, dgate, dg_post, dg_pre,
                                 ws, ws_bytes, stream)
+
+
+# ------------------------------------------------ the ends of a training step
+
+def _workspace(name: str, what: str, a: int, b: int, c: int) -> int:
+    _int32(a | b | c)
+    n = getattr(_lib(), name)(a, b, c)
+    if n == 0:
+        _raise(f"unsupported {what}")
+    return n
+
+
+def balance_loss_workspace_bytes(T: int, k: int, n_experts: int) -> int:
+    return _workspace("strata_moe_balance_workspace_bytes", "balance loss", T, k, n_experts)
+
+
+def balance_loss(z, zdtype: int, idx, T: int, k: int, n_experts: int, losses, counts, lse, tokens, ws, ws_bytes: int,
+                 prob=None, keep=None, stream=None):
+    """Balance and z loss of a router's logits, its picks counted per expert (see strata_moe_balance)."""
+    _native.balance_loss(z, zdtype, idx, T, k, n_experts, losses, counts, lse, tokens, ws, ws_bytes, prob, keep, stream)
+
+
+def balance_loss_backward(z, zdtype: int, idx, T: int, k: int, n_experts: int, lse, counts, tokens, dlosses, dz, keep=None,
+                          dpicks=None, stream=None):
+    """The logits' gradient, that of the picked logits added (see strata_moe_balance_backward)."""
+    _native.balance_loss_backward(z, zdtype, idx, T, k, n_experts, lse, counts, tokens, dlosses, dz, keep, dpicks, stream)
+
+
+def embed(W, wdtype: int, V: int, d: int, ids, T: int, scale: float, out, odtype: int, stream=None):
+    """out[t] = scale * W[ids[t]] (see strata_embed)."""
+    _native.embed(W, wdtype, V, d, ids, T, scale, out, odtype, stream)
+
+
+def embed_backward_workspace_bytes(T: int, V: int, d: int) -> int:
+    return _workspace("strata_embed_backward_workspace_bytes", "embedding", T, V, d)
+
+
+def embed_backward(dout, odtype: int, ids, T: int, V: int, d: int, scale: float, dW, wdtype: int, ws, ws_bytes: int,
+                   flags: int = 0, stream=None):
+    """dW[v] = scale * sum of dout[t] over the tokens of id v (see strata_embed_backward)."""
+    _native.embed_backward(dout, odtype, ids, T, V, d, scale, dW, wdtype, ws, ws_bytes, flags, stream)
+
+
+def vocab_loss_workspace_bytes(T: int, V: int, d: int) -> int:
+    return _workspace("strata_vocab_loss_workspace_bytes", "vocabulary loss", T, V, d)
+
+
+def vocab_loss(h, W, targets, T: int, V: int, d: int, loss, lse, ws, ws_bytes: int, stream=None):
+    """Softmax cross entropy of W h[t] at targets[t] (see strata_vocab_loss)."""
+    _native.vocab_loss(h, W, targets, T, V, d, loss, lse, ws, ws_bytes, stream)
+
+
+def vocab_loss_backward_workspace_bytes(T: int, V: int, d: int) -> int:
+    return _workspace("strata_vocab_loss_backward_workspace_bytes", "vocabulary loss", T, V, d)
+
+
+def vocab_loss_backward(h, W, targets, T: int, V: int, d: int, lse, dloss, ws, ws_bytes: int, dlse=None, dh=None,
+                        dhdtype: int = 0, dW=None, dwdtype: int = 0, flags: int = 0, stream=None):
+    """Gradients of the hidden rows and of the output matrix (see strata_vocab_loss_backward)."""
+    _native.vocab_loss_backward(h, W, targets, T, V, d, lse, dloss, ws, ws_bytes, dlse, dh, dhdtype, dW, dwdtype, flags,
+                                stream)
+
+
+def orthogonalise_workspace_bytes(n: int, N: int, K: int) -> int:
+    return _workspace("strata_orthogonalise_workspace_bytes", "matrices", n, N, K)
+
+
+def orthogonalise(G, gdtype: int, n: int, N: int, K: int, out, ws, ws_bytes: int, steps: int = 5,
+                  coefficients=(3.4445, -4.7750, 2.0315), scale: float = 1.0, eps: float = 1e-7, stream=None):
+    """out = scale * the matrices of G orthogonalised by Newton-Schulz products (see strata_orthogonalise)."""
+    a, b, c = coefficients
+    _native.orthogonalise(G, gdtype, n, N, K, out, ws, ws_bytes, steps, a, b, c, scale, eps, stream)
