@@ -1,12 +1,13 @@
 // Balance losses of a router with the picks counted per expert, and the
 // logits' gradient (strata_moe_balance, strata_moe_balance_backward).
 //
-// Both read the logits once: a wave takes a token, the row lies in its
-// registers (up to 16 values a lane).  Forward, a lane adds its experts'
-// probabilities over all tokens of the wave; the waves of a block are added
-// in LDS, the blocks by a second launch, whose last block sums the losses
-// over the experts.  No sum depends on the order in which blocks run.  A
-// call of few tokens is one block of one launch.
+// Both read the logits once: 16 to 64 lanes take a token, its row lies in
+// their registers, 16 values a lane (so that a wave meets up to four tokens
+// and their reductions run side by side).  Forward, a lane adds its experts'
+// probabilities over all tokens it meets; the lanes of a block are added in
+// LDS, the blocks by a second launch, whose last block sums the losses over
+// the experts.  No sum depends on the order in which blocks run.  A call of
+// few tokens is one block of one launch.
 #include "ops.hpp"
 
 namespace strata {
@@ -15,7 +16,8 @@ constexpr int BAL_E = 1024;          // most experts
 constexpr int BAL_WAVES = 8;         // of a block
 constexpr int BAL_BLOCKS = 512;      // most blocks of the forward launch
 constexpr int BAL_ONE = 64;          // tokens up to which one block does it all
-constexpr int BAL_SLAB = 64;         // experts of a block of the second launch
+constexpr int BAL_C = 16;            // values of a row a lane holds
+constexpr int BAL_SLAB = 16;         // experts of a block of the second launch
 constexpr int BAL_SLABS = BAL_E / BAL_SLAB;
 
 struct BalanceArgs {
@@ -46,69 +48,88 @@ __device__ __forceinline__ float exp_of(float x) {
     return y > -126.f ? fmaf(e, r * LN2, e) : e;   // far down e is 0, and r may be NaN at -inf
 }
 
-// C values of token t: value j of piece i is expert (64 i + lane) V + j; -inf behind the last one.
-template <typename Z, int V, int C> struct LogitRow {
-    Raw<Z, V> raw[C / V];
-    __device__ __forceinline__ static int expert(int i) { return (64 * i + (int)(threadIdx.x & 63)) * V; }
+// Sum and maximum over the P lanes of a token, in all of them.
+template <int P> __device__ __forceinline__ float row_sum(float v) {
+    if constexpr (P > 32) v += lane_xor<32>(v);
+    if constexpr (P > 16) v += lane_xor<16>(v);
+    v += lane_xor<8>(v);
+    v += lane_xor<4>(v);
+    v += lane_xor<2>(v);
+    return v + lane_xor<1>(v);
+}
+template <int P> __device__ __forceinline__ float row_max(float v) {
+    if constexpr (P > 32) v = fmaxf(v, lane_xor<32>(v));
+    if constexpr (P > 16) v = fmaxf(v, lane_xor<16>(v));
+    v = fmaxf(v, lane_xor<8>(v));
+    v = fmaxf(v, lane_xor<4>(v));
+    v = fmaxf(v, lane_xor<2>(v));
+    return fmaxf(v, lane_xor<1>(v));
+}
+// Whether any of the P lanes of this lane's token says so.
+template <int P> __device__ __forceinline__ bool row_any(bool v) {
+    const uint64_t m = __ballot(v);
+    return P == 64 ? m != 0 : (m >> (threadIdx.x & (64 - P)) & ((1ull << (P & 63)) - 1)) != 0;
+}
+
+// A token's logits over P lanes: value j of piece i is expert (P i + lane) V + j; -inf behind the last one.
+template <typename Z, int V, int P> struct LogitRow {
+    Raw<Z, V> raw[BAL_C / V];
+    __device__ __forceinline__ static int expert(int i) { return (P * i + (int)(threadIdx.x % P)) * V; }
     __device__ __forceinline__ void load(const Z *z, int64_t t, int E) {
 #pragma unroll
-        for (int i = 0; i < C / V; ++i)
-            if (expert(i) < E) load_raw<V>(z, t * E + expert(i), raw[i]);
+        for (int i = 0; i < BAL_C / V; ++i)
+            if (expert(i) < E) load_raw<V, true>(z, t * E + expert(i), raw[i]);
     }
-    __device__ __forceinline__ void values(int E, float (&v)[C]) const {
+    __device__ __forceinline__ void values(int E, float (&v)[BAL_C]) const {
 #pragma unroll
-        for (int i = 0; i < C / V; ++i)
+        for (int i = 0; i < BAL_C / V; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i * V + j] = expert(i) < E ? value<V>(raw[i], j) : -INFINITY;
     }
 };
 
-template <typename Z, int V, int C>
-__global__ __launch_bounds__(64 * BAL_WAVES) void balance_rows_kernel(BalanceArgs a) {
-    __shared__ float red[BAL_WAVES][64 * C];
+// Lanes of the tokens that do not count go along with zeros, so that the reductions run in whole waves.
+template <typename Z, int V, int P> __global__ __launch_bounds__(64 * BAL_WAVES) void balance_rows_kernel(BalanceArgs a) {
+    constexpr int C = BAL_C, W = BAL_WAVES, ROWS = 64 / P;   // tokens of a wave at a time
+    __shared__ float red[W][P * C];
     __shared__ int hist[BAL_E];
-    __shared__ float zred[BAL_WAVES];
-    __shared__ int nred[BAL_WAVES];
-    const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6);
-    for (int e = th; e < a.E; e += 64 * BAL_WAVES) hist[e] = 0;
+    __shared__ float zred[W];
+    __shared__ int nred[W];
+    const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6), place = lane % P;
+    for (int e = th; e < a.E; e += 64 * W) hist[e] = 0;
     __syncthreads();
-    const int first = blockIdx.x * BAL_WAVES + w, step = a.blocks * BAL_WAVES;
-    const auto counted = [&](int t) { return t < a.T && (!a.keep || a.keep[t]); };
+    const int step = a.blocks * W * ROWS;
+    const auto counted = [&](int64_t t) { return t < a.T && (!a.keep || a.keep[t]); };
     float acc[C], zz = 0.f;
     int n = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    LogitRow<Z, V, C> row;
+    LogitRow<Z, V, P> row;
     int pick = -1;
-    bool on = counted(first);
-    const auto fetch = [&](int t) {
-        row.load((const Z *)a.z, t, a.E);
-        pick = lane < a.k ? a.idx[(int64_t)t * a.k + lane] : -1;
+    int64_t t = (int64_t)(blockIdx.x * W + w) * ROWS + lane / P;
+    const int64_t first = (int64_t)(blockIdx.x * W + w) * ROWS;   // the wave's first token decides its trips
+    bool on = counted(t);
+    const auto fetch = [&](int64_t u) {
+        row.load((const Z *)a.z, u, a.E);
+        pick = place < a.k ? a.idx[u * a.k + place] : -1;
     };
-    if (on) fetch(first);
-    for (int64_t t = first; t < a.T; t += step) {
+    if (on) fetch(t);
+    for (int64_t f = first; f < a.T; f += step, t += step) {
         float v[C];
         const int e = pick;
-        const bool here = on;
-        if (here) row.values(a.E, v);
-        on = t + step < a.T && counted((int)(t + step));
-        if (on) fetch((int)(t + step));
-        if (!here) {
-            if (lane == 0) a.lse[t] = 0.f;
-            continue;
-        }
+        bool here = on;
+        row.values(a.E, v);
+        on = counted(t + step);
+        if (on) fetch(t + step);
         float m = v[0];
 #pragma unroll
         for (int c = 1; c < C; ++c) m = fmaxf(m, v[c]);
-        m = wave_max(m);
+        m = row_max<P>(m);
         if (m == -INFINITY) {   // nothing there, or NaN beside nothing
             bool nan = false;
 #pragma unroll
             for (int c = 0; c < C; ++c) nan |= v[c] != v[c];
-            if (!__any(nan)) {
-                if (lane == 0) a.lse[t] = 0.f;
-                continue;
-            }
+            here = row_any<P>(nan) && here;
         }
         float s = 0.f;
 #pragma unroll
@@ -116,19 +137,32 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_rows_kernel(BalanceArg
             v[c] = exp_of(v[c] - m);
             s += v[c];
         }
-        s = wave_sum(s);
+        s = row_sum<P>(s);
         const float lse = m + logf(s), r = 1.f / s;
+        if (here) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = fmaf(v[c], r, acc[c]);
-        zz = fmaf(lse, lse, zz);
-        ++n;
-        if (lane == 0) a.lse[t] = lse;
-        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&hist[e], 1);
+            for (int c = 0; c < C; ++c) acc[c] = fmaf(v[c], r, acc[c]);
+            if (place == 0) {
+                zz = fmaf(lse, lse, zz);
+                ++n;
+            }
+            if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&hist[e], 1);
+        }
+        if (place == 0 && t < a.T) a.lse[t] = here ? lse : 0.f;
     }
+    zz = wave_sum(zz);
+    n = wave_sum(n);
 #pragma unroll
-    for (int i = 0; i < C / V; ++i)
+    for (int c = 0; c < C; ++c) {   // the wave's tokens, side by side
+        if constexpr (P <= 16) acc[c] += lane_xor<16>(acc[c]);
+        if constexpr (P <= 32) acc[c] += lane_xor<32>(acc[c]);
+    }
+    if (lane < P) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) red[w][LogitRow<Z, V, C>::expert(i) + j] = acc[i * V + j];
+        for (int i = 0; i < C / V; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) red[w][LogitRow<Z, V, P>::expert(i) + j] = acc[i * V + j];
+    }
     if (lane == 0) {
         zred[w] = zz;
         nred[w] = n;
@@ -137,16 +171,16 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_rows_kernel(BalanceArg
     float z = 0.f;
     n = 0;
 #pragma unroll
-    for (int q = 0; q < BAL_WAVES; ++q) {
+    for (int q = 0; q < W; ++q) {
         z += zred[q];
         n += nred[q];
     }
     const bool one = a.blocks == 1;
     float dot = 0.f;
-    for (int e = th; e < a.E; e += 64 * BAL_WAVES) {
+    for (int e = th; e < a.E; e += 64 * W) {
         float p = 0.f;
 #pragma unroll
-        for (int q = 0; q < BAL_WAVES; ++q) p += red[q][e];
+        for (int q = 0; q < W; ++q) p += red[q][e];
         const int c = hist[e];
         if (one) {
             p = n ? p / (float)n : 0.f;
@@ -166,7 +200,7 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_rows_kernel(BalanceArg
         if (th == 0) {
             float d = 0.f;
 #pragma unroll
-            for (int q = 0; q < BAL_WAVES; ++q) d += zred[q];
+            for (int q = 0; q < W; ++q) d += zred[q];
             a.losses[0] = n ? d * (float)a.E / ((float)n * (float)a.k) : 0.f;
             a.losses[1] = n ? z / (float)n : 0.f;
             *a.tokens = n;
@@ -178,29 +212,34 @@ __global__ __launch_bounds__(64 * BAL_WAVES) void balance_rows_kernel(BalanceArg
     }
 }
 
-// 64 experts to a block: 16 waves share the blocks' sums.  The block that takes
-// the last ticket sums the losses, in the order of the slabs.
+// 16 experts to a block: its 64 groups of 16 lanes share the blocks' sums.  The
+// block that takes the last ticket sums the losses, in the order of the slabs.
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
     __shared__ float pw[16][BAL_SLAB];
     __shared__ int cw[16][BAL_SLAB];
     __shared__ float zw[16];
     __shared__ int nw[16];
     const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6);
-    const int e = blockIdx.x * BAL_SLAB + lane, ec = min(e, a.E - 1);
+    const int col = th % BAL_SLAB, e = blockIdx.x * BAL_SLAB + col, ec = min(e, a.E - 1);
     float p = 0.f;
     int c = 0;
-    const int per = (a.blocks + 15) / 16, b0 = w * per, b1 = min(b0 + per, a.blocks);
 #pragma unroll 8
-    for (int b = b0; b < b1; ++b) {
+    for (int b = th / BAL_SLAB; b < a.blocks; b += 1024 / BAL_SLAB) {
         p += a.psum[(int64_t)b * a.E + ec];
         c += a.csum[(int64_t)b * a.E + ec];
     }
-    pw[w][lane] = p;
-    cw[w][lane] = c;
     float z = th < a.blocks ? a.zsum[th] : 0.f;
     int n = th < a.blocks ? a.nsum[th] : 0;
+    p += lane_xor<16>(p);
+    p += lane_xor<32>(p);
+    c += lane_xor<16>(c);
+    c += lane_xor<32>(c);
     z = wave_sum(z);
     n = wave_sum(n);
+    if (lane < BAL_SLAB) {
+        pw[w][lane] = p;
+        cw[w][lane] = c;
+    }
     if (lane == 0) {
         zw[w] = z;
         nw[w] = n;
@@ -215,29 +254,30 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a) {
     for (int q = 0; q < 16; ++q) {
         z += zw[q];
         n += nw[q];
-        p += pw[q][lane];
-        c += cw[q][lane];
+        p += pw[q][col];
+        c += cw[q][col];
     }
     p = n ? p / (float)n : 0.f;
     float dot = 0.f;
-    if (e < a.E) {
+    if (e < a.E && lane < BAL_SLAB) {
         a.counts[e] = c;
         if (a.prob) a.prob[e] = p;
         dot = (float)c * p;
     }
     dot = wave_sum(dot);
+    int last = 0;
     if (lane == 0) {
         __hip_atomic_store(&a.dots[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const bool last =
-            __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
-        if (last) {
-            float d = 0.f;
-            for (int q = 0; q < (int)gridDim.x; ++q)
-                d += __hip_atomic_load(&a.dots[q], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            a.losses[0] = n ? d * (float)a.E / ((float)n * (float)a.k) : 0.f;
-            a.losses[1] = n ? z / (float)n : 0.f;
-            *a.tokens = n;
-        }
+        last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+    }
+    if (!__builtin_amdgcn_readfirstlane(last)) return;
+    dot = lane < (int)gridDim.x ? __hip_atomic_load(&a.dots[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
+    static_assert(BAL_SLABS <= 64, "a lane for every slab");
+    dot = wave_sum(dot);
+    if (lane == 0) {
+        a.losses[0] = n ? dot * (float)a.E / ((float)n * (float)a.k) : 0.f;
+        a.losses[1] = n ? z / (float)n : 0.f;
+        *a.tokens = n;
     }
 }
 
@@ -253,13 +293,15 @@ struct BalanceBack {
 };
 
 // g is the same for every token and stays in registers.  The picks' gradients
-// reach their experts through a row of LDS per wave: lane r holds pick r, the
-// first of equal picks adds up all of them in order.
-template <typename Z, int V, int C>
-__global__ __launch_bounds__(256) void balance_back_kernel(BalanceBack a) {
+// reach their experts through a row of LDS per token: lane r of the token
+// holds pick r (P is k at least), the first of equal picks adds up all of them
+// in order.
+template <typename Z, int V, int P> __global__ __launch_bounds__(256) void balance_back_kernel(BalanceBack a) {
+    constexpr int C = BAL_C, ROWS = 64 / P;
     __shared__ __attribute__((aligned(16))) float add[4][64 * C];
-    const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6);
-    typedef LogitRow<Z, V, C> Row;
+    const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6), place = lane % P;
+    typedef LogitRow<Z, V, P> Row;
+    float *const mine = &add[w][(lane / P) * P * C];   // this token's row
 #pragma unroll
     for (int c = 0; c < C; ++c) add[w][c * 64 + lane] = 0.f;
     const float n = fmaxf((float)*a.tokens, 1.f);
@@ -269,77 +311,71 @@ __global__ __launch_bounds__(256) void balance_back_kernel(BalanceBack a) {
     for (int i = 0; i < C / V; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) g[i * V + j] = Row::expert(i) < a.E ? scale * (float)a.counts[Row::expert(i) + j] : 0.f;
-    const int step = a.blocks * 4;
+    const int step = a.blocks * 4 * ROWS;
     const auto counted = [&](int64_t t) { return t < a.T && (!a.keep || a.keep[t]); };
     Row row;
     float lse = 0.f, up = 0.f;
     int pick = -1;
-    int64_t t = blockIdx.x * 4 + w;
+    int64_t t = (int64_t)(blockIdx.x * 4 + w) * ROWS + lane / P;
     const auto fetch = [&](int64_t u) {
         row.load((const Z *)a.z, u, a.E);
         lse = a.lse[u];
-        if (a.dpicks && lane < a.k) {
-            pick = a.idx[u * a.k + lane];
-            up = a.dpicks[u * a.k + lane];
+        if (a.dpicks && place < a.k) {
+            pick = a.idx[u * a.k + place];
+            up = a.dpicks[u * a.k + place];
         }
     };
     bool on = counted(t);
     if (on) fetch(t);
-    for (; t < a.T; t += step) {
+    for (int64_t f = (int64_t)(blockIdx.x * 4 + w) * ROWS; f < a.T; f += step, t += step) {
         float v[C];
-        const float l = lse, mine = up;
+        const float l = lse, u = up;
         const int e = pick;
         bool here = on;
-        if (here) row.values(a.E, v);
+        row.values(a.E, v);
         on = counted(t + step);
         if (on) fetch(t + step);
-        if (here && l == 0.f) {   // a row of -inf has lse 0 too
-            bool any = false;
+        bool any = l != 0.f;   // a row of -inf has lse 0 too
 #pragma unroll
-            for (int c = 0; c < C; ++c) any |= v[c] != -INFINITY;
-            here = __any(any);
+        for (int c = 0; c < C; ++c) any |= v[c] != -INFINITY;
+        here = row_any<P>(any) && here;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            v[c] = exp_of(v[c] - l);
+            s = fmaf(v[c], g[c], s);
         }
-        if (!here) {
+        s = row_sum<P>(s) - zscale * l;
 #pragma unroll
-            for (int c = 0; c < C; ++c) v[c] = 0.f;
-        } else {
-            float s = 0.f;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                v[c] = exp_of(v[c] - l);
-                s = fmaf(v[c], g[c], s);
+        for (int c = 0; c < C; ++c) v[c] = here ? v[c] * (g[c] - s) : 0.f;
+        if (a.dpicks) {
+            float sum = 0.f;
+            bool before = false;
+            for (int r = 0; r < a.k; ++r) {
+                const int er = __shfl(e, r, P);
+                const float ur = __shfl(u, r, P);
+                sum += er == e ? ur : 0.f;
+                before |= er == e && r < place;
             }
-            s = wave_sum(s) - zscale * l;
+            const bool adds = here && place < a.k && (uint32_t)e < (uint32_t)a.E && !before;
+            if (adds) mine[e] = sum;
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int c = 0; c < C; ++c) v[c] *= g[c] - s;
-            if (a.dpicks) {
-                const bool in = lane < a.k && (uint32_t)e < (uint32_t)a.E;
-                float sum = 0.f;
-                bool before = false;
-                for (int r = 0; r < a.k; ++r) {
-                    const int er = __builtin_amdgcn_readlane(e, r);
-                    const float ur = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), r));
-                    sum += er == e ? ur : 0.f;
-                    before |= er == e && r < lane;
-                }
-                const bool adds = in && !before;
-                if (adds) add[w][e] = sum;
-                __builtin_amdgcn_wave_barrier();
+            for (int i = 0; i < C / V; ++i)
 #pragma unroll
-                for (int i = 0; i < C / V; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) v[i * V + j] += add[w][Row::expert(i) + j];
-                __builtin_amdgcn_wave_barrier();
-                if (adds) add[w][e] = 0.f;
-                __builtin_amdgcn_wave_barrier();
-            }
+                for (int j = 0; j < V; ++j) v[i * V + j] += mine[Row::expert(i) + j];
+            __builtin_amdgcn_wave_barrier();
+            if (adds) mine[e] = 0.f;
+            __builtin_amdgcn_wave_barrier();
         }
+        if (t < a.T) {
 #pragma unroll
-        for (int i = 0; i < C / V; ++i) {
-            float q[V];
+            for (int i = 0; i < C / V; ++i) {
+                float q[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) q[j] = v[i * V + j];
-            if (Row::expert(i) < a.E) store_values<V>((Z *)a.dz, t * a.E + Row::expert(i), q);
+                for (int j = 0; j < V; ++j) q[j] = v[i * V + j];
+                if (Row::expert(i) < a.E) store_values<V, true>((Z *)a.dz, t * a.E + Row::expert(i), q);
+            }
         }
     }
 }
@@ -353,42 +389,44 @@ strata_status check_balance(int32_t T, int32_t k, int32_t E) {
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 
-// Blocks of the forward launch: a wave's tokens share the block's way through LDS and memory.
-int balance_blocks(int T) {
+// Lanes of a token: 16 values each hold its row, and a lane each its picks.
+int balance_lanes(int E, int k) { return E > 512 ? 64 : E > 256 || k > 16 ? 32 : 16; }
+
+// Blocks of the forward launch: a few trips of its waves share the block's way through LDS and memory.
+int balance_blocks(int T, int E, int k) {
     if (T <= BAL_ONE) return 1;
-    const int b = (T + 2 * BAL_WAVES - 1) / (2 * BAL_WAVES);
+    const int rows = BAL_WAVES * (64 / balance_lanes(E, k)), b = (T + 2 * rows - 1) / (2 * rows);
     return b < BAL_BLOCKS ? b : BAL_BLOCKS;
 }
 
 size_t part_bytes(int64_t n) { return (size_t)((n * 4 + 255) / 256 * 256); }
 
-// C values a lane hold the row, in pieces of V.
 template <template <typename, int, int> class F, typename Z, int V, typename A> void by_length(const A &a, hipStream_t s) {
-    if constexpr (V <= 4) {
-        if (a.E <= 256) return F<Z, V, 4>::run(a, s);
+    switch (balance_lanes(a.E, a.k)) {
+        case 16: return F<Z, V, 16>::run(a, s);
+        case 32: return F<Z, V, 32>::run(a, s);
+        default: F<Z, V, 64>::run(a, s);
     }
-    if (a.E <= 512) return F<Z, V, 8>::run(a, s);
-    F<Z, V, 16>::run(a, s);
 }
 
 // The widest pieces that divide the row.
 template <template <typename, int, int> class F, typename Z, typename A> void by_width(const A &a, hipStream_t s) {
     if constexpr (sizeof(Z) == 2) {
-        if (a.E % 8 == 0 && a.E > 256) return by_length<F, Z, 8>(a, s);
+        if (a.E % 8 == 0) return by_length<F, Z, 8>(a, s);
     }
     if (a.E % 4 == 0) return by_length<F, Z, 4>(a, s);
     if (a.E % 2 == 0) return by_length<F, Z, 2>(a, s);
     by_length<F, Z, 1>(a, s);
 }
 
-template <typename Z, int V, int C> struct Rows {
+template <typename Z, int V, int P> struct Rows {
     static void run(const BalanceArgs &a, hipStream_t s) {
-        STRATA_LAUNCH((balance_rows_kernel<Z, V, C>), dim3(a.blocks), dim3(64 * BAL_WAVES), 0, s, a);
+        STRATA_LAUNCH((balance_rows_kernel<Z, V, P>), dim3(a.blocks), dim3(64 * BAL_WAVES), 0, s, a);
     }
 };
-template <typename Z, int V, int C> struct Back {
+template <typename Z, int V, int P> struct Back {
     static void run(const BalanceBack &a, hipStream_t s) {
-        STRATA_LAUNCH((balance_back_kernel<Z, V, C>), dim3(a.blocks), dim3(256), 0, s, a);
+        STRATA_LAUNCH((balance_back_kernel<Z, V, P>), dim3(a.blocks), dim3(256), 0, s, a);
     }
 };
 
@@ -402,7 +440,7 @@ extern "C" {
 
 size_t strata_moe_balance_workspace_bytes(int32_t T, int32_t k, int32_t n_experts) {
     if (check_balance(T, k, n_experts) != STRATA_OK) return 0;
-    const int b = balance_blocks(T);
+    const int b = balance_blocks(T, n_experts, k);
     return b == 1 ? 256 : 2 * part_bytes((int64_t)b * n_experts) + 2 * part_bytes(b) + part_bytes(BAL_SLABS) + 256;
 }
 
@@ -416,7 +454,7 @@ strata_status strata_moe_balance(const void *z, strata_xdtype zdtype, const int3
         return STRATA_EINVAL;
     if (T > 0 && (bad_rows(z) || !idx || !aligned4(idx) || !lse || !aligned4(lse) || bad_rows(ws))) return STRATA_EINVAL;
     if (T > 0 && ws_bytes < strata_moe_balance_workspace_bytes(T, k, n_experts)) return STRATA_EWORKSPACE;
-    BalanceArgs a{z, idx, keep, T, k, n_experts, balance_blocks(T), losses, counts, prob, lse, tokens};
+    BalanceArgs a{z, idx, keep, T, k, n_experts, balance_blocks(T, n_experts, k), losses, counts, prob, lse, tokens};
     const hipStream_t s = (hipStream_t)stream;
     if (a.blocks > 1) {
         char *p = (char *)ws;
@@ -450,8 +488,8 @@ strata_status strata_moe_balance_backward(const void *z, strata_xdtype zdtype, c
     if (bad_rows(z) || bad_rows(dz) || !lse || !counts || !tokens || !dlosses || !aligned4(lse) || !aligned4(counts) ||
         !aligned4(tokens) || !aligned4(dlosses) || !aligned4(dpicks) || (dpicks && (!idx || !aligned4(idx))))
         return STRATA_EINVAL;
-    const int64_t want = ((int64_t)T + 3) / 4;
-    BalanceBack a{z, idx, keep, T, k, n_experts, (int)(want < 2048 ? want : 2048), lse, counts, tokens, dlosses, dpicks, dz};
+    const int64_t rows = 4 * (64 / balance_lanes(n_experts, k)), want = (T + rows - 1) / rows;
+    BalanceBack a{z, idx, keep, T, k, n_experts, (int)(want < 1024 ? want : 1024), lse, counts, tokens, dlosses, dpicks, dz};
     if (zdtype == STRATA_X_BF16) by_width<Back, uint16_t>(a, (hipStream_t)stream);
     else by_width<Back, float>(a, (hipStream_t)stream);
     return hip_status(hipGetLastError());

@@ -142,14 +142,10 @@ template <typename W, int V> __global__ __launch_bounds__(256) void embed_join_k
     if (id < 0 || id_at(p1) != id) return;                                            // no run leaves the chunk
     const int p0 = c * EB_ROWS;
     if (p0 > 0 && id_at(p0) == id && id_at(p0 - 1) == id) return;                     // it started before
-    int lo = p1, hi = a.T;   // the run's last position is in lo..hi-1
-    while (hi - lo > 1) {
-        const int m = lo + (hi - lo) / 2, v = id_at(m);
-        if (v == id) lo = m;
-        else hi = m;   // larger ids, and -1 behind them all
-    }
-    const int last = lo / EB_ROWS, n = last - c;   // heads of chunks c+1 .. last
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    int n = 0;   // chunks behind this one that begin with the run: 64 at a time
+    for (uint64_t m = ~0ull; m == ~0ull; n += __popcll(m)) m = __ballot(id_at((c + 1 + n + lane) * EB_ROWS) == id);
+    const int last = c + n, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int per = (n + 3) / 4, b0 = c + 1 + w * per, b1 = min(b0 + per, last + 1);
     for (int i0 = blockIdx.y * 64 * V; i0 < a.d; i0 += gridDim.y * 64 * V) {
         const int i = i0 + lane * V;
@@ -188,11 +184,21 @@ template <typename W, int V> __global__ __launch_bounds__(256) void embed_join_k
     }
 }
 
-// n 16-byte pieces of zeros, and the bytes behind them.
-__global__ __launch_bounds__(256) void embed_zero_kernel(u32x4_t *p, int64_t n, int rest) {
-    const int64_t step = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) put<true>(p + i, u32x4_t{0, 0, 0, 0});
-    if (blockIdx.x == 0 && (int)threadIdx.x < rest) ((uint8_t *)(p + n))[threadIdx.x] = 0;
+// n 16-byte pieces of zeros, and the bytes behind them: the share of block b of nb.
+__device__ __forceinline__ void embed_zeros(u32x4_t *p, int64_t n, int rest, int b, int nb) {
+    const int64_t step = (int64_t)nb * SORT_TH;
+    for (int64_t i = (int64_t)b * SORT_TH + threadIdx.x; i < n; i += step) p[i] = u32x4_t{0, 0, 0, 0};
+    if (b == 0 && (int)threadIdx.x < rest) ((uint8_t *)(p + n))[threadIdx.x] = 0;
+}
+
+__global__ __launch_bounds__(SORT_TH) void embed_zero_kernel(u32x4_t *p, int64_t n, int rest) {
+    embed_zeros(p, n, rest, blockIdx.x, gridDim.x);
+}
+
+// A pass of the sort, and beside it, on the CUs that the sort leaves idle, zeros for a part of the table.
+__global__ __launch_bounds__(SORT_TH) void embed_sort_kernel(SortArgs a, TokenKey key, int copies, u32x4_t *p, int64_t n, int rest) {
+    if ((int)blockIdx.x < a.blocks) sort_once(a, key, copies);
+    else embed_zeros(p, n, rest, blockIdx.x - a.blocks, gridDim.x - a.blocks);
 }
 
 namespace {
@@ -273,6 +279,23 @@ SortArgs pass_plan(int T, int E) {
     return a;
 }
 
+// n pieces of zeros and the bytes behind them.
+struct Zeros {
+    u32x4_t *p;
+    int64_t n;
+    int rest;
+};
+unsigned zero_blocks(int64_t n) {
+    const int64_t b = (n + SORT_TH - 1) / SORT_TH;
+    return (unsigned)(b < 1 ? 1 : b < 2048 ? b : 2048);
+}
+
+hipError_t sort_beside(const SortArgs &a, const TokenKey &key, const Zeros &z, hipStream_t s) {
+    const unsigned more = z.n || z.rest ? zero_blocks(z.n) : 0;
+    STRATA_LAUNCH(embed_sort_kernel, dim3(a.blocks + more), dim3(SORT_TH), 0, s, a, key, sort_copies(a), z.p, z.n, z.rest);
+    return hipGetLastError();
+}
+
 struct BackPlan {
     int chunks;
     size_t order, half, counts, head, tail, bytes;   // offsets of the workspace's parts
@@ -335,28 +358,31 @@ strata_status strata_embed_backward(const void *dout, strata_xdtype odtype, cons
     if (T > 0 && (overlap(dW, bytes, ws, p.bytes) || overlap(dW, bytes, ids, (size_t)T * 4) ||
                   overlap(ws, p.bytes, ids, (size_t)T * 4)))
         return STRATA_EINVAL;
-    if (!add) {
-        const int64_t n = bytes / 16, blocks = (n + 255) / 256;
-        STRATA_LAUNCH(embed_zero_kernel, dim3((unsigned)(blocks < 1 ? 1 : blocks < 8192 ? blocks : 8192)), dim3(256), 0, s,
-                      (u32x4_t *)dW, n, (int)(bytes % 16));
+    // The zeros: beside the sort's passes where those are one launch each.
+    const bool two = V > EB_DIGIT, beside = T > 0 && T <= SORT_ONCE;
+    Zeros z{(u32x4_t *)dW, add ? 0 : bytes / 16, add ? 0 : (int)(bytes % 16)};
+    if (!add && !beside) {
+        STRATA_LAUNCH(embed_zero_kernel, dim3(zero_blocks(z.n)), dim3(SORT_TH), 0, s, z.p, z.n, z.rest);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return hip_status(e);
     }
     if (T == 0) return STRATA_OK;
     char *const w = (char *)ws;
     int32_t *order = (int32_t *)(w + p.order);
-    const bool two = V > EB_DIGIT;
     SortArgs a = pass_plan(T, two ? EB_DIGIT : V);
     a.bcnt = (int32_t *)(w + p.counts);
     a.perm = two ? (int32_t *)(w + p.half) : order;
-    hipError_t e = launch_sort(a, TokenKey{ids, nullptr, 0, V}, s);
+    const int64_t n0 = two ? z.n / 2 : z.n;   // pieces of the first pass
+    hipError_t e = beside ? sort_beside(a, TokenKey{ids, nullptr, 0, V}, Zeros{z.p, n0, two ? 0 : z.rest}, s)
+                          : launch_sort(a, TokenKey{ids, nullptr, 0, V}, s);
     if (e != hipSuccess) return hip_status(e);
     if (two) {
         const int32_t *half = a.perm;
         a = pass_plan(T, ((V - 1) >> EB_BITS) + 1);
         a.bcnt = (int32_t *)(w + p.counts);
         a.perm = order;
-        e = launch_sort(a, TokenKey{ids, half, EB_BITS, V}, s);
+        e = beside ? sort_beside(a, TokenKey{ids, half, EB_BITS, V}, Zeros{z.p + n0, z.n - n0, z.rest}, s)
+                   : launch_sort(a, TokenKey{ids, half, EB_BITS, V}, s);
         if (e != hipSuccess) return hip_status(e);
     }
     BackCall c{EmbedBack{dout, ids, order, dW, (float *)(w + p.head), (float *)(w + p.tail), T, d, p.chunks, add, scale}, d, s};

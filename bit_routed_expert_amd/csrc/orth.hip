@@ -13,7 +13,7 @@
 // 1536 x 2048 came out 2% off).
 #include <cmath>
 
-#include "orth_impl.hpp"
+#include "orth_small.hpp"
 
 namespace strata {
 
@@ -143,6 +143,19 @@ template <typename G> hipError_t orth_begin_width(const OrthArgs &a, int steps, 
     return orth_begin<G, 1>(a, steps, s);
 }
 
+// Whether a matrix fits a block: its registers hold X, its LDS the fp16 copy, A and B.
+enum SmallShape { SMALL_NONE, SMALL_128, SMALL_64 };
+SmallShape small_shape(int32_t N, int32_t K) {
+    const int side = N < K ? N : K, longer = N < K ? K : N;
+    return side <= 64 && longer <= 512 ? (longer <= 256 && side > 32 ? SMALL_128 : SMALL_64) : side <= 128 && longer <= 256 ? SMALL_128 : SMALL_NONE;
+}
+
+template <typename G> hipError_t orth_small(const OrthArgs &a, int steps, SmallShape k, hipStream_t s) {
+    if (k == SMALL_128) STRATA_LAUNCH((orth_small_kernel<G, 4, 8, 2, 4>), dim3(a.n), dim3(512), 0, s, a, steps);
+    else STRATA_LAUNCH((orth_small_kernel<G, 2, 16, 1, 8>), dim3(a.n), dim3(512), 0, s, a, steps);
+    return hipGetLastError();
+}
+
 dim3 range_grid(int64_t tiles) { return dim3((unsigned)((tiles + 7) / 8 * 8)); }
 
 template <int BM, int WM, int WN, int ST, int SQUARE, int ACROSS> void square(const OrthArgs &a, hipStream_t s) {
@@ -156,22 +169,30 @@ template <int BM, int BN, int WM, int WN, int ST, int TALL> void step(const Orth
     STRATA_LAUNCH((orth_step_kernel<BM, BN, WM, WN, ST, TALL>), range_grid(a.n * nr * nk), dim3(64 * WM * WN), 0, s, a);
 }
 
+// Tiles of the symmetric products by how many there are (8 waves to a tile of
+// 128, two blocks of two buffers to a CU or one of four; 4 waves to one of 64),
+// us of X X^T and of A^2.  64 square below 112 tiles of 128 (4 of 768 x 768, 84
+// tiles: 8.0 and 8.7 against 9.8 and 11.1; 2 of 512 x 2048, 20: 9.8 and 5.5
+// against 14.9 and 8.9; 1 of 2048 x 2048, 136: 23 and 24 against 18 and 20).  128
+// square with four buffers up to 256 tiles (8 of 2048 x 768, 168: 18.7 and 11.9
+// against 23.2 and 13.4 with two), with two above (32 of 512 x 512, 320: 14.3 and
+// 16.3 against 15.6 and 18.4; 16 of 1536 x 2048, 1248: 112 and 87 against 110 and
+// 91).  256 square, whose tiles are few and all of one length, leaves more CUs
+// idle than its fewer LDS reads save (the latter 123 and 112).
 template <int SQUARE, int ACROSS> hipError_t squares(const OrthArgs &a, hipStream_t s) {
-    const auto tiles = [&](int64_t t) {
-        const int64_t nt = (a.side + t - 1) / t;
-        return a.n * (nt * (nt + 1) / 2);
-    };
-    if (tiles(256) >= 192) square<256, 2, 4, 2, SQUARE, ACROSS>(a, s);
-    else if (tiles(128) >= 192) square<128, 2, 2, 4, SQUARE, ACROSS>(a, s);
-    else square<64, 1, 2, 4, SQUARE, ACROSS>(a, s);
+    const int64_t nt = (a.side + 127) / 128, tiles = a.n * (nt * (nt + 1) / 2);
+    if (tiles < 112) square<64, 2, 2, 4, SQUARE, ACROSS>(a, s);
+    else if (tiles <= 256) square<128, 2, 4, 4, SQUARE, ACROSS>(a, s);
+    else square<128, 2, 4, 2, SQUARE, ACROSS>(a, s);
     return hipGetLastError();
 }
 
 template <int TALL> hipError_t steps_of(const OrthArgs &a, hipStream_t s) {
-    const auto tiles = [&](int64_t r, int64_t c) { return a.n * ((a.N + r - 1) / r) * ((a.K + c - 1) / c); };
-    if (tiles(256, 256) >= 192) step<256, 256, 2, 4, 2, TALL>(a, s);
-    else if (tiles(128, 256) >= 192) step<128, 256, 2, 4, 3, TALL>(a, s);
-    else step<64, 128, 2, 2, 4, TALL>(a, s);
+    const int64_t tiles = a.n * ((a.N + 127) / 128) * ((a.K + 127) / 128);
+    if (tiles < 144) step<64, 128, 2, 2, 4, TALL>(a, s);
+    else if (tiles <= 256) step<128, 128, 2, 2, 4, TALL>(a, s);
+    else if (tiles <= 2048) step<128, 128, 2, 2, 2, TALL>(a, s);
+    else step<128, 256, 2, 4, 3, TALL>(a, s);
     return hipGetLastError();
 }
 
@@ -199,9 +220,9 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     if (bad_rows(G) || bad_rows(out) || bad_rows(ws)) return STRATA_EINVAL;
     const OrthPlan p = orth_plan(n, N, K);
     if (ws_bytes < p.bytes) return STRATA_EWORKSPACE;
-    // Without steps blocks convert G while others still read it: only piece by piece in place.
+    // Blocks read G while others may already store: only a matrix's own place is safe.
     const size_t values = (size_t)n * N * K;
-    if (steps == 0 && !(G == out && gdtype == STRATA_X_BF16) && overlap(G, values * (gdtype == STRATA_X_BF16 ? 2 : 4), out, values * 2))
+    if (!(G == out && gdtype == STRATA_X_BF16) && overlap(G, values * (gdtype == STRATA_X_BF16 ? 2 : 4), out, values * 2))
         return STRATA_EINVAL;
     const hipStream_t s = (hipStream_t)stream;
     char *const w = (char *)ws;
@@ -228,6 +249,9 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     a.c = coefficients[2];
     a.scale = scale;
     a.eps = eps;
+    const SmallShape k = small_shape(N, K);
+    if (k != SMALL_NONE)
+        return hip_status(gdtype == STRATA_X_BF16 ? orth_small<uint16_t>(a, steps, k, s) : orth_small<float>(a, steps, k, s));
     const bool tall = N > K;
     hipError_t e = gdtype == STRATA_X_BF16 ? orth_begin_width<uint16_t>(a, steps, s) : orth_begin_width<float>(a, steps, s);
     for (int i = 0; i < steps && e == hipSuccess; ++i) {

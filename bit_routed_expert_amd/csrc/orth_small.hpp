@@ -1,0 +1,202 @@
+// Orthogonalised updates of small matrices: all steps of a matrix in one block.
+//
+// The shorter side (of up to 32 RT) lies along the rows of X.  X stays in the
+// registers in fp32, in the layout of the products' sums, so a X is where the
+// sum of B X starts from; its fp16 copy, A and B lie in LDS.  X is read both
+// along (X X^T) and, by the transposing reads, across (B X): its 16-byte
+// chunks are permuted by the row so that 8 rows' equal chunks and 4 rows'
+// equal 64-byte pieces lie in different banks.
+//
+// 16 matrices of 128 x 256, 5 steps: 3 launches of tiles a step take 87 us.
+#pragma once
+#include "orth_impl.hpp"
+
+namespace strata {
+
+// Permutation of the chunks of row r: its low three bits differ over 8 rows, bits 2 and 3 over 4.
+__device__ __forceinline__ int small_swz(int r) { return (r & 1) << 2 | (r & 2) | (r >> 2 & 1) | (r & 2) << 2; }
+
+template <int COLS> struct SmallRows {   // LDS rows of COLS fp16 values
+    static constexpr int MASK = COLS >= 128 ? 15 : 7;
+    __device__ __forceinline__ static int at(int r, int chunk) { return r * COLS * 2 + 16 * (chunk ^ (small_swz(r) & MASK)); }
+    // 8 values of row r from 16 kk + 8 (lane / 32) on
+    __device__ __forceinline__ static f16x8_t along(const uint8_t *t, int r, int kk) {
+        return __builtin_bit_cast(f16x8_t, *(const u32x4_t *)(t + at(r, 2 * kk + (int)((threadIdx.x & 63) >> 5))));
+    }
+    // columns n0.. of rows 16 kk..
+    __device__ __forceinline__ static f16x8_t across(const uint8_t *t, int n0, int kk) {
+        const int i = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+        const int c = 16 * kk + 8 * (g >> 1) + (i >> 2), chunk = (n0 >> 3) + 2 * (g & 1) + ((i >> 1) & 1);
+        typedef __attribute__((address_space(3))) s16x4_t lds4;
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(t + at(c, chunk) + 8 * (i & 1)));
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(t + at(c + 4, chunk) + 8 * (i & 1)));
+        return __builtin_bit_cast(f16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    // a subtile's 16 values of this lane, row r, columns n0 + 8 q + 4 (lane / 32) + 0..3
+    __device__ __forceinline__ static void put(uint8_t *t, int r, int n0, const f32x16_t &v) {
+        const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *(u32x2_t *)(t + at(r, (n0 >> 3) + q) + 8 * h) =
+                u32x2_t{half_pair(v[4 * q], v[4 * q + 1]), half_pair(v[4 * q + 2], v[4 * q + 3])};
+    }
+};
+
+// RT x CT subtiles of 32 x 32 hold X, 8 waves of 2 x 2 of them (WM x WN waves).
+template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds__(512) void orth_small_kernel(OrthArgs a, int steps) {
+    static_assert(WM * WN == 8 && 2 * WM == RT && 2 * WN == CT, "2 x 2 subtiles a wave");
+    constexpr int PA = RT * RT / 8 > 0 ? RT * RT / 8 : 1;   // subtiles of A a wave
+    typedef SmallRows<CT * 32> XR;
+    typedef SmallRows<RT * 32> AR;
+    __shared__ __attribute__((aligned(128))) uint8_t Xs[RT * CT * 2048], As[RT * RT * 2048], Bs[RT * RT * 2048];
+    __shared__ double sums[8];
+    const int th = threadIdx.x, lane = th & 63, l = lane & 31, h = lane >> 5, w = __builtin_amdgcn_readfirstlane(th >> 6);
+    const int m0 = (w / WN) * 64, n0 = (w % WN) * 64;
+    const bool tall = a.N > a.K;
+    const int L = tall ? a.N : a.K;   // the longer side
+    const G *g = (const G *)a.G + (int64_t)blockIdx.x * a.N * a.K;
+    const bool live = m0 < a.side && n0 < L;   // this wave has values of X
+    f32x16_t X[2][2];
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int m = m0 + 32 * i + l, c = n0 + 32 * j + 8 * q + 4 * h;
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+                if (m < a.side && c < L) {
+                    if (!tall && a.K % 4 == 0) {
+                        Raw<G, 4> r;
+                        load_raw<4>(g, (int64_t)m * a.K + c, r);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = value<4>(r, k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (c + k < L) {
+                                Raw<G, 1> r;
+                                load_raw<1>(g, tall ? (int64_t)(c + k) * a.K + m : (int64_t)m * a.K + c + k, r);
+                                v[k] = value<1>(r, 0);
+                            }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s = fma((double)v[k], (double)v[k], s);
+                    X[i][j][4 * q + k] = v[k];
+                }
+            }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
+    if (lane == 0) sums[w] = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += sums[q];
+    const double r = 1.0 / (sqrt(s) + (double)a.eps) * (double)a.size;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) X[i][j][v] = (float)((double)X[i][j][v] * r);
+    const float unsize = 1.f / (a.size * a.size);
+    const int kl = (L + 15) / 16, ks = (a.side + 15) / 16;   // 16s of either contraction
+    // subtiles of A: row ar, columns ac + p
+    const int ar = RT == 4 ? w >> 1 : (w >> 1) & 1, ac = RT == 4 ? 2 * (w & 1) : w & 1;
+    const bool squares = (RT == 4 || w < 4) && 32 * ar < a.side && 32 * ac < a.side;
+    for (int step = 0; step < steps; ++step) {
+        if (step) __syncthreads();   // everyone has read the last X
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) XR::put(Xs, m0 + 32 * i + l, n0 + 32 * j, X[i][j]);
+        __syncthreads();
+        f32x16_t A[PA];
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) A[p][v] = 0.f;
+        if (squares) {
+#pragma unroll 4
+            for (int kk = 0; kk < kl; ++kk) {
+                const f16x8_t x = XR::along(Xs, 32 * ar + l, kk);
+#pragma unroll
+                for (int p = 0; p < PA; ++p) A[p] = mfma(XR::along(Xs, 32 * (ac + p) + l, kk), x, A[p]);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) A[p][v] *= unsize;
+            if (RT == 4 || w < 4) AR::put(As, 32 * ar + l, 32 * (ac + p), A[p]);
+        }
+        __syncthreads();
+        if (squares) {
+            f32x16_t S[PA];
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) S[p][v] = 0.f;
+#pragma unroll 4
+            for (int kk = 0; kk < ks; ++kk) {
+                const f16x8_t x = AR::along(As, 32 * ar + l, kk);
+#pragma unroll
+                for (int p = 0; p < PA; ++p) S[p] = mfma(AR::along(As, 32 * (ac + p) + l, kk), x, S[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) A[p][v] = fmaf(a.c, S[p][v], a.b * A[p][v]);
+        }
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+            if (RT == 4 || w < 4) AR::put(Bs, 32 * ar + l, 32 * (ac + p), A[p]);
+        __syncthreads();
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) X[i][j][v] *= a.a;
+#pragma unroll 2
+            for (int kk = 0; kk < ks; ++kk) {
+                f16x8_t b[2], x[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) b[i] = AR::along(Bs, m0 + 32 * i + l, kk);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) x[j] = XR::across(Xs, n0 + 32 * j, kk);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) X[i][j] = mfma(x[j], b[i], X[i][j]);
+            }
+        }
+    }
+    const float scale = a.scale / a.size;
+    uint16_t *out = a.out + (int64_t)blockIdx.x * a.N * a.K;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int m = m0 + 32 * i + l, c = n0 + 32 * j + 8 * q + 4 * h;
+                if (m >= a.side || c >= L) continue;
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = X[i][j][4 * q + k] * scale;
+                if (!tall && a.K % 4 == 0) {
+                    store_values<4>(out, (int64_t)m * a.K + c, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c + k < L) out[tall ? (int64_t)(c + k) * a.K + m : (int64_t)m * a.K + c + k] = f2bf(v[k]);
+                }
+            }
+}
+
+}  // namespace strata

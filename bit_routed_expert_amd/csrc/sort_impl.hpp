@@ -115,8 +115,8 @@ __device__ __forceinline__ int sort_bases(const SortArgs &a, int mine, int befor
     return kept;
 }
 
-// Chunks of 1024 picks (SORT_ONCE is less than SORT_BLOCKS of them).
-template <typename Key> __global__ __launch_bounds__(SORT_TH) void sort_once_kernel(SortArgs a, Key key, int copies) {
+// Chunks of 1024 picks (SORT_ONCE is less than SORT_BLOCKS of them): the work of block blockIdx.x of a.blocks.
+template <typename Key> __device__ __forceinline__ void sort_once(const SortArgs &a, const Key &key, int copies) {
     __shared__ int base[SORT_E];
     __shared__ uint16_t whist[SORT_WAVES][SORT_E];
     __shared__ uint32_t cells[SORT_CELLS];
@@ -172,6 +172,10 @@ template <typename Key> __global__ __launch_bounds__(SORT_TH) void sort_once_ker
     if (a.perm && i0 + th < n && i0 + th >= kept) a.perm[i0 + th] = -1;
 }
 
+template <typename Key> __global__ __launch_bounds__(SORT_TH) void sort_once_kernel(SortArgs a, Key key, int copies) {
+    sort_once(a, key, copies);
+}
+
 template <typename Key> __global__ __launch_bounds__(SORT_TH) void sort_count_kernel(SortArgs a, Key key) {
     __shared__ int hist[SORT_E];
     const int th = threadIdx.x;
@@ -220,12 +224,17 @@ inline void sort_plan(SortArgs &a) {
 // Bytes of counts that a sort of a.n picks keeps between its launches.
 inline size_t sort_counts_bytes(const SortArgs &a) { return a.n <= SORT_ONCE ? 0 : (size_t)a.blocks * a.E * 4; }
 
+// Copies of the LDS counters for a sort in one launch.
+inline int sort_copies(const SortArgs &a) {
+    int copies = a.blocks > 4 ? 32 : a.blocks;   // fewer picks, fewer meetings
+    while (copies * a.E > SORT_CELLS || (copies & (copies - 1))) --copies;
+    return copies;
+}
+
 // The sort of a planned call.
 template <typename Key> hipError_t launch_sort(const SortArgs &a, const Key &key, hipStream_t s) {
     if (a.n <= SORT_ONCE) {
-        int copies = a.blocks > 4 ? 32 : a.blocks;   // fewer picks, fewer meetings
-        while (copies * a.E > SORT_CELLS || (copies & (copies - 1))) --copies;
-        STRATA_LAUNCH(sort_once_kernel<Key>, dim3(a.blocks), dim3(SORT_TH), 0, s, a, key, copies);
+        STRATA_LAUNCH(sort_once_kernel<Key>, dim3(a.blocks), dim3(SORT_TH), 0, s, a, key, sort_copies(a));
         return hipGetLastError();
     }
     STRATA_LAUNCH(sort_count_kernel<Key>, dim3(a.blocks), dim3(SORT_TH), 0, s, a, key);

@@ -148,11 +148,11 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
 /* Bytes of workspace the call needs; 0 for arguments it refuses. */
 size_t strata_orthogonalise_workspace_bytes(int32_t n, int32_t N, int32_t K);
 
-/*   G [dev] [n][N][K] of gdtype, out [dev] [n][N][K] bf16; out may lie over G
- *   (with steps = 0 only a bf16 G's own place).
+/*   G [dev] [n][N][K] of gdtype, out [dev] [n][N][K] bf16; out may be a bf16 G.
  *   steps 0..32; coefficients [host] {a, b, c}.
  * n = 0: no-op.  EINVAL: a null or misaligned pointer, n < 0, N or K < 1, a bad dtype, steps outside 0..32,
- * a coefficient or scale that is not finite, eps not a positive finite number; EUNSUPPORTED: N or K > 16384,
+ * a coefficient or scale that is not finite, eps not a positive finite number, an out that shares memory with
+ * G otherwise; EUNSUPPORTED: N or K > 16384,
  * n > 1024, n*N*K > 2^33; EWORKSPACE; EHIP. */
 strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t n, int32_t N, int32_t K, int32_t steps,
                                    const float *coefficients, float scale, float eps, void *out, void *ws, size_t ws_bytes,

@@ -126,8 +126,7 @@ def test_orthogonalise_refusals():
     for bad in (dict(g=None), dict(g=G + 8), dict(t=2), dict(n=-1), dict(N=0), dict(K=0), dict(steps=-1), dict(steps=33),
                 dict(c=None), dict(c=(nan, 1, 1)), dict(c=(1, inf, 1)), dict(c=(1, 1, -inf)), dict(scale=nan), dict(scale=inf),
                 dict(eps=0.0), dict(eps=-1.0), dict(eps=nan), dict(eps=inf), dict(out=None), dict(out=G + 2), dict(w=None),
-                dict(w=G + 8), dict(steps=0, out=G), dict(steps=0, out=G + 16), dict(steps=0, t=0, out=G + 16),
-                dict(steps=0, t=0, out=G - 16)):
+                dict(w=G + 8), dict(out=G), dict(out=G + 16), dict(t=0, out=G + 16), dict(t=0, out=G - 16), dict(steps=0, out=G)):
         assert call(**bad) == EINVAL, bad
     for bad in (dict(N=16385), dict(K=16385), dict(n=1025), dict(n=1024, N=16384, K=16384)):
         a = dict(n=3, N=40, K=72) | bad
