@@ -96,8 +96,6 @@ template <typename Z, int V, int P> __global__ __launch_bounds__(64 * BAL_WAVES)
     __shared__ float zred[W];
     __shared__ int nred[W];
     const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6), place = lane % P;
-    for (int e = th; e < a.E; e += 64 * W) hist[e] = 0;
-    __syncthreads();
     const int step = a.blocks * W * ROWS;
     const auto counted = [&](int64_t t) { return t < a.T && (!a.keep || a.keep[t]); };
     float acc[C], zz = 0.f;
@@ -108,19 +106,22 @@ template <typename Z, int V, int P> __global__ __launch_bounds__(64 * BAL_WAVES)
     int pick = -1;
     int64_t t = (int64_t)(blockIdx.x * W + w) * ROWS + lane / P;
     const int64_t first = (int64_t)(blockIdx.x * W + w) * ROWS;   // the wave's first token decides its trips
-    bool on = counted(t);
     const auto fetch = [&](int64_t u) {
         row.load((const Z *)a.z, u, a.E);
         pick = place < a.k ? a.idx[u * a.k + place] : -1;
     };
-    if (on) fetch(t);
+    if (t < a.T) fetch(t);   // the first ones counted or not; then flags two trips ahead of their rows' use
+    bool on = counted(t), soon = counted(t + step);
+    for (int e = th; e < a.E; e += 64 * W) hist[e] = 0;
+    __syncthreads();
     for (int64_t f = first; f < a.T; f += step, t += step) {
         float v[C];
         const int e = pick;
         bool here = on;
         row.values(a.E, v);
-        on = counted(t + step);
+        on = soon;
         if (on) fetch(t + step);
+        soon = counted(t + 2 * (int64_t)step);
         float m = v[0];
 #pragma unroll
         for (int c = 1; c < C; ++c) m = fmaxf(m, v[c]);
@@ -304,19 +305,14 @@ template <typename Z, int V, int P> __global__ __launch_bounds__(256) void balan
     float *const mine = &add[w][(lane / P) * P * C];   // this token's row
 #pragma unroll
     for (int c = 0; c < C; ++c) add[w][c * 64 + lane] = 0.f;
-    const float n = fmaxf((float)*a.tokens, 1.f);
-    const float scale = a.dlosses[0] * (float)a.E / (n * n * (float)a.k), zscale = 2.f * a.dlosses[1] / n;
-    float g[C];
-#pragma unroll
-    for (int i = 0; i < C / V; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) g[i * V + j] = Row::expert(i) < a.E ? scale * (float)a.counts[Row::expert(i) + j] : 0.f;
+    // the first tokens' rows ahead of all that waits, counted or not; then flags two trips ahead of their rows' use
     const int step = a.blocks * 4 * ROWS;
-    const auto counted = [&](int64_t t) { return t < a.T && (!a.keep || a.keep[t]); };
+    const int64_t f0 = (int64_t)(blockIdx.x * 4 + w) * ROWS;
+    int64_t t = f0 + lane / P;
     Row row;
     float lse = 0.f, up = 0.f;
     int pick = -1;
-    int64_t t = (int64_t)(blockIdx.x * 4 + w) * ROWS + lane / P;
+    const auto kept = [&](int64_t u) { return u < a.T && (!a.keep || a.keep[u]); };
     const auto fetch = [&](int64_t u) {
         row.load((const Z *)a.z, u, a.E);
         lse = a.lse[u];
@@ -325,16 +321,24 @@ template <typename Z, int V, int P> __global__ __launch_bounds__(256) void balan
             up = a.dpicks[u * a.k + place];
         }
     };
-    bool on = counted(t);
-    if (on) fetch(t);
-    for (int64_t f = (int64_t)(blockIdx.x * 4 + w) * ROWS; f < a.T; f += step, t += step) {
+    if (t < a.T) fetch(t);
+    bool on = kept(t), soon = kept(t + step);
+    const float n = fmaxf((float)*a.tokens, 1.f);
+    const float scale = a.dlosses[0] * (float)a.E / (n * n * (float)a.k), zscale = 2.f * a.dlosses[1] / n;
+    float g[C];
+#pragma unroll
+    for (int i = 0; i < C / V; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) g[i * V + j] = Row::expert(i) < a.E ? scale * (float)a.counts[Row::expert(i) + j] : 0.f;
+    for (int64_t f = f0; f < a.T; f += step, t += step) {
         float v[C];
         const float l = lse, u = up;
         const int e = pick;
         bool here = on;
         row.values(a.E, v);
-        on = counted(t + step);
+        on = soon;
         if (on) fetch(t + step);
+        soon = kept(t + 2 * (int64_t)step);
         bool any = l != 0.f;   // a row of -inf has lse 0 too
 #pragma unroll
         for (int c = 0; c < C; ++c) any |= v[c] != -INFINITY;

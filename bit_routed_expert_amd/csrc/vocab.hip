@@ -78,30 +78,45 @@ template <int GRAD> __global__ __launch_bounds__(256) void vocab_pack_kernel(Voc
     if (t1 == a.T && th == 0) *a.n = base;
 }
 
-// A row's tiles joined: R rows to a block, 1024 / R threads to a row.
-template <int R> __global__ __launch_bounds__(1024) void vocab_join_kernel(VocabArgs a) {
+// The running maximum and sum of exponentials, met by another.
+__device__ __forceinline__ void meet(float &m, float &s, float2 p) {
+    const float u = fmaxf(m, p.x), b = u == -INFINITY ? 0.f : u;
+    s = s * exp_diff(m, b) + p.y * exp_diff(p.x, b);
+    m = u;
+}
+
+// A row's tiles joined: R rows to a block, 1024 / R threads to a row.  FEW: a
+// block for each of up to 32 tokens, of which it finds the row itself.
+template <int R, int FEW> __global__ __launch_bounds__(1024) void vocab_join_kernel(VocabArgs a) {
     __shared__ float2 sh[16][R];
-    const int n = *a.n, th = threadIdx.x, lane = th & 63, w = th >> 6;
-    const int r = th % R, sub = th / R, row = blockIdx.x * R + r;
-    if ((int)blockIdx.x * R >= n) return;
+    const int th = threadIdx.x, lane = th & 63, w = th >> 6;
+    const int r = th % R, sub = th / R;
+    int row = blockIdx.x * R + r, n = 0;
+    if constexpr (FEW) {
+        const uint32_t there = few_tokens(a);
+        if (!(there >> blockIdx.x & 1)) {
+            if (th == 0) a.loss[blockIdx.x] = a.lse[blockIdx.x] = 0.f;
+            return;
+        }
+        row = __popc(there & ((1u << blockIdx.x) - 1));
+        n = 32;
+    } else {
+        n = *a.n;
+        if ((int)blockIdx.x * R >= n) return;
+    }
     float m = -INFINITY, s = 0.f;
-    const auto meet = [&](float2 p) {   // the running maximum and sum
-        const float u = fmaxf(m, p.x), b = u == -INFINITY ? 0.f : u;
-        s = s * exp_diff(m, b) + p.y * exp_diff(p.x, b);
-        m = u;
-    };
     if (row < n) {
 #pragma unroll 4
-        for (int c = sub; c < a.tiles; c += 1024 / R) meet(a.part[(int64_t)c * a.ldp + row]);
+        for (int c = sub; c < a.tiles; c += 1024 / R) meet(m, s, a.part[(int64_t)c * a.ldp + row]);
     }
 #pragma unroll
-    for (int o = R; o < 64; o <<= 1) meet(float2{__shfl_xor(m, o, 64), __shfl_xor(s, o, 64)});
+    for (int o = R; o < 64; o <<= 1) meet(m, s, float2{__shfl_xor(m, o, 64), __shfl_xor(s, o, 64)});
     if (lane < R) sh[w][lane] = float2{m, s};
     __syncthreads();
     if (th >= R || row >= n) return;
-    for (int q = 1; q < 16; ++q) meet(sh[q][r]);
+    for (int q = 1; q < 16; ++q) meet(m, s, sh[q][r]);
     const float lse = m + logf(s);
-    const int t = a.map[row];
+    const int t = FEW ? (int)blockIdx.x : a.map[row];
     a.lse[t] = lse;
     a.loss[t] = lse - a.zt[row];
 }
@@ -212,8 +227,13 @@ dim3 tile_grid(int64_t nr, int64_t nc) { return dim3((unsigned)up_to(nr * nc, 8)
 template <int GRAD> strata_status launch_logits(const VocabArgs &a, hipStream_t s) {
     const RowTile k = row_tile(a.T);
     const dim3 g = tile_grid((a.T + TILE_ROWS[k] - 1) / TILE_ROWS[k], (a.pw + TILE_COLS[k] - 1) / TILE_COLS[k]);
-    if (k == ROWS_32) STRATA_LAUNCH((vocab_logits_kernel<32, 128, 1, 4, 4, GRAD>), g, dim3(256), 0, s, a);
-    else if (k == ROWS_128) STRATA_LAUNCH((vocab_logits_kernel<128, 256, 2, 4, 3, GRAD>), g, dim3(512), 0, s, a);
+    if constexpr (GRAD != 0) {   // a forward call of few rows has its own
+        if (k == ROWS_32) {
+            STRATA_LAUNCH((vocab_logits_kernel<32, 128, 1, 4, 4, GRAD>), g, dim3(256), 0, s, a);
+            return hip_status(hipGetLastError());
+        }
+    }
+    if (k == ROWS_128) STRATA_LAUNCH((vocab_logits_kernel<128, 256, 2, 4, 3, GRAD>), g, dim3(512), 0, s, a);
     else STRATA_LAUNCH((vocab_logits_kernel<256, 256, 2, 4, 2, GRAD>), g, dim3(512), 0, s, a);
     return hip_status(hipGetLastError());
 }
@@ -285,12 +305,17 @@ strata_status strata_vocab_loss(const void *h, const void *W, const int32_t *tar
     a.ldp = (int)up_to(T, 16);
     a.pw = V;
     a.tiles = (V + TILE_COLS[row_tile(T)] - 1) / TILE_COLS[row_tile(T)];
+    if (row_tile(T) == ROWS_32) {   // packing and joining apart cost 5 tokens of 128000 x 2048 another 6 of 103 us
+        STRATA_LAUNCH((vocab_logits_kernel<32, 128, 1, 4, 4, 0, 1>), tile_grid(1, a.tiles), dim3(256), 0, s, a);
+        VOCAB_TRY;
+        STRATA_LAUNCH((vocab_join_kernel<1, 1>), dim3(T), dim3(1024), 0, s, a);
+        return hip_status(hipGetLastError());
+    }
     STRATA_LAUNCH(vocab_pack_kernel<0>, dim3((T + a.rows_block - 1) / a.rows_block), dim3(256), 0, s, a);
     VOCAB_TRY;
     const strata_status lt = launch_logits<0>(a, s);
     if (lt != STRATA_OK) return lt;
-    if (T <= 4) STRATA_LAUNCH(vocab_join_kernel<4>, dim3(1), dim3(1024), 0, s, a);
-    else STRATA_LAUNCH(vocab_join_kernel<16>, dim3((T + 15) / 16), dim3(1024), 0, s, a);
+    STRATA_LAUNCH((vocab_join_kernel<16, 0>), dim3((T + 15) / 16), dim3(1024), 0, s, a);
     return hip_status(hipGetLastError());
 }
 

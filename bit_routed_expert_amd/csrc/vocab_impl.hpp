@@ -80,15 +80,30 @@ __device__ __forceinline__ bool vocab_tile(int nr, int nc, int &rt, int &ct) {
     return true;
 }
 
+// The tokens of a call of up to 32 that have a target, a bit each.
+__device__ __forceinline__ uint32_t few_tokens(const VocabArgs &a) {
+    const int lane = threadIdx.x & 63;
+    return (uint32_t)__ballot(lane < a.T && (uint32_t)a.targets[lane < a.T ? lane : 0] < (uint32_t)a.V);
+}
+
+// Place of the r-th set bit.
+__device__ __forceinline__ int bit_of(uint32_t m, int r) {
+    for (int i = 0; i < r; ++i) m &= m - 1;
+    return __ffs((int)m) - 1;
+}
+
 // Tiles of the logits z = hc W^T of a piece.  GRAD 0: the maximum and the sum
-// of each row's tile, and the targets' logits; else dz to hi (and lo).
-template <int BM, int BN, int WM, int WN, int ST, int GRAD>
+// of each row's tile, and the targets' logits; else dz to hi (and lo).  FEW: a
+// call of up to 32 tokens takes its rows from h itself, no launch packs them.
+template <int BM, int BN, int WM, int WN, int ST, int GRAD, int FEW = 0>
 __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BN / 32 / WN, C = 64;
     typedef Operand<BM, 0, NT, C> OA;
     typedef Operand<BN, 0, NT, C> OB;
     GROUP_BUFFERS(ST, OA, OB)
-    const int n = *a.n, nc = (a.pw + BN - 1) / BN;
+    static_assert(!FEW || BM == 32, "one tile of rows");
+    const uint32_t there = FEW ? few_tokens(a) : 0;
+    const int n = FEW ? __popc(there) : *a.n, nc = (a.pw + BN - 1) / BN;
     int rt, ct;
     if (!vocab_tile((n + BM - 1) / BM, nc, rt, ct)) return;
     rt = __builtin_amdgcn_readfirstlane(rt);
@@ -96,7 +111,16 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
     const int row0 = rt * BM, rows = min(n - row0, BM), c0 = ct * BN;
     OA A;
     OB B;
-    A.init(a.hc + (int64_t)row0 * a.d, a.d, 0, rows, a.d);
+    if constexpr (FEW) {
+        A.init(a.h, a.d, 0, a.T, a.d);
+#pragma unroll
+        for (int i = 0; i < OA::LOADS; ++i) {   // rows from their tokens; behind the last one out of range
+            const int r = (i * NT + (int)threadIdx.x) / OA::CH;
+            A.off[i] = r < n ? A.off[i] + (uint32_t)(bit_of(there, r) - r) * (uint32_t)a.d * 2u : 0x80000000u;
+        }
+    } else {
+        A.init(a.hc + (int64_t)row0 * a.d, a.d, 0, rows, a.d);
+    }
     B.init(a.W + (int64_t)a.v0 * a.d, a.d, c0, a.pw, a.d);
     int m0, n0;
     wave_place<WM, WN, MT, NT2>(m0, n0);
@@ -121,7 +145,7 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const int row = row0 + m0 + 32 * i + l;
-                const int want = (row < n ? a.tc[row] : -1) - a.v0 - c0 - n0 - 4 * h;   // the target's place among the columns
+                const int want = (row < n ? FEW ? a.targets[bit_of(there, row)] : a.tc[row] : -1) - a.v0 - c0 - n0 - 4 * h;   // the target's place among the columns
                 float m = -INFINITY, s = 0.f, picked = 0.f;
                 bool mine = false;
 #pragma unroll
