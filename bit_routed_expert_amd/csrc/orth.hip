@@ -7,10 +7,11 @@
 // tiles of their lower halves are computed.  The operands are fp16: the values
 // are in known ranges (|X| and |A| at most about 1, X kept times a power of
 // two), and 11 bits leave the result about 3e-4 off where bf16's 8 would leave
-// 5e-3.  X itself is hi + lo, 22 bits: with hi alone the rounding of X, a
-// matrix of full rank, would be multiplied by a at every step like the small
-// directions of G itself (3.4^5 = 485 in five steps; a gradient of 80 rows in
-// 1536 x 2048 came out 2% off).
+// 5e-3.  X itself is hi + lo, 22 bits (X_0 is G): with hi alone the rounding
+// of X, a matrix of full rank, would be multiplied by a at every step like the
+// small directions of G itself (3.4^5 = 485 in five steps; a gradient of 80 rows
+// in 1536 x 2048 would come out 2% off).  The last step takes hi alone: one
+// factor a.
 #include <cmath>
 
 #include "orth_small.hpp"
@@ -48,47 +49,38 @@ template <typename G, int V> __global__ __launch_bounds__(256) void orth_norm_ke
     if (threadIdx.x == 0) a.norms[e * a.parts + part] = sh[0] + sh[1] + sh[2] + sh[3];
 }
 
-// X_0 = G / (|G| + eps), times size, in two pieces (or, without steps, times scale to out).
+// X_0 = G / (|G| + eps), times size, rounded to fp16 (or, without steps, times scale to out).
 template <typename G, int V> __global__ __launch_bounds__(256) void orth_start_kernel(OrthArgs a, int steps) {
     const int e = blockIdx.y;
     double s = 0.0;
     for (int q = 0; q < a.parts; ++q) s += a.norms[e * a.parts + q];
-    const double r = 1.0 / (sqrt(s) + (double)a.eps);
-    const int nc = (steps ? a.ldx : a.K + V - 1) / V;   // pieces of a row, those of zeros behind its end too
+    const double r = 1.0 / (sqrt(s) + (double)a.eps) * (steps ? (double)a.size : (double)a.scale);
+    const float f = (float)r;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.factor[e] = f;
+    const int nc = (steps ? a.ldx : a.K) / V;   // pieces of a row, those of zeros behind its end too
     const G *g = (const G *)a.G + (int64_t)e * a.N * a.K;
     const int64_t all = (int64_t)a.N * nc;
     for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < all; p += (int64_t)gridDim.x * 256) {
         const int64_t m = p / nc;
         const int c = (int)(p - m * nc) * V;
-        float v[V], l[V];
+        float v[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = 0.f;
         if (c < a.K) piece_values<V, G>(g, m * a.K + c, v);
         if (!steps) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = (float)((double)v[j] * r * (double)a.scale);
+            for (int j = 0; j < V; ++j) v[j] = (float)((double)v[j] * r);
             store_values<V>(a.out + (int64_t)e * a.N * a.K, m * a.K + c, v);
             continue;
         }
-        uint16_t *hi = a.hi + ((int64_t)e * a.N + m) * a.ldx + c, *lo = a.lo + ((int64_t)e * a.N + m) * a.ldx + c;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float x = (float)((double)v[j] * r) * a.size;
-            v[j] = x;
-            l[j] = x - (float)(_Float16)x;
-        }
+        uint16_t *hi = a.hi + ((int64_t)e * a.N + m) * a.ldx + c;
         if constexpr (V == 1) {
-            *hi = (uint16_t)half_pair(v[0], 0.f);
-            *lo = (uint16_t)half_pair(l[0], 0.f);
+            *hi = (uint16_t)half_pair(v[0] * f, 0.f);
         } else {
-            uint32_t w[V / 2], x[V / 2];
+            uint32_t w[V / 2];
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                w[j] = half_pair(v[2 * j], v[2 * j + 1]);
-                x[j] = half_pair(l[2 * j], l[2 * j + 1]);
-            }
+            for (int j = 0; j < V / 2; ++j) w[j] = half_pair(v[2 * j] * f, v[2 * j + 1] * f);
             __builtin_memcpy(__builtin_assume_aligned(hi, 2 * V), w, 2 * V);
-            __builtin_memcpy(__builtin_assume_aligned(lo, 2 * V), x, 2 * V);
         }
     }
 }
@@ -103,8 +95,21 @@ strata_status check_orth(int32_t n, int32_t N, int32_t K) {
 
 struct OrthPlan {
     int side, ldx, lds;
-    size_t hi, next, lo, A, B, bytes;
+    size_t factor, hi, next, lo, A, B, bytes;
 };
+
+// Tiles of a step by how many of 128 square there are (us of a step): below 144,
+// 64 x 128 (2 of 512 x 2048, 128 tiles: 10.0 against 13.2; 1 of 1000 x 1000: 11.4
+// against 14.5); up to 256, 128 square with four buffers (1 of 2048 x 2048: 27.6
+// against 33.6 and, with two buffers, 31.7), up to 2048 with two, two blocks to a CU
+// (8 of 2048 x 768, 768 tiles: 40.6 against 46.8; 32 of 512 x 512: 24.0 against
+// 29.6); then 128 x 256 (16 of 1536 x 2048: 244 against 251; 256 square 249).
+enum StepTile { STEP_64, STEP_128, STEP_128_TWO, STEP_256 };
+constexpr int STEP_ROWS[] = {64, 128, 128, 128}, STEP_COLS[] = {128, 128, 128, 256};
+StepTile step_tile(int32_t n, int32_t N, int32_t K) {
+    const int64_t tiles = (int64_t)n * ((N + 127) / 128) * ((K + 127) / 128);
+    return tiles < 144 ? STEP_64 : tiles <= 256 ? STEP_128 : tiles <= 2048 ? STEP_128_TWO : STEP_256;
+}
 
 OrthPlan orth_plan(int32_t n, int32_t N, int32_t K) {
     OrthPlan p{};
@@ -118,9 +123,12 @@ OrthPlan orth_plan(int32_t n, int32_t N, int32_t K) {
         return q;
     };
     const size_t x = (size_t)n * N * p.ldx, s = (size_t)n * p.side * p.lds;
+    const StepTile t = step_tile(n, N, K);
+    const size_t rows = (size_t)(N + STEP_ROWS[t] - 1) / STEP_ROWS[t] * STEP_ROWS[t];
+    p.factor = take((size_t)(n > 0 ? n : 1) * 2);
     p.hi = take(x);
     p.next = take(x);
-    p.lo = take(x);
+    p.lo = take(n * rows * ((K + STEP_COLS[t] - 1) / STEP_COLS[t] * STEP_COLS[t]));   // whole tiles
     p.A = take(s);
     p.B = take(s);
     p.bytes = at;
@@ -188,11 +196,12 @@ template <int SQUARE, int ACROSS> hipError_t squares(const OrthArgs &a, hipStrea
 }
 
 template <int TALL> hipError_t steps_of(const OrthArgs &a, hipStream_t s) {
-    const int64_t tiles = a.n * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-    if (tiles < 144) step<64, 128, 2, 2, 4, TALL>(a, s);
-    else if (tiles <= 256) step<128, 128, 2, 2, 4, TALL>(a, s);
-    else if (tiles <= 2048) step<128, 128, 2, 2, 2, TALL>(a, s);
-    else step<128, 256, 2, 4, 3, TALL>(a, s);
+    switch (step_tile(a.n, a.N, a.K)) {
+        case STEP_64: step<64, 128, 2, 2, 4, TALL>(a, s); break;
+        case STEP_128: step<128, 128, 2, 2, 4, TALL>(a, s); break;
+        case STEP_128_TWO: step<128, 128, 2, 2, 2, TALL>(a, s); break;
+        default: step<128, 256, 2, 4, 3, TALL>(a, s);
+    }
     return hipGetLastError();
 }
 
@@ -230,6 +239,8 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     a.G = G;
     a.out = (uint16_t *)out;
     a.norms = (double *)w;
+    a.factor = (float *)(w + p.factor);
+    a.g_bf16 = gdtype == STRATA_X_BF16;
     a.hi = (uint16_t *)(w + p.hi);
     a.next = (uint16_t *)(w + p.next);
     a.lo = (uint16_t *)(w + p.lo);
@@ -255,7 +266,11 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     const bool tall = N > K;
     hipError_t e = gdtype == STRATA_X_BF16 ? orth_begin_width<uint16_t>(a, steps, s) : orth_begin_width<float>(a, steps, s);
     for (int i = 0; i < steps && e == hipSuccess; ++i) {
-        a.last = i + 1 == steps;
+        const int left = steps - 1 - i;   // steps behind this one
+        a.first = i == 0;
+        a.last = left == 0;
+        a.lo_in = i > 0 && left > 0;
+        a.lo_out = left > 1;
         e = tall ? squares<0, 1>(a, s) : squares<0, 0>(a, s);
         if (e == hipSuccess) e = squares<1, 0>(a, s);
         if (e == hipSuccess) e = tall ? steps_of<1>(a, s) : steps_of<0>(a, s);

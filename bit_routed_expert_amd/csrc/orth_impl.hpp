@@ -6,15 +6,19 @@ namespace strata {
 
 // n matrices of N x K; side = min(N, K), the order of A and B.  X is kept
 // times `size` (a power of two near sqrt(max(N, K)), so that its values are
-// about 1 in size at the end), in rows of ldx values; A and B in rows of lds.
-// What lies in a row behind its last column is zero in all of them.
+// about 1 in size at the end).  hi, its fp16 rounding, lies in rows of ldx
+// values, A and B in rows of lds; what lies in a row behind its last column is
+// zero.  lo, what the rounding left, is the step kernel's alone and lies in the
+// order of its lanes: 4 values to a lane, the wave's lanes side by side.
 struct OrthArgs {
     const void *G;
     uint16_t *out;              // bf16 [n][N][K]
     double *norms;              // [n][parts] sums of squares
+    float *factor;              // [n] X_0 / G, size included
     uint16_t *hi, *next, *lo;   // X = hi + lo, the next X's hi
     uint16_t *A, *B;
-    int n, N, K, side, ldx, lds, parts, last;
+    int n, N, K, side, ldx, lds, parts, g_bf16;
+    int first, lo_in, lo_out, last;   // of a step: its X is G's, X has a lo, X' gets one, X' goes to out
     float size, a, b, c, scale, eps;
 };
 
@@ -143,6 +147,41 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
         }
 }
 
+// a X added to a tile's sums while the rows (TALL: columns) of the tile pass
+// through LDS as an operand: a wave's subtiles that lie in step s.
+template <int BN, int MT, int NT2, int TALL> struct AddX {
+    f32x16_t (&acc)[MT][NT2];
+    float a;
+    int from, m0, n0;   // the wave's first row (TALL: column) in the matrix; its place in the tile
+    bool on;
+    __device__ __forceinline__ void operator()(int s, const uint8_t *ta, const uint8_t *tb) const {
+        constexpr int L = 32 * (TALL ? NT2 : MT);
+        if (!on || 64 * s + 64 <= from || 64 * s >= from + L) return;
+        const int l = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT2; ++j) {
+                const int at = from + 32 * (TALL ? j : i) - 64 * s;   // the subtile in the step
+                if (at < 0 || at >= 64) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    u32x2_t w;
+                    if (TALL) {
+                        const int r = m0 + 32 * i + l;
+                        w = *(const u32x2_t *)(ta + r * 128 + 16 * (((at >> 3) + q) ^ along_swz(r)) + 8 * h);
+                    } else {
+                        const int c = at + l, chunk = ((n0 + 32 * j) >> 3) + q;
+                        w = *(const u32x2_t *)(tb + c * (BN * 2) + 16 * (chunk ^ across_swz<BN>(c)) + 8 * h);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[i][j][4 * q + k] = fmaf(a, half_value(w[k / 2], k & 1), acc[i][j][4 * q + k]);
+                }
+            }
+    }
+};
+
 // X' = a X + B X (TALL: a X + X B, B symmetric), the last one to out.
 template <int BM, int BN, int WM, int WN, int ST, int TALL>
 __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
@@ -181,21 +220,62 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
         contract<ST, false, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
         return;
     }
-    contract<ST, true, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
-    const auto hi = half_rows(X + (int64_t)r0 * a.ldx, M, a.ldx), lo = half_rows(a.lo + e * xs + (int64_t)r0 * a.ldx, M, a.ldx);
-    const auto next = half_rows(a.next + e * xs + (int64_t)r0 * a.ldx, M, a.ldx);
+    const AddX<BN, MT, NT2, TALL> hook{acc, a.a, TALL ? k0 + n0 : r0 + m0, m0, n0, !a.first};
+    contract<ST, true, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
+    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+    if (a.first) {   // X is G, to all of its digits
+        const float r = a.a * a.factor[e];
+        const int64_t g0 = ((int64_t)e * a.N + r0) * a.K;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        __builtin_amdgcn_sched_barrier(0);   // no more than a subtile row's loads ahead: registers
+        for (int i = 0; i < MT; ++i) {
+            __builtin_amdgcn_sched_barrier(0);   // no more than a subtile row's loads ahead: registers
 #pragma unroll
-        for (int j = 0; j < NT2; ++j)
+            for (int j = 0; j < NT2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t p = quad_at(m0, k0 + n0, a.ldx, i, j, q);
-                const f32x4_t x = load_quad(hi, p) + load_quad(lo, p);
+                for (int q = 0; q < 4; ++q) {
+                    const int m = m0 + 32 * i + l, n = k0 + n0 + 32 * j + 8 * q + 4 * h;
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (m < M && n < a.K) {
+                        const int64_t p = g0 + (int64_t)m * a.K + n;
+                        if (a.K % 4 == 0) {
+                            if (a.g_bf16) {
+                                Raw<uint16_t, 4> w;
+                                load_raw<4>((const uint16_t *)a.G, p, w);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[i][j][4 * q + c] = fmaf(a.a, x[c], acc[i][j][4 * q + c]);
-            }
+                                for (int k = 0; k < 4; ++k) x[k] = value<4>(w, k);
+                            } else {
+                                Raw<float, 4> w;
+                                load_raw<4>((const float *)a.G, p, w);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) x[k] = value<4>(w, k);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n + k < a.K)
+                                    x[k] = a.g_bf16 ? bf16_to_float(((const uint16_t *)a.G)[p + k]) : ((const float *)a.G)[p + k];
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[i][j][4 * q + k] = fmaf(r, x[k], acc[i][j][4 * q + k]);
+                }
+        }
+    }
+    u32x2_t *const lo = (u32x2_t *)a.lo + (t * (WM * WN) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * (MT * NT2 * 4 * 64) + lane;
+    if (a.lo_in) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const u32x2_t w = lo[((i * NT2 + j) * 4 + q) * 64];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[i][j][4 * q + k] = fmaf(a.a, half_value(w[k / 2], k & 1), acc[i][j][4 * q + k]);
+                }
+        }
     }
     if (a.last) {
         const float r = a.scale / a.size;
@@ -207,31 +287,37 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
                 for (int v = 0; v < 16; ++v) acc[i][j][v] *= r;
         uint16_t *to = a.out + ((int64_t)e * a.N + r0) * a.K;
         if (a.K % 8 == 0) return store_tile<MT, NT2>(to, 1, m0, M, k0 + n0, a.K, acc);
-        const int lane = threadIdx.x & 63;   // rows that 16 bytes do not divide
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MT; ++i)   // rows that 16 bytes do not divide
 #pragma unroll
             for (int j = 0; j < NT2; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
-                    const int m = m0 + 32 * i + (lane & 31), n = k0 + n0 + 32 * j + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
+                    const int m = m0 + 32 * i + l, n = k0 + n0 + 32 * j + 8 * (v / 4) + 4 * h + (v & 3);
                     if (m < M && n < a.K) to[(int64_t)m * a.K + n] = f2bf(acc[i][j][v]);
                 }
         return;
     }
+    const auto next = half_rows(a.next + e * xs + (int64_t)r0 * a.ldx, M, a.ldx);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT2; ++j) {
-            uint32_t w[8], l[8];
+            uint32_t w[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float x = acc[i][j][2 * q], y = acc[i][j][2 * q + 1];
-                w[q] = half_pair(x, y);
-                l[q] = half_pair(x - half_value(w[q], 0), y - half_value(w[q], 1));
+            for (int q = 0; q < 8; ++q) w[q] = half_pair(acc[i][j][2 * q], acc[i][j][2 * q + 1]);
+            if (a.lo_out) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    u32x2_t x;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        x[p] = half_pair(acc[i][j][4 * q + 2 * p] - half_value(w[2 * q + p], 0),
+                                         acc[i][j][4 * q + 2 * p + 1] - half_value(w[2 * q + p], 1));
+                    lo[((i * NT2 + j) * 4 + q) * 64] = x;
+                }
             }
             store_halves(next, m0, k0 + n0, a.ldx, i, j, w);
-            store_halves(lo, m0, k0 + n0, a.ldx, i, j, l);
         }
 }
 

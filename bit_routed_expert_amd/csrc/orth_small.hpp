@@ -103,7 +103,7 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
 #pragma unroll
             for (int v = 0; v < 16; ++v) X[i][j][v] = (float)((double)X[i][j][v] * r);
     const float unsize = 1.f / (a.size * a.size);
-    const int kl = (L + 15) / 16, ks = (a.side + 15) / 16;   // 16s of either contraction
+    const int kl = (L + 63) / 64, ks = (a.side + 63) / 64;   // 64s of either contraction
     // subtiles of A: row ar, columns ac + p
     const int ar = RT == 4 ? w >> 1 : (w >> 1) & 1, ac = RT == 4 ? 2 * (w & 1) : w & 1;
     const bool squares = (RT == 4 || w < 4) && 32 * ar < a.side && 32 * ac < a.side;
@@ -120,12 +120,13 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
 #pragma unroll
             for (int v = 0; v < 16; ++v) A[p][v] = 0.f;
         if (squares) {
-#pragma unroll 4
-            for (int kk = 0; kk < kl; ++kk) {
-                const f16x8_t x = XR::along(Xs, 32 * ar + l, kk);
+            for (int k0 = 0; k0 < kl; ++k0)
 #pragma unroll
-                for (int p = 0; p < PA; ++p) A[p] = mfma(XR::along(Xs, 32 * (ac + p) + l, kk), x, A[p]);
-            }
+                for (int kk = 4 * k0, u = 0; u < 4; ++u, ++kk) {
+                    const f16x8_t x = XR::along(Xs, 32 * ar + l, kk);
+#pragma unroll
+                    for (int p = 0; p < PA; ++p) A[p] = mfma(XR::along(Xs, 32 * (ac + p) + l, kk), x, A[p]);
+                }
         }
 #pragma unroll
         for (int p = 0; p < PA; ++p) {
@@ -140,12 +141,13 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
             for (int p = 0; p < PA; ++p)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) S[p][v] = 0.f;
-#pragma unroll 4
-            for (int kk = 0; kk < ks; ++kk) {
-                const f16x8_t x = AR::along(As, 32 * ar + l, kk);
+            for (int k0 = 0; k0 < ks; ++k0)
 #pragma unroll
-                for (int p = 0; p < PA; ++p) S[p] = mfma(AR::along(As, 32 * (ac + p) + l, kk), x, S[p]);
-            }
+                for (int kk = 4 * k0, u = 0; u < 4; ++u, ++kk) {
+                    const f16x8_t x = AR::along(As, 32 * ar + l, kk);
+#pragma unroll
+                    for (int p = 0; p < PA; ++p) S[p] = mfma(AR::along(As, 32 * (ac + p) + l, kk), x, S[p]);
+                }
 #pragma unroll
             for (int p = 0; p < PA; ++p)
 #pragma unroll
@@ -162,18 +164,19 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int v = 0; v < 16; ++v) X[i][j][v] *= a.a;
-#pragma unroll 2
-            for (int kk = 0; kk < ks; ++kk) {
-                f16x8_t b[2], x[2];
+            for (int k0 = 0; k0 < ks; ++k0)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) b[i] = AR::along(Bs, m0 + 32 * i + l, kk);
+                for (int kk = 4 * k0, u = 0; u < 4; ++u, ++kk) {
+                    f16x8_t b[2], x[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) x[j] = XR::across(Xs, n0 + 32 * j, kk);
+                    for (int i = 0; i < 2; ++i) b[i] = AR::along(Bs, m0 + 32 * i + l, kk);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int j = 0; j < 2; ++j) x[j] = XR::across(Xs, n0 + 32 * j, kk);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) X[i][j] = mfma(x[j], b[i], X[i][j]);
-            }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) X[i][j] = mfma(x[j], b[i], X[i][j]);
+                }
         }
     }
     const float scale = a.scale / a.size;

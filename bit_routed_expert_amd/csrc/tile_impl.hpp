@@ -129,6 +129,12 @@ __device__ __forceinline__ void read_frags(const uint8_t *ta, const uint8_t *tb,
     for (int i = 0; i < MT; ++i) f.a[set][i] = read_frag<BM, TA, C, FT>(ta, m0 + 32 * i, kk);
 }
 
+// What a contraction does besides, at the start of every step while the step's
+// operands lie in LDS (at ta and tb): nothing.
+struct NoHook {
+    __device__ __forceinline__ void operator()(int, const uint8_t *, const uint8_t *) const {}
+};
+
 // Step s, whose first 16 are in set 0 of f already; leaves the next step's
 // there.  Ahead of the step's last products every wave has read all of the
 // step's buffers and the next step's loads are done: the barrier stands there,
@@ -143,10 +149,11 @@ __device__ __forceinline__ void read_frags(const uint8_t *ta, const uint8_t *tb,
 // that may still be under way at the barrier.  TAIL 1: no more steps to load
 // but B's last; 2: none.  A wave that is not ACTIVE has no rows and only stages.
 template <int ST, int BM, int BN, int C, int MT, int NT2, int TA, int TB, int WAIT, int TAIL, bool ACTIVE, typename OA,
-          typename OB, typename FT>
+          typename OB, typename FT, typename Hook>
 __device__ __forceinline__ void step_product(const OA &A, const OB &B, int s, int steps, uint8_t *ta, const uint8_t *tb,
                                              const uint8_t *na, const uint8_t *nb, uint8_t *wb, int m0, int n0,
-                                             f32x16_t (&acc)[MT][NT2], Frags<MT, NT2, FT> &f) {
+                                             f32x16_t (&acc)[MT][NT2], Frags<MT, NT2, FT> &f, const Hook &hook) {
+    if constexpr (ACTIVE) hook(s, ta, tb);
     constexpr int KS = C / 16;
     const bool more = !TAIL || s + 1 < steps;
 #pragma unroll
@@ -176,21 +183,22 @@ __device__ __forceinline__ void step_product(const OA &A, const OB &B, int s, in
 // pointer here is restrict (those scopes would hide the arrays'), reads are
 // one addition away from their array, and the loop has one exit.
 template <int ST, bool ACTIVE, int BM, int BN, int C, int MT, int NT2, int TA, int TB, typename FT = bf16x8_t, typename OA,
-          typename OB>
+          typename OB, typename Hook = NoHook>
 __device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *a0, uint8_t *b0, uint8_t *a1, uint8_t *b1,
                                          uint8_t *a2, uint8_t *b2, uint8_t *a3, uint8_t *b3, int steps, int m0, int n0,
-                                         f32x16_t (&acc)[MT][NT2]) {
+                                         f32x16_t (&acc)[MT][NT2], const Hook &hook = Hook{}) {
     constexpr int L = OA::LOADS + OB::LOADS;   // a wave's loads per step
     constexpr int W = (ST - 2) * L;
     if (steps == 0) return;
     Frags<MT, NT2, FT> f;
 #define STEP(S, WAIT, TAIL, AR, BR, AN, BN_, BP) \
-    step_product<ST, BM, BN, C, MT, NT2, TA, TB, WAIT, TAIL, ACTIVE>(A, B, S, steps, AR, BR, AN, BN_, BP, m0, n0, acc, f);
+    step_product<ST, BM, BN, C, MT, NT2, TA, TB, WAIT, TAIL, ACTIVE>(A, B, S, steps, AR, BR, AN, BN_, BP, m0, n0, acc, f, hook);
     A.load(0, a0);
     B.load(0, b0);
     if (steps == 1) {   // on its own: nothing to wait for but its loads
         wait_and_meet<0>();
         if (!ACTIVE) return;
+        hook(0, a0, b0);
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk) {
             read_frags<BM, BN, C, MT, NT2, TA, TB>(a0, b0, m0, n0, kk, 0, f);

@@ -182,7 +182,9 @@ def orth_norm_bound(G, steps, coefficients, eps, size):
             dA = 2 * S * xh + HALF * A + HALF_LEAST * n + 2 * K * U * F * F
             spec = float((b * s ** 2 + c * s ** 4).abs().max())
             dB = (abs(b) + 2 * abs(c) * S * S) * dA + HALF * (abs(b) + abs(c) * S * S) * A + HALF_LEAST * n + 2 * n * U * A * A
-            own = dB * S + spec * xh + abs(a) * 2.0 ** -21 * F + 2 * n * U * F * (abs(b) + abs(c) * S * S) * S
+            # X has 22 bits but ahead of the last of several steps, which takes its first piece
+            kept = xh if steps > 1 and i == steps - 1 else 2.0 ** -21 * F
+            own = dB * S + spec * xh + abs(a) * kept + 2 * n * U * F * (abs(b) + abs(c) * S * S) * S
             s1 = f(s)
             v, w = torch.cat([s1, torch.zeros(1, dtype=s.dtype)]), torch.cat([s1, torch.zeros(1, dtype=s.dtype)])
             d = torch.ones_like(v)
