@@ -258,6 +258,9 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     a.a = coefficients[0];
     a.b = coefficients[1];
     a.c = coefficients[2];
+    // B = c (b/c A + A^2): a c too small beside b to show is made one that divides
+    if (fabsf(a.c) < fabsf(a.b) * 0x1p-60f) a.c = a.b * 0x1p-60f;
+    a.b_over_c = a.c != 0.f ? a.b / a.c : 0.f;
     a.scale = scale;
     a.eps = eps;
     const SmallShape k = small_shape(N, K);

@@ -19,7 +19,7 @@ struct OrthArgs {
     uint16_t *A, *B;
     int n, N, K, side, ldx, lds, parts, g_bf16;
     int first, lo_in, lo_out, last;   // of a step: its X is G's, X has a lo, X' gets one, X' goes to out
-    float size, a, b, c, scale, eps;
+    float size, a, b, c, b_over_c, scale, eps;
 };
 
 __device__ __forceinline__ float half_value(uint32_t w, int high) { return half_to_float((uint16_t)(high ? w >> 16 : w)); }
@@ -32,18 +32,6 @@ __device__ __forceinline__ uint32_t half_pair(float a, float b) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t half_rows(const void *p, int M, int ld) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, __builtin_amdgcn_readfirstlane((int)((uint32_t)M * (uint32_t)ld * 2u)),
                                              0x00020000);
-}
-
-// This lane's 4 values of subtile (i, j), group q, at row m0 + 32 i + lane % 32, column n0 + 32 j + 8 q + 4 (lane / 32):
-// offset in bytes, past every buffer for columns behind ld.
-__device__ __forceinline__ uint32_t quad_at(int m0, int n0, int ld, int i, int j, int q) {
-    const int lane = threadIdx.x & 63, m = m0 + 32 * i + (lane & 31), n = n0 + 32 * j + 8 * q + 4 * (lane >> 5);
-    return n < ld ? ((uint32_t)m * (uint32_t)ld + n) * 2u : 0xFFFFFFF0u;
-}
-
-__device__ __forceinline__ f32x4_t load_quad(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    const u32x2_t w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
-    return f32x4_t{half_value(w[0], 0), half_value(w[0], 1), half_value(w[1], 0), half_value(w[1], 1)};
 }
 
 // 16 values of a subtile as fp16 pairs to rows of ld: 16-byte stores after the wave's halves have exchanged groups.
@@ -72,79 +60,6 @@ __device__ __forceinline__ bool range_tile(int64_t total, int64_t &t) {
     const int64_t per = (total + 7) >> 3, q = blockIdx.x >> 3;
     t = (int64_t)(blockIdx.x & 7) * per + q;
     return q < per && t < total;
-}
-
-// SQUARE 0: A = X X^T (ACROSS 1: X^T X), else B = b A + c A A: symmetric, so
-// only the tiles of the lower half are computed; those off the diagonal are
-// stored a second time, transposed.
-template <int BM, int WM, int WN, int ST, int C, int SQUARE, int ACROSS>
-__global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
-    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BM / 32 / WN;
-    typedef Operand<BM, ACROSS, NT, C> OA;
-    typedef Operand<BM, ACROSS, NT, C> OB;
-    GROUP_BUFFERS(ST, OA, OB)
-    const int nt = (a.side + BM - 1) / BM, tri = nt * (nt + 1) / 2;
-    int64_t t;
-    if (!range_tile((int64_t)a.n * tri, t)) return;
-    const int e = __builtin_amdgcn_readfirstlane((int)(t / tri));
-    int ti, tj;
-    lower_tile(__builtin_amdgcn_readfirstlane((int)(t - (int64_t)e * tri)), ti, tj);
-    ti = __builtin_amdgcn_readfirstlane(ti);
-    tj = __builtin_amdgcn_readfirstlane(tj);
-    const int64_t squares = (int64_t)a.side * a.lds;
-    const uint16_t *A0 = a.A + e * squares;
-    const uint16_t *X = SQUARE ? A0 : a.hi + (int64_t)e * a.N * a.ldx;
-    const int ld = SQUARE ? a.lds : a.ldx, cd = ACROSS ? a.N : ld;
-    const int r0 = ti * BM, k0 = tj * BM, M = min(a.side - r0, BM);
-    OA A;
-    OB B;
-    A.init(X, ld, r0, a.side, cd);
-    B.init(X, ld, k0, a.side, cd);
-    int m0, n0;
-    wave_place<WM, WN, MT, NT2>(m0, n0);
-    f32x16_t acc[MT][NT2];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT2; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    const int steps = (cd + C - 1) / C;
-    const bool active = m0 < M && k0 + n0 < a.lds;
-    if (!active) {
-        contract<ST, false, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
-        return;
-    }
-    contract<ST, true, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
-    uint16_t *to = (SQUARE ? a.B : a.A) + e * squares;
-    const auto old = half_rows(A0 + (int64_t)r0 * a.lds, M, a.lds), rows = half_rows(to + (int64_t)r0 * a.lds, M, a.lds);
-    const auto cols = half_rows(to + (int64_t)k0 * a.lds, min(a.side - k0, BM), a.lds);
-    const float r = SQUARE ? a.c : 1.f / (a.size * a.size);
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT2; ++j) {
-            uint32_t w[8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f32x4_t v = {acc[i][j][4 * q] * r, acc[i][j][4 * q + 1] * r, acc[i][j][4 * q + 2] * r, acc[i][j][4 * q + 3] * r};
-                if (SQUARE) v += a.b * load_quad(old, quad_at(m0, k0 + n0, a.lds, i, j, q));
-                w[2 * q] = half_pair(v[0], v[1]);
-                w[2 * q + 1] = half_pair(v[2], v[3]);
-            }
-            if (ti != tj) {
-                const int m = r0 + m0 + 32 * i + (lane & 31);
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int n = n0 + 32 * j + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
-                    const uint32_t at = m < a.lds ? ((uint32_t)n * (uint32_t)a.lds + m) * 2u : 0xFFFFFFF0u;
-                    const uint32_t x = w[v / 2];
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v & 1 ? x >> 16 : x), cols, at, 0, 0);
-                }
-            }
-            store_halves(rows, m0, k0 + n0, a.lds, i, j, w);
-        }
 }
 
 // a X added to a tile's sums while the rows (TALL: columns) of the tile pass
@@ -181,6 +96,100 @@ template <int BN, int MT, int NT2, int TALL> struct AddX {
             }
     }
 };
+
+// SQUARE 0: A = X X^T (ACROSS 1: X^T X), else B = b A + c A A: symmetric, so
+// only the tiles of the lower half are computed.  Those off the diagonal are
+// stored a second time, transposed: a wave turns its part in LDS, where 16-byte
+// stores would otherwise be 2-byte ones.  b A is met as an operand passes
+// through LDS (b/c A is, ahead of the factor c).
+template <int BM, int WM, int WN, int ST, int C, int SQUARE, int ACROSS>
+__global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
+    constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BM / 32 / WN;
+    typedef Operand<BM, ACROSS, NT, C> OA;
+    typedef Operand<BM, ACROSS, NT, C> OB;
+    GROUP_BUFFERS(ST, OA, OB)
+    const int nt = (a.side + BM - 1) / BM, tri = nt * (nt + 1) / 2;
+    int64_t t;
+    if (!range_tile((int64_t)a.n * tri, t)) return;
+    const int e = __builtin_amdgcn_readfirstlane((int)(t / tri));
+    int ti, tj;
+    lower_tile(__builtin_amdgcn_readfirstlane((int)(t - (int64_t)e * tri)), ti, tj);
+    ti = __builtin_amdgcn_readfirstlane(ti);
+    tj = __builtin_amdgcn_readfirstlane(tj);
+    const int64_t squares = (int64_t)a.side * a.lds;
+    const uint16_t *A0 = a.A + e * squares;
+    const uint16_t *X = SQUARE ? A0 : a.hi + (int64_t)e * a.N * a.ldx;
+    const int ld = SQUARE ? a.lds : a.ldx, cd = ACROSS ? a.N : ld;
+    const int r0 = ti * BM, k0 = tj * BM, M = min(a.side - r0, BM);
+    OA A;
+    OB B;
+    A.init(X, ld, r0, a.side, cd);
+    B.init(X, ld, k0, a.side, cd);
+    int m0, n0;
+    wave_place<WM, WN, MT, NT2>(m0, n0);
+    f32x16_t acc[MT][NT2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int steps = (cd + C - 1) / C;
+    const bool active = m0 < M && k0 + n0 < a.lds;
+    if (!active) {
+        contract<ST, false, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+    } else if constexpr (SQUARE) {
+        const AddX<BM, MT, NT2, 1> hook{acc, a.b_over_c, k0 + n0, m0, n0, true};
+        contract<ST, true, BM, BM, C, MT, NT2, 0, 0, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
+    } else {
+        contract<ST, true, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
+    }
+    uint16_t *to = (SQUARE ? a.B : a.A) + e * squares;
+    const float r = SQUARE ? a.c : 1.f / (a.size * a.size);
+    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    uint32_t w[MT][NT2][8];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[i][j][q] = half_pair(acc[i][j][2 * q] * r, acc[i][j][2 * q + 1] * r);
+    if (ti != tj) {
+        // the wave's part [32 NT2 columns][32 MT rows], rows 16 bytes apart from a multiple of the banks
+        constexpr int LD = 32 * MT + 8, PER = ST == 2 ? 2 : 1, PART = OA::BYTES / PER;
+        static_assert(32 * NT2 * LD * 2 <= PART && WM * WN <= 2 * ST * PER, "a place for every wave");
+        __syncthreads();   // every wave has read its last step
+        const int u = wv / PER;
+        uint8_t *const p = (u == 0 ? a0 : u == 1 ? b0 : u == 2 ? a1 : u == 3 ? b1 : u == 4 ? a2 : u == 5 ? b2 : u == 6 ? a3 : b3) + wv % PER * PART;
+        if (active) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const int n = 32 * j + 8 * (v / 4) + 4 * h + (v & 3);
+                        const uint32_t x = w[i][j][v / 2];
+                        *(uint16_t *)(p + (n * LD + 32 * i + l) * 2) = (uint16_t)(v & 1 ? x >> 16 : x);
+                    }
+            const auto cols = half_rows(to + (int64_t)k0 * a.lds, min(a.side - k0, BM), a.lds);
+            constexpr int CH = 4 * MT;   // 16-byte pieces of a row
+#pragma unroll
+            for (int q = 0; q < 32 * NT2 * CH / 64; ++q) {
+                const int n = (64 * q + lane) / CH, c = (64 * q + lane) % CH, m = r0 + m0 + 8 * c;
+                const u32x4_t x = *(const u32x4_t *)(p + (n * LD + 8 * c) * 2);
+                const uint32_t at = m < a.lds ? ((uint32_t)(n0 + n) * (uint32_t)a.lds + m) * 2u : 0xFFFFFFF0u;
+                __builtin_amdgcn_raw_buffer_store_b128(x, cols, at, 0, 0);
+            }
+        }
+    }
+    if (!active) return;
+    const auto rows = half_rows(to + (int64_t)r0 * a.lds, M, a.lds);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT2; ++j) store_halves(rows, m0, k0 + n0, a.lds, i, j, w[i][j]);
+}
 
 // X' = a X + B X (TALL: a X + X B, B symmetric), the last one to out.
 template <int BM, int BN, int WM, int WN, int ST, int TALL>

@@ -512,6 +512,22 @@ def test_orthogonalise_zeros_infinities_and_scales():
         assert torch.equal(run_orth((G[[0, 4]] * s).cuda(), 5, COEF, 1.0, 2.0 ** -24 * s), want)
 
 
+@pytest.mark.parametrize("c", [(1.0, 0.0, 0.0), (0.0, 1.0, 0.0), (0.0, 0.0, 1.0), (1.5, -0.5, 0.0), (2.0, -1.5, 1e-30), (0.0, 0.0, 0.0),
+                               (2.0, -1.2, 0.2)])
+@pytest.mark.parametrize("n,N,K", [(2, 60, 72), (3, 200, 300), (3, 300, 200), (70, 256, 264)])
+def test_orthogonalise_other_polynomials(n, N, K, c):
+    """Terms apart, coefficients of zero: one step elementwise, three in Frobenius norm."""
+    G = orth_case(n, N, K, F32, seed=5)
+    c = tuple(f32(v) for v in c)
+    got = run_orth(G.cuda(), 1, c, 1.0, 1e-7)
+    g = G[:3].double()
+    check(got[:3], R.orthogonalise(g, 1, c, 1.0, f32(1e-7)), R.orth_one_step_bound(g, c, 1.0, f32(1e-7), size_of(N, K)), "one step")
+    got = run_orth(G.cuda(), 3, c, 1.0, 1e-7)[:3]
+    ref = R.orthogonalise(g, 3, c, 1.0, f32(1e-7))
+    bound = R.orth_norm_bound(g, 3, c, f32(1e-7), size_of(N, K)) + 2.0 ** -8 * ref.flatten(1).norm(dim=1)
+    assert bool(((got.cpu().double() - ref).flatten(1).norm(dim=1) <= bound).all())
+
+
 def test_orthogonalise_in_place():
     for n, N, K in ((3, 72, 136), (2, 130, 61)):
         G = orth_case(n, N, K, BF).cuda()
