@@ -184,10 +184,12 @@ template <typename W, int V> __global__ __launch_bounds__(256) void embed_join_k
     }
 }
 
-// n 16-byte pieces of zeros, and the bytes behind them: the share of block b of nb.
+// n 16-byte pieces of zeros, and the bytes behind them: the share of block b of
+// nb, in one piece (524 MB beside the sort: 126 us the gradient, 133 where the
+// blocks go through it side by side).
 __device__ __forceinline__ void embed_zeros(u32x4_t *p, int64_t n, int rest, int b, int nb) {
-    const int64_t step = (int64_t)nb * SORT_TH;
-    for (int64_t i = (int64_t)b * SORT_TH + threadIdx.x; i < n; i += step) p[i] = u32x4_t{0, 0, 0, 0};
+    const int64_t per = (n + nb - 1) / nb, i0 = b * per, i1 = min(i0 + per, n);
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += SORT_TH) p[i] = u32x4_t{0, 0, 0, 0};
     if (b == 0 && (int)threadIdx.x < rest) ((uint8_t *)(p + n))[threadIdx.x] = 0;
 }
 

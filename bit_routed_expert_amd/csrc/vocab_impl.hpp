@@ -146,25 +146,40 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
             for (int i = 0; i < MT; ++i) {
                 const int row = row0 + m0 + 32 * i + l;
                 const int want = (row < n ? FEW ? a.targets[bit_of(there, row)] : a.tc[row] : -1) - a.v0 - c0 - n0 - 4 * h;   // the target's place among the columns
-                float m = -INFINITY, s = 0.f, picked = 0.f;
-                bool mine = false;
+                if (__any((uint32_t)want < 32u * NT2)) {
+                    float picked = 0.f;
+                    bool mine = false;
+#pragma unroll
+                    for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) {
+                            const int at = 32 * j + 8 * (v / 4) + (v & 3);
+                            picked = at == want ? acc[i][j][v] : picked;
+                            mine |= at == want;
+                        }
+                    if (mine) a.zt[row] = picked;
+                }
+                if (c0 + n0 + 32 * NT2 > a.pw) {   // columns behind the last one
+#pragma unroll
+                    for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (c0 + n0 + 4 * h + 32 * j + 8 * (v / 4) + (v & 3) >= a.pw) acc[i][j][v] = -INFINITY;
+                }
+                float m = -INFINITY, s = 0.f;
 #pragma unroll
                 for (int j = 0; j < NT2; ++j)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int at = 32 * j + 8 * (v / 4) + (v & 3);
-                        picked = at == want ? acc[i][j][v] : picked;
-                        mine |= at == want;
-                        if (c0 + n0 + 4 * h + at >= a.pw) acc[i][j][v] = -INFINITY;
-                        m = fmaxf(m, acc[i][j][v]);
-                    }
-                if (mine) a.zt[row] = picked;
+                    for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[i][j][v]);
                 m = fmaxf(m, lane_xor<32>(m));
-                const float base = m == -INFINITY ? 0.f : m;
+                // one fma a value; what the rounding of m log2(e) makes of all of them goes back at the end
+                const float base = m == -INFINITY ? 0.f : m * VOCAB_LOG2E;
+                const float off = m == -INFINITY ? 0.f : fmaf(m, VOCAB_LOG2E, -base);
 #pragma unroll
                 for (int j = 0; j < NT2; ++j)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) s += exp_diff(acc[i][j][v], base);
+                    for (int v = 0; v < 16; ++v) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], VOCAB_LOG2E, -base));
+                s *= __builtin_amdgcn_exp2f(-off);
                 s += lane_xor<32>(s);
                 if (h == 0) stat[(m0 + 32 * i + l) * WN + n0 / (32 * NT2)] = float2{m, s};
             }
@@ -195,15 +210,26 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
             un[i] = a.dc[row];
             want[i] = a.tc[row] - a.v0;
         }
+        const bool ragged = c0 + n0 + 32 * NT2 > a.pw;   // columns behind the last one
         uint16_t *hi = a.hi + (int64_t)row0 * a.ldv, *lo = a.lo + (int64_t)row0 * a.ldv;
         each_quad<MT, NT2>(m0, c0 + n0, acc, [&](int, int col, int i, f32x4_t &v) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float p = exp_diff(v[c], lse[i]) * up[i];
-                p -= col + c == want[i] ? un[i] : 0.f;
-                v[c] = col + c < a.pw ? p : 0.f;
+            for (int c = 0; c < 4; ++c) v[c] = exp_diff(v[c], lse[i]) * up[i];
+            if (ragged) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = col + c < a.pw ? v[c] : 0.f;
             }
         });
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int place = want[i] - c0 - n0 - 4 * h;
+            if (__any((uint32_t)place < 32u * NT2)) {
+#pragma unroll
+                for (int j = 0; j < NT2; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) acc[i][j][v] -= 32 * j + 8 * (v / 4) + (v & 3) == place ? un[i] : 0.f;
+            }
+        }
         store_tile<MT, NT2>(hi, 1, m0, rows, c0 + n0, a.ldv, acc);
         if constexpr (GRAD == 2) {   // what the first piece leaves
             each_quad<MT, NT2>(m0, c0 + n0, acc, [&](int, int, int, f32x4_t &v) {
