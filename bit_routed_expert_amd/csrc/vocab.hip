@@ -158,7 +158,7 @@ RowTile row_tile(int T) { return T <= 32 ? ROWS_32 : T <= 512 ? ROWS_128 : ROWS_
 constexpr int TILE_ROWS[] = {32, 128, 256}, TILE_COLS[] = {128, 256, 256};
 
 struct VocabPlan {
-    int piece, splits, span;
+    int piece, splits;
     size_t map, tc, hc, zt, part, lc, gc, dc, hi, lo, acc, bytes;
 };
 
@@ -196,7 +196,6 @@ VocabPlan vocab_plan(int32_t T, int32_t V, int32_t d, bool grad) {
         const int64_t most = p.piece / 512;
         s = s > most ? most : s;
         p.splits = (int)(s < 1 ? 1 : s);
-        p.span = (int)up_to((p.piece + p.splits - 1) / p.splits, 64);
         p.hi = take((size_t)T * p.piece * 2);
         p.lo = take((size_t)T * p.piece * 2);
         p.acc = take((size_t)p.splits * T * d * 4);
@@ -370,7 +369,6 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
     a.lo = (uint16_t *)(w + p.lo);
     a.acc = (float *)(w + p.acc);
     a.splits = p.splits;
-    a.span = p.span;
     const bool h2 = dh && !a.dh_bf16, w2 = dW && !a.dw_bf16;   // outputs that take both pieces of dz
     STRATA_LAUNCH(vocab_pack_kernel<1>, dim3((T + a.rows_block - 1) / a.rows_block), dim3(256), 0, s, a);
     VOCAB_TRY;
@@ -379,6 +377,7 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
         a.pw = V - v0 < p.piece ? V - v0 : p.piece;
         a.ldv = (int)up_to(a.pw, 8);
         a.first = v0 == 0;
+        a.span = (int)up_to((a.pw + p.splits - 1) / p.splits, 64);
         strata_status q = h2 || w2 ? launch_logits<2>(a, s) : launch_logits<1>(a, s);
         if (q == STRATA_OK && dW) q = w2 ? launch_dw<2>(a, s) : launch_dw<1>(a, s);
         if (q == STRATA_OK && dh) q = h2 ? launch_dh<2>(a, s) : launch_dh<1>(a, s);
