@@ -669,3 +669,188 @@ def test_two_calls_under_way_together():
     torch.cuda.synchronize()
     for c, w in zip(a + b, want):
         assert same(c[3], w), c[0]
+
+
+# ------------------------------------------------------- offsets past 2^31
+
+def test_balance_past_32_bits():
+    T, k, E = (1 << 21) + 5, 1, 1024
+    z = torch.zeros(T, E, dtype=BF, device="cuda")
+    z[-1, 1000], z[-2, 3] = 5.0, -INF
+    idx = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    losses, counts, prob, lse, tokens = run_balance(z, idx, None, T, k, E)
+    assert int(tokens) == T and int(counts[0]) == T
+    want = torch.log(torch.tensor([1023 + 2.718281828459045 ** 5, 1023.0, 1024.0], dtype=torch.float64))
+    O.check(lse[[-1, -2, -3]].cpu(), want, (E + 40) * U, "lse")
+    dl = torch.tensor([0.0, 1.0]).cuda()
+    brx.balance_loss_backward(z, 0, idx, T, k, E, lse, counts, tokens, dl, z)
+    row = torch.exp(torch.tensor([0.0, 5.0], dtype=torch.float64) - want[0]) * 2 * want[0] / T
+    O.check(z[-1, [0, 1000]].cpu(), row, (2 * E + 80) * U * row, "dz")
+    assert float(z[-2, 3]) == 0.0 and int(torch.count_nonzero(z[-2])) == E - 1
+
+
+def test_vocab_loss_past_32_bits():
+    T, V, d = 3, 1 << 20, 2056
+    assert V * d > 1 << 31
+    W = torch.zeros(V, d, dtype=BF, device="cuda")
+    rows = torch.tensor([V - 1, V - 2, 5, (1 << 31) // d + 1])
+    W[rows.cuda()] = rand(4, d, seed=1, dtype=BF, scale=0.1).cuda()
+    h = rand(T, d, seed=2, dtype=BF).cuda()
+    t = torch.tensor([V - 1, 77, (1 << 31) // d + 1], dtype=torch.int32).cuda()
+    loss, lse = run_vocab(h, W, t, T, V, d)
+    z = h.double() @ W[rows.cuda()].double().t()
+    want = torch.log(z.exp().sum(1) + V - 4)
+    bound = 2 * d * U * (h.double().abs() @ W[rows.cuda()].double().abs().t()).max() + (V + 64) * U
+    check(lse, want, bound, "lse")
+    check(loss, want - torch.stack([z[0, 0], z[1, 0] * 0, z[2, 3]]), 2 * bound, "loss")
+    up = torch.ones(T, device="cuda")
+    dh, dW = Out(T, d, dtype=F32), torch.full((V, d), 3.0, dtype=BF, device="cuda")
+    nb = brx.vocab_loss_backward_workspace_bytes(T, V, d)
+    brx.vocab_loss_backward(h, W, t, T, V, d, lse, up, ws_of(nb), nb, dh=dh.t, dhdtype=1, dW=dW)
+    p = torch.exp(z - lse.double()[:, None])
+    p[0, 0] -= 1
+    p[2, 3] -= 1
+    ref = p @ W[rows.cuda()].double()
+    check(dh.guarded(), ref, (2.0 ** -16 + 4 * bound) * (p.abs() @ W[rows.cuda()].double().abs()) + 8 * U * ref.abs(), "dh")
+    ref = p.t() @ h.double()
+    check(dW[rows.cuda()], ref, (2.0 ** -8 + 4 * bound) * (p.abs().t() @ h.double().abs()), "dW")
+    q = torch.exp(-lse.double())[:, None]
+    rest = (q * h.double()).sum(0)
+    check(dW[V // 2], rest, (2.0 ** -8 + 4 * bound) * (q * h.double().abs()).sum(0), "dW of a row of zeros")
+
+
+def test_orthogonalise_past_32_bits():
+    n, N, K = 600, 1900, 1900
+    G = torch.zeros(n, N, K, device="cuda")
+    few = [0, 497, 598, 599]
+    for e in few:
+        G[e] = rand(N, K, seed=e).cuda()
+    out = torch.full((n, N, K), 3.0, dtype=BF, device="cuda")
+    nb = brx.orthogonalise_workspace_bytes(n, N, K)
+    brx.orthogonalise(G, 1, n, N, K, out, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb, steps=1)
+    c = tuple(f32(v) for v in COEF)
+    for e in few:
+        g = G[e:e + 1].double()
+        check(out[e:e + 1], R.orthogonalise(g, 1, c, 1.0, f32(1e-7)), R.orth_one_step_bound(g, c, 1.0, f32(1e-7), size_of(N, K)),
+              f"matrix {e}")
+        out[e] = 0
+    assert int(torch.count_nonzero(out)) == 0
+
+
+# ------------------------------------------------------------- all together
+
+def test_a_training_step():
+    """Token rows in -> norm -> router, its balance losses and its picks ->
+    sparse experts -> residual -> norm -> vocabulary loss over the same table,
+    all gradients (the table's from both ends, the router's from the loss and
+    from its own losses), and the experts' update orthogonalised, against
+    automatic differentiation in 64 bits with the same picks.  Rows between the
+    operators are bf16: each of the about twelve roundings on a path is at most
+    2^-8 of its value, and independent ones add in squares, so losses and
+    gradients are within 12 * 2^-8 in 2-norm."""
+    T, V, d, E, k, f = 120, 500, 256, 16, 4, 128
+    sh = brx.shape(E, k, d, f, 3)
+    table = rand(V, d, seed=1, dtype=BF, scale=0.1)
+    Wr, g0, g1 = rand(E, d, seed=2, scale=d ** -0.5), 1 + 0.1 * rand(d, seed=3), 1 + 0.1 * rand(d, seed=4)
+    W1, W2 = rand(E, 2 * f, d, seed=6, dtype=BF, scale=d ** -0.5), rand(E, d, f, seed=7, dtype=BF, scale=f ** -0.5)
+    ids, targets = draw_ids(T, V, 8, pad=0.0), draw_ids(T, V, 9, pad=0.25)
+    n, has = T * k, (targets >= 0) & (targets < V)
+    m = int(has.sum())
+    c_balance, c_z, c_lse, scale = 0.05, 0.01, 0.002, 10.0
+    TB, WR, G0, G1, W1c, W2c, I, TG = (v.cuda() for v in (table, Wr, g0, g1, W1, W2, ids, targets))
+    e = lambda *s, dt=F32: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
+    # forward
+    x = e(T, d)
+    brx.embed(TB, 0, V, d, I, T, scale, x, 1)
+    a0 = brx.block_norm_args(T, d, 1, 0, 0, brx.PRE_NORM)
+    u, r0 = e(T, d, dt=BF), e(T)
+    brx.block_norm(a0, x, None, g_pre=G0, u=u, rstd_r=r0)
+    nb = brx.workspace_bytes(sh, T)
+    ro = dict(topk_idx=e(T, k, dt=torch.int32), topk_w=e(T, k))
+    brx.route(sh, brx.LayerData(router_w=WR, codes=None, scales=None), u, brx.X_BF16, T, ro, ws_of(nb), nb)
+    z = u.float() @ WR.t()
+    losses, counts, lse_r, tokens = e(2), e(E, dt=torch.int32), e(T), e(1, dt=torch.int32)
+    bb = brx.balance_loss_workspace_bytes(T, k, E)
+    brx.balance_loss(z, 1, ro["topk_idx"], T, k, E, losses, counts, lse_r, tokens, ws_of(bb), bb)
+    off, pos = e(E + 1, dt=torch.int32), e(n, dt=torch.int32)
+    sb = brx.sort_workspace_bytes(T, k, E)
+    brx.sort_picks(ro["topk_idx"], T, k, E, None, off, None, pos, ws_of(sb), sb)
+    xs, gu, ys = e(n, d, dt=BF), e(n, 2 * f, dt=BF), e(n, d, dt=BF)
+    brx.dispatch(u, 0, T, k, d, pos, xs, n)
+    gb = max(brx.grouped_workspace_bytes(n, E, 2 * f, d), brx.grouped_workspace_bytes(n, E, d, f))
+    gws = ws_of(gb)
+    brx.grouped_product(xs, W1c, off, n, E, 2 * f, d, gu, 0, gws, gb)
+    gl, ul = gu.float()[:, :f], gu.float()[:, f:]
+    hh = (gl * torch.sigmoid(gl) * ul).to(BF)
+    brx.grouped_product(hh, W2c, off, n, E, d, f, ys, 0, gws, gb)
+    y = e(T, d, dt=BF)
+    brx.combine(ys, 0, n, pos, ro["topk_w"], T, k, d, y, 0)
+    a1 = brx.block_norm_args(T, d, 1, 0, 0, brx.PRE_NORM)
+    r, h, sr = e(T, d), e(T, d, dt=BF), e(T)
+    brx.block_norm(a1, x, y, g_pre=G1, r=r, u=h, rstd_r=sr)
+    loss, lse = e(T), e(T)
+    vb = brx.vocab_loss_workspace_bytes(T, V, d)
+    brx.vocab_loss(h, TB, TG, T, V, d, loss, lse, ws_of(vb), vb)
+    # backward of mean loss + c_lse mean lse^2 + c_balance balance + c_z z loss
+    up, un = torch.full((T,), 1.0 / m, device="cuda"), 2 * c_lse / m * lse
+    dh, dT = e(T, d, dt=BF), e(V, d)
+    vb = brx.vocab_loss_backward_workspace_bytes(T, V, d)
+    brx.vocab_loss_backward(h, TB, TG, T, V, d, lse, up, ws_of(vb), vb, dlse=un, dh=dh, dW=dT, dwdtype=1)
+    dX, dy, dg1 = e(T, d), e(T, d, dt=BF), e(d)
+    wb = brx.block_norm_backward_workspace_bytes(a1)
+    brx.block_norm_backward(a1, None, dh, r, y, g_pre=G1, rstd_r=sr, dx=dX, dy=dy, dg_pre=dg1, ws=ws_of(wb), ws_bytes=wb)
+    dys, dpk = e(n, d, dt=BF), e(T, k)
+    brx.combine_backward(dy, 0, ys, 0, n, pos, ro["topk_w"], T, k, d, dys=dys, dz=dpk)
+    dhh, dxs, dW1, dW2 = e(n, f), e(n, d, dt=BF), e(E, 2 * f, d), e(E, d, f)
+    brx.grouped_dgrad(dys, W2c, off, n, E, d, f, dhh, 1, gws, gb)
+    brx.grouped_wgrad(dys, hh, off, n, E, d, f, dW2, 1, gws, gb)
+    sg = torch.sigmoid(gl)
+    dgu = torch.cat([dhh * ul * sg * (1 + gl * (1 - sg)), dhh * gl * sg], 1).to(BF)
+    brx.grouped_dgrad(dgu, W1c, off, n, E, 2 * f, d, dxs, 0, gws, gb)
+    brx.grouped_wgrad(dgu, xs, off, n, E, 2 * f, d, dW1, 1, gws, gb)
+    du = e(T, d, dt=BF)
+    brx.dispatch_backward(dxs, 0, n, pos, T, k, d, du)
+    dz = e(T, E)
+    brx.balance_loss_backward(z, 1, ro["topk_idx"], T, k, E, lse_r, counts, tokens, torch.tensor([c_balance, c_z], device="cuda"),
+                              dz, dpicks=dpk)
+    dWr = dz.t().contiguous() @ u.float()
+    du_all = (du.float() + dz @ WR).to(BF)
+    dXn, dg0 = e(T, d), e(d)
+    wb0 = brx.block_norm_backward_workspace_bytes(a0)
+    brx.block_norm_backward(a0, dX, du_all, x, None, g_pre=G0, rstd_r=r0, dx=dXn, dg_pre=dg0, ws=ws_of(wb0), ws_bytes=wb0)
+    eb = brx.embed_backward_workspace_bytes(T, V, d)
+    brx.embed_backward(dXn, 1, I, T, V, d, scale, dT, 1, ws_of(eb), eb, flags=brx.ACCUMULATE)
+    ob = brx.orthogonalise_workspace_bytes(E, 2 * f, d)
+    step = e(E, 2 * f, d, dt=BF)
+    brx.orthogonalise(dW1, 1, E, 2 * f, d, step, ws_of(ob), ob)
+    torch.cuda.synchronize()
+    # the same in 64 bits
+    L = {q: v.double().clone().requires_grad_(True) for q, v in dict(table=table, Wr=Wr, g0=g0, g1=g1, W1=W1, W2=W2).items()}
+    idx = ro["topk_idx"].cpu().long()
+    eps = f32(1e-6)
+    xd = L["table"][ids.long()] * scale
+    ud = O.norm_rows(xd, L["g0"], eps)
+    zd = ud @ L["Wr"].t()
+    bal, _, _, _, _ = R.balance(zd, idx, None, E)
+    wd = torch.softmax(zd.gather(1, idx), 1)
+    yd = torch.zeros(T, d, dtype=torch.float64)
+    for q in range(k):
+        guv = torch.bmm(L["W1"][idx[:, q]], ud[:, :, None])[:, :, 0]
+        hv = torch.nn.functional.silu(guv[:, :f]) * guv[:, f:]
+        yd = yd + wd[:, q:q + 1] * torch.bmm(L["W2"][idx[:, q]], hv[:, :, None])[:, :, 0]
+    hd = O.norm_rows(xd + yd, L["g1"], eps)
+    ld, sd, _ = R.vocab(hd, L["table"], targets)
+    total = ld.sum() / m + c_lse * sd.square().sum() / m + c_balance * bal[0] + c_z * bal[1]
+    names = ("table", "Wr", "g0", "g1", "W1", "W2")
+    grads = dict(zip(names, torch.autograd.grad(total, [L[q] for q in names])))
+    for q, got, ref in (("loss", loss, ld), ("lse", lse, sd), ("balance", losses, bal), ("table", dT, grads["table"]),
+                        ("Wr", dWr, grads["Wr"]), ("g0", dg0, grads["g0"]), ("g1", dg1, grads["g1"]), ("W1", dW1, grads["W1"]),
+                        ("W2", dW2, grads["W2"])):
+        ref = ref.detach()
+        off_by = float((got.cpu().double() - ref).norm() / ref.norm())
+        print(f"  {q}: {off_by:.2e}", flush=True)
+        assert off_by <= 12 * 2.0 ** -8, f"{q}: off by {off_by:.3e} in 2-norm"
+    G, c = dW1.cpu().double(), tuple(f32(v) for v in COEF)
+    ref = R.orthogonalise(G, 5, c, 1.0, f32(1e-7))
+    bound = R.orth_norm_bound(G, 5, c, f32(1e-7), size_of(2 * f, d)) + 2.0 ** -8 * ref.flatten(1).norm(dim=1)
+    assert bool(((step.cpu().double() - ref).flatten(1).norm(dim=1) <= bound).all())
