@@ -152,13 +152,66 @@ strata_status check_vocab(int32_t T, int32_t V, int32_t d) {
 
 int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// Row tiles by the tokens of the call (how many have a target only the device knows).
-enum RowTile { ROWS_32, ROWS_128, ROWS_256 };
-RowTile row_tile(int T) { return T <= 32 ? ROWS_32 : T <= 512 ? ROWS_128 : ROWS_256; }
-constexpr int TILE_ROWS[] = {32, 128, 256}, TILE_COLS[] = {128, 256, 256};
+// Tiles, and what a round of them over the CUs costs (a tile of 256 square 100).
+// A launch takes the tile whose rounds cost least: most calls have a few rounds
+// or a part of one, and their number matters more than a tile's own rate.  By the
+// tokens of the call: how many have a target only the device knows.  Calls of up
+// to 32 tokens, which the matrix bounds, take tiles of 32 rows.  64 x 128 and, of
+// dW, 64 square against 256 square and 128 square: 2655 tokens, 1287 x 160, both
+// gradients, 99 -> 56 us; 128 x 256 against 256 square: 2828 tokens, 6228 x 1032,
+// the loss, 73 -> 68 us.
+enum Tile { ROWS_32, ROWS_64, ROWS_128, ROWS_256 };
+constexpr int TILE_ROWS[] = {32, 64, 128, 256}, TILE_COLS[] = {128, 128, 256, 256}, TILE_COST[] = {12, 20, 56, 100};
+int64_t tiles_of(Tile k, int64_t rows, int64_t cols) {
+    return (rows + TILE_ROWS[k] - 1) / TILE_ROWS[k] * ((cols + TILE_COLS[k] - 1) / TILE_COLS[k]);
+}
+Tile logits_tile(int64_t T, int64_t pw) {
+    if (T <= 32) return ROWS_32;
+    Tile best = ROWS_256;
+    int64_t least = INT64_MAX;
+    for (const Tile k : {ROWS_256, ROWS_128, ROWS_64}) {
+        const int64_t c = (tiles_of(k, T, pw) + 255) / 256 * TILE_COST[k];
+        if (c < least) best = k, least = c;
+    }
+    return best;
+}
+
+// Tile of dh and the spans that its contraction over a piece's columns is cut
+// into, 512 columns or more each; a span's sums cost as much as 8 of its rounds.
+struct DhTile {
+    Tile tile;
+    int splits;
+};
+DhTile dh_tile(int64_t T, int64_t d, int64_t piece) {
+    DhTile best{ROWS_32, 1};
+    int64_t least = INT64_MAX;
+    const int64_t most = piece / 512 > 1 ? piece / 512 : 1;
+    for (const Tile k : {ROWS_256, ROWS_128, ROWS_64, ROWS_32}) {
+        if ((T <= 32) != (k == ROWS_32)) continue;
+        const int64_t t = tiles_of(k, T, d);
+        int64_t s = t ? 256 / t : 1;
+        s = s < 1 ? 1 : s > most ? most : s;
+        const int64_t c = (t * s + 255) / 256 * TILE_COST[k] * 64 / s + 8 * s;
+        if (c < least) best = DhTile{k, (int)s}, least = c;
+    }
+    return best;
+}
+
+// Tiles of dW, squares: one of 256 to a CU, up to three of 128 or two of 64, which alone on a CU take less.
+enum Square { SQUARE_64, SQUARE_128, SQUARE_256 };
+Square dw_tile(int64_t pw, int64_t d) {
+    const auto count = [&](int64_t n) { return (pw + n - 1) / n * ((d + n - 1) / n); };
+    const int64_t t256 = count(256), t128 = count(128), t64 = count(64);
+    const int64_t c256 = (t256 + 255) / 256 * 100;
+    const int64_t c128 = t128 <= 256 ? 35 : t128 <= 512 ? 55 : (t128 + 767) / 768 * 75;
+    const int64_t c64 = t64 <= 256 ? 14 : (t64 + 511) / 512 * 18;
+    return c64 < c128 && c64 < c256 ? SQUARE_64 : c128 < c256 ? SQUARE_128 : SQUARE_256;
+}
 
 struct VocabPlan {
-    int piece, splits;
+    int piece;
+    Tile tile;    // of the loss
+    DhTile dh;
     size_t map, tc, hc, zt, part, lc, gc, dc, hi, lo, acc, bytes;
 };
 
@@ -179,26 +232,22 @@ VocabPlan vocab_plan(int32_t T, int32_t V, int32_t d, bool grad) {
         at += (n + 255) / 256 * 256;
         return q;
     };
-    const RowTile k = row_tile(T);
     p.map = take((size_t)T * 4);
     p.tc = take((size_t)T * 4);
     p.hc = take((size_t)T * d * 2);
     if (!grad) {
         p.zt = take((size_t)T * 4);
-        p.part = take((size_t)((V + TILE_COLS[k] - 1) / TILE_COLS[k]) * up_to(T, 16) * 8);
+        p.tile = logits_tile(T, V);
+        p.part = take((size_t)((V + TILE_COLS[p.tile] - 1) / TILE_COLS[p.tile]) * up_to(T, 16) * 8);
     } else {
         p.lc = take((size_t)T * 4);
         p.gc = take((size_t)T * 4);
         p.dc = take((size_t)T * 4);
         p.piece = piece_columns(T > 0 ? T : 1, V);
-        const int64_t tiles = ((T + TILE_ROWS[k] - 1) / TILE_ROWS[k]) * (int64_t)((d + TILE_COLS[k] - 1) / TILE_COLS[k]);
-        int64_t s = tiles ? 256 / tiles : 1;
-        const int64_t most = p.piece / 512;
-        s = s > most ? most : s;
-        p.splits = (int)(s < 1 ? 1 : s);
+        p.dh = dh_tile(T, d, p.piece);
         p.hi = take((size_t)T * p.piece * 2);
         p.lo = take((size_t)T * p.piece * 2);
-        p.acc = take((size_t)p.splits * T * d * 4);
+        p.acc = take((size_t)p.dh.splits * T * d * 4);
     }
     p.bytes = at;
     return p;
@@ -223,8 +272,7 @@ dim3 tile_grid(int64_t nr, int64_t nc) { return dim3((unsigned)up_to(nr * nc, 8)
         if (e_ != hipSuccess) return hip_status(e_);              \
     } while (0)
 
-template <int GRAD> strata_status launch_logits(const VocabArgs &a, hipStream_t s) {
-    const RowTile k = row_tile(a.T);
+template <int GRAD> strata_status launch_logits(const VocabArgs &a, Tile k, hipStream_t s) {
     const dim3 g = tile_grid((a.T + TILE_ROWS[k] - 1) / TILE_ROWS[k], (a.pw + TILE_COLS[k] - 1) / TILE_COLS[k]);
     if constexpr (GRAD != 0) {   // a forward call of few rows has its own
         if (k == ROWS_32) {
@@ -232,28 +280,27 @@ template <int GRAD> strata_status launch_logits(const VocabArgs &a, hipStream_t 
             return hip_status(hipGetLastError());
         }
     }
-    if (k == ROWS_128) STRATA_LAUNCH((vocab_logits_kernel<128, 256, 2, 4, 3, GRAD>), g, dim3(512), 0, s, a);
+    if (k == ROWS_64) STRATA_LAUNCH((vocab_logits_kernel<64, 128, 2, 2, 4, GRAD>), g, dim3(256), 0, s, a);
+    else if (k == ROWS_128) STRATA_LAUNCH((vocab_logits_kernel<128, 256, 2, 4, 3, GRAD>), g, dim3(512), 0, s, a);
     else STRATA_LAUNCH((vocab_logits_kernel<256, 256, 2, 4, 2, GRAD>), g, dim3(512), 0, s, a);
     return hip_status(hipGetLastError());
 }
 
-template <int PIECES> strata_status launch_dh(const VocabArgs &a, hipStream_t s) {
-    const RowTile k = row_tile(a.T);
+template <int PIECES> strata_status launch_dh(const VocabArgs &a, Tile k, hipStream_t s) {
     const dim3 g = tile_grid((int64_t)((a.T + TILE_ROWS[k] - 1) / TILE_ROWS[k]) * a.splits, (a.d + TILE_COLS[k] - 1) / TILE_COLS[k]);
     if (k == ROWS_32) STRATA_LAUNCH((vocab_dh_kernel<32, 128, 1, 4, 4, PIECES>), g, dim3(256), 0, s, a);
+    else if (k == ROWS_64) STRATA_LAUNCH((vocab_dh_kernel<64, 128, 2, 2, 4, PIECES>), g, dim3(256), 0, s, a);
     else if (k == ROWS_128) STRATA_LAUNCH((vocab_dh_kernel<128, 256, 2, 4, 3, PIECES>), g, dim3(512), 0, s, a);
     else STRATA_LAUNCH((vocab_dh_kernel<256, 256, 2, 4, 2, PIECES>), g, dim3(512), 0, s, a);
     return hip_status(hipGetLastError());
 }
 
 template <int PIECES> strata_status launch_dw(const VocabArgs &a, hipStream_t s) {
-    const int64_t large = (int64_t)((a.pw + 255) / 256) * ((a.d + 255) / 256);
-    if (large >= 192) {
-        STRATA_LAUNCH((vocab_dw_kernel<256, 256, 2, 4, 3, 32, PIECES>), tile_grid((a.pw + 255) / 256, (a.d + 255) / 256), dim3(512),
-                      0, s, a);
-    } else {
-        STRATA_LAUNCH((vocab_dw_kernel<128, 128, 2, 2, 3, 32, PIECES>), tile_grid((a.pw + 127) / 128, (a.d + 127) / 128), dim3(256),
-                      0, s, a);
+    const auto grid = [&](int64_t n) { return tile_grid((a.pw + n - 1) / n, (a.d + n - 1) / n); };
+    switch (dw_tile(a.pw, a.d)) {
+        case SQUARE_64: STRATA_LAUNCH((vocab_dw_kernel<64, 64, 1, 2, 4, 64, PIECES>), grid(64), dim3(128), 0, s, a); break;
+        case SQUARE_128: STRATA_LAUNCH((vocab_dw_kernel<128, 128, 2, 2, 3, 32, PIECES>), grid(128), dim3(256), 0, s, a); break;
+        default: STRATA_LAUNCH((vocab_dw_kernel<256, 256, 2, 4, 3, 32, PIECES>), grid(256), dim3(512), 0, s, a);
     }
     return hip_status(hipGetLastError());
 }
@@ -303,8 +350,8 @@ strata_status strata_vocab_loss(const void *h, const void *W, const int32_t *tar
     a.part = (float2 *)(w + p.part);
     a.ldp = (int)up_to(T, 16);
     a.pw = V;
-    a.tiles = (V + TILE_COLS[row_tile(T)] - 1) / TILE_COLS[row_tile(T)];
-    if (row_tile(T) == ROWS_32) {   // packing and joining apart cost 5 tokens of 128000 x 2048 another 6 of 103 us
+    a.tiles = (V + TILE_COLS[p.tile] - 1) / TILE_COLS[p.tile];
+    if (p.tile == ROWS_32) {   // packing and joining apart cost 5 tokens of 128000 x 2048 another 6 of 103 us
         STRATA_LAUNCH((vocab_logits_kernel<32, 128, 1, 4, 4, 0, 1>), tile_grid(1, a.tiles), dim3(256), 0, s, a);
         VOCAB_TRY;
         STRATA_LAUNCH((vocab_join_kernel<1, 1>), dim3(T), dim3(1024), 0, s, a);
@@ -312,7 +359,7 @@ strata_status strata_vocab_loss(const void *h, const void *W, const int32_t *tar
     }
     STRATA_LAUNCH(vocab_pack_kernel<0>, dim3((T + a.rows_block - 1) / a.rows_block), dim3(256), 0, s, a);
     VOCAB_TRY;
-    const strata_status lt = launch_logits<0>(a, s);
+    const strata_status lt = launch_logits<0>(a, p.tile, s);
     if (lt != STRATA_OK) return lt;
     STRATA_LAUNCH((vocab_join_kernel<16, 0>), dim3((T + 15) / 16), dim3(1024), 0, s, a);
     return hip_status(hipGetLastError());
@@ -368,7 +415,7 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
     a.hi = (uint16_t *)(w + p.hi);
     a.lo = (uint16_t *)(w + p.lo);
     a.acc = (float *)(w + p.acc);
-    a.splits = p.splits;
+    a.splits = p.dh.splits;
     const bool h2 = dh && !a.dh_bf16, w2 = dW && !a.dw_bf16;   // outputs that take both pieces of dz
     STRATA_LAUNCH(vocab_pack_kernel<1>, dim3((T + a.rows_block - 1) / a.rows_block), dim3(256), 0, s, a);
     VOCAB_TRY;
@@ -377,10 +424,11 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
         a.pw = V - v0 < p.piece ? V - v0 : p.piece;
         a.ldv = (int)up_to(a.pw, 8);
         a.first = v0 == 0;
-        a.span = (int)up_to((a.pw + p.splits - 1) / p.splits, 64);
-        strata_status q = h2 || w2 ? launch_logits<2>(a, s) : launch_logits<1>(a, s);
+        a.span = (int)up_to((a.pw + a.splits - 1) / a.splits, 64);
+        const Tile k = logits_tile(T, a.pw);
+        strata_status q = h2 || w2 ? launch_logits<2>(a, k, s) : launch_logits<1>(a, k, s);
         if (q == STRATA_OK && dW) q = w2 ? launch_dw<2>(a, s) : launch_dw<1>(a, s);
-        if (q == STRATA_OK && dh) q = h2 ? launch_dh<2>(a, s) : launch_dh<1>(a, s);
+        if (q == STRATA_OK && dh) q = h2 ? launch_dh<2>(a, p.dh.tile, s) : launch_dh<1>(a, p.dh.tile, s);
         if (q != STRATA_OK) return q;
     }
     if (!dh) return STRATA_OK;
