@@ -151,16 +151,27 @@ template <typename G> hipError_t orth_begin_width(const OrthArgs &a, int steps, 
     return orth_begin<G, 1>(a, steps, s);
 }
 
-// Whether a matrix fits a block: its registers hold X, its LDS the fp16 copy, A and B.
-enum SmallShape { SMALL_NONE, SMALL_128, SMALL_64 };
+// Whether a matrix fits a block: its registers hold X, its LDS the fp16 copy, A and B.  The shorter side, and the
+// longer side that goes with it.
+enum SmallShape { SMALL_NONE, SMALL_32, SMALL_64, SMALL_64_LONG, SMALL_128, SMALL_128_LONG };
 SmallShape small_shape(int32_t N, int32_t K) {
     const int side = N < K ? N : K, longer = N < K ? K : N;
-    return side <= 64 && longer <= 512 ? (longer <= 256 && side > 32 ? SMALL_128 : SMALL_64) : side <= 128 && longer <= 256 ? SMALL_128 : SMALL_NONE;
+    if (side <= 32 && longer <= 1792 && longer > 256) return SMALL_32;
+    if (side <= 64 && longer <= 512) return SMALL_64;
+    if (side <= 64 && longer <= 1024) return SMALL_64_LONG;
+    if (side <= 128 && longer <= 256) return SMALL_128;
+    return side <= 128 && longer <= 384 ? SMALL_128_LONG : SMALL_NONE;
 }
 
 template <typename G> hipError_t orth_small(const OrthArgs &a, int steps, SmallShape k, hipStream_t s) {
-    if (k == SMALL_128) STRATA_LAUNCH((orth_small_kernel<G, 4, 8, 2, 4>), dim3(a.n), dim3(512), 0, s, a, steps);
-    else STRATA_LAUNCH((orth_small_kernel<G, 2, 16, 1, 8>), dim3(a.n), dim3(512), 0, s, a, steps);
+    const dim3 g(a.n), b(512);
+    switch (k) {
+        case SMALL_32: STRATA_LAUNCH((orth_small_kernel<G, 1, 1, 7>), g, b, 0, s, a, steps); break;
+        case SMALL_64: STRATA_LAUNCH((orth_small_kernel<G, 2, 2, 2>), g, b, 0, s, a, steps); break;
+        case SMALL_64_LONG: STRATA_LAUNCH((orth_small_kernel<G, 2, 2, 4>), g, b, 0, s, a, steps); break;
+        case SMALL_128: STRATA_LAUNCH((orth_small_kernel<G, 4, 2, 2>), g, b, 0, s, a, steps); break;
+        default: STRATA_LAUNCH((orth_small_kernel<G, 4, 2, 3>), g, b, 0, s, a, steps);
+    }
     return hipGetLastError();
 }
 

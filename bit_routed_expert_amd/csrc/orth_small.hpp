@@ -1,13 +1,17 @@
 // Orthogonalised updates of small matrices: all steps of a matrix in one block.
 //
-// The shorter side (of up to 32 RT) lies along the rows of X.  X stays in the
+// The shorter side (up to 32 RT) lies along the rows of X.  X stays in the
 // registers in fp32, in the layout of the products' sums, so a X is where the
 // sum of B X starts from; its fp16 copy, A and B lie in LDS.  X is read both
 // along (X X^T) and, by the transposing reads, across (B X): its 16-byte
 // chunks are permuted by the row so that 8 rows' equal chunks and 4 rows'
-// equal 64-byte pieces lie in different banks.
+// equal 64-byte pieces lie in different banks.  Where A has fewer subtiles than
+// the block has waves, its contraction is dealt to them and their sums meet in
+// LDS.
 //
-// 16 matrices of 128 x 256, 5 steps: 3 launches of tiles a step take 87 us.
+// 5 steps, against 3 launches of tiles a step: 16 matrices of 128 x 256 34 and 87
+// us, 18 of 22 x 556 33 and 66, 6 of 73 x 274 54 and 76, 7 of 18 x 1225 58 and
+// 81.  Bound by LDS reads and the turns between its four phases a step.
 #pragma once
 #include "orth_impl.hpp"
 
@@ -16,8 +20,8 @@ namespace strata {
 // Permutation of the chunks of row r: its low three bits differ over 8 rows, bits 2 and 3 over 4.
 __device__ __forceinline__ int small_swz(int r) { return (r & 1) << 2 | (r & 2) | (r >> 2 & 1) | (r & 2) << 2; }
 
-template <int COLS> struct SmallRows {   // LDS rows of COLS fp16 values
-    static constexpr int MASK = COLS >= 128 ? 15 : 7;
+template <int COLS> struct SmallRows {   // LDS rows of COLS fp16 values, a multiple of 32
+    static constexpr int MASK = COLS % 128 == 0 ? 15 : COLS % 64 == 0 ? 7 : 3;
     __device__ __forceinline__ static int at(int r, int chunk) { return r * COLS * 2 + 16 * (chunk ^ (small_swz(r) & MASK)); }
     // 8 values of row r from 16 kk + 8 (lane / 32) on
     __device__ __forceinline__ static f16x8_t along(const uint8_t *t, int r, int kk) {
@@ -42,26 +46,31 @@ template <int COLS> struct SmallRows {   // LDS rows of COLS fp16 values
     }
 };
 
-// RT x CT subtiles of 32 x 32 hold X, 8 waves of 2 x 2 of them (WM x WN waves).
-template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds__(512) void orth_small_kernel(OrthArgs a, int steps) {
-    static_assert(WM * WN == 8 && 2 * WM == RT && 2 * WN == CT, "2 x 2 subtiles a wave");
+// RT (1, 2 or 4) rows of subtiles of 32 x 32 hold X, 8 waves of MT x NT of them, WM = RT / MT rows of waves.
+template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) void orth_small_kernel(OrthArgs a, int steps) {
+    constexpr int WM = RT / MT, WN = 8 / WM, CT = WN * NT;
     constexpr int PA = RT * RT / 8 > 0 ? RT * RT / 8 : 1;   // subtiles of A a wave
+    constexpr int KS = RT * RT < 8 ? 8 / (RT * RT) : 1;     // waves that share a subtile's contraction
     typedef SmallRows<CT * 32> XR;
     typedef SmallRows<RT * 32> AR;
-    __shared__ __attribute__((aligned(128))) uint8_t Xs[RT * CT * 2048], As[RT * RT * 2048], Bs[RT * RT * 2048];
+    // B lies over the waves' sums of A, or, with none, over A
+    constexpr int A_BYTES = RT * RT * 2048, SUMS = KS > 1 ? (8 - RT * RT) * 4096 : 0;
+    __shared__ __attribute__((aligned(128))) uint8_t Xs[RT * CT * 2048], As[A_BYTES], more[SUMS ? SUMS : 128];
+    static_assert(sizeof(Xs) + sizeof(As) + sizeof(more) + 128 <= 160 * 1024 && (!SUMS || A_BYTES <= SUMS), "fits the LDS");
     __shared__ double sums[8];
+    uint8_t *const Bs = SUMS ? more : As;
     const int th = threadIdx.x, lane = th & 63, l = lane & 31, h = lane >> 5, w = __builtin_amdgcn_readfirstlane(th >> 6);
-    const int m0 = (w / WN) * 64, n0 = (w % WN) * 64;
+    const int m0 = (w / WN) * 32 * MT, n0 = (w % WN) * 32 * NT;
     const bool tall = a.N > a.K;
     const int L = tall ? a.N : a.K;   // the longer side
     const G *g = (const G *)a.G + (int64_t)blockIdx.x * a.N * a.K;
     const bool live = m0 < a.side && n0 < L;   // this wave has values of X
-    f32x16_t X[2][2];
+    f32x16_t X[MT][NT];
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int m = m0 + 32 * i + l, c = n0 + 32 * j + 8 * q + 4 * h;
@@ -97,22 +106,23 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
     for (int q = 0; q < 8; ++q) s += sums[q];
     const double r = 1.0 / (sqrt(s) + (double)a.eps) * (double)a.size;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) X[i][j][v] = (float)((double)X[i][j][v] * r);
     const float unsize = 1.f / (a.size * a.size);
-    const int kl = (L + 63) / 64, ks = (a.side + 63) / 64;   // 64s of either contraction
-    // subtiles of A: row ar, columns ac + p
-    const int ar = RT == 4 ? w >> 1 : (w >> 1) & 1, ac = RT == 4 ? 2 * (w & 1) : w & 1;
-    const bool squares = (RT == 4 || w < 4) && 32 * ar < a.side && 32 * ac < a.side;
+    const int kl = (L + 31) / 32, ks = (a.side + 31) / 32;   // 32s of either contraction
+    // subtiles of A: row ar, columns ac + p; the kp-th of KS shares of the contraction
+    const int kp = RT == 4 ? 0 : RT == 2 ? w >> 2 : w;
+    const int ar = RT == 4 ? w >> 1 : RT == 2 ? (w >> 1) & 1 : 0, ac = RT == 4 ? 2 * (w & 1) : RT == 2 ? w & 1 : 0;
+    const bool squares = 32 * ar < a.side && 32 * ac < a.side;
     for (int step = 0; step < steps; ++step) {
         if (step) __syncthreads();   // everyone has read the last X
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) XR::put(Xs, m0 + 32 * i + l, n0 + 32 * j, X[i][j]);
+            for (int j = 0; j < NT; ++j) XR::put(Xs, m0 + 32 * i + l, n0 + 32 * j, X[i][j]);
         __syncthreads();
         f32x16_t A[PA];
 #pragma unroll
@@ -120,22 +130,38 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
 #pragma unroll
             for (int v = 0; v < 16; ++v) A[p][v] = 0.f;
         if (squares) {
-            for (int k0 = 0; k0 < kl; ++k0)
+            for (int k0 = kp; k0 < kl; k0 += KS)
 #pragma unroll
-                for (int kk = 4 * k0, u = 0; u < 4; ++u, ++kk) {
+                for (int kk = 2 * k0, u = 0; u < 2; ++u, ++kk) {
                     const f16x8_t x = XR::along(Xs, 32 * ar + l, kk);
 #pragma unroll
                     for (int p = 0; p < PA; ++p) A[p] = mfma(XR::along(Xs, 32 * (ac + p) + l, kk), x, A[p]);
                 }
         }
+        if constexpr (KS > 1) {   // the shares' sums, in order
+            float *const q = (float *)more;   // [wave behind the first shares'][value][lane]
+            constexpr int T = RT * RT;
+            if (kp) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) q[((w - T) * 16 + v) * 64 + lane] = A[0][v];
+            }
+            __syncthreads();
+            if (!kp) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+#pragma unroll
+                    for (int k = 1; k < KS; ++k) A[0][v] += q[(((k - 1) * T + w) * 16 + v) * 64 + lane];
+            }
+        }
+        const bool first = KS == 1 || kp == 0;   // of the waves that hold the same subtile
 #pragma unroll
         for (int p = 0; p < PA; ++p) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) A[p][v] *= unsize;
-            if (RT == 4 || w < 4) AR::put(As, 32 * ar + l, 32 * (ac + p), A[p]);
+            if (first) AR::put(As, 32 * ar + l, 32 * (ac + p), A[p]);
         }
         __syncthreads();
-        if (squares) {
+        if (squares && first) {
             f32x16_t S[PA];
 #pragma unroll
             for (int p = 0; p < PA; ++p)
@@ -143,7 +169,7 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
                 for (int v = 0; v < 16; ++v) S[p][v] = 0.f;
             for (int k0 = 0; k0 < ks; ++k0)
 #pragma unroll
-                for (int kk = 4 * k0, u = 0; u < 4; ++u, ++kk) {
+                for (int kk = 2 * k0, u = 0; u < 2; ++u, ++kk) {
                     const f16x8_t x = AR::along(As, 32 * ar + l, kk);
 #pragma unroll
                     for (int p = 0; p < PA; ++p) S[p] = mfma(AR::along(As, 32 * (ac + p) + l, kk), x, S[p]);
@@ -153,38 +179,39 @@ template <typename G, int RT, int CT, int WM, int WN> __global__ __launch_bounds
 #pragma unroll
                 for (int v = 0; v < 16; ++v) A[p][v] = fmaf(a.c, S[p][v], a.b * A[p][v]);
         }
+        if constexpr (!SUMS) __syncthreads();   // B over A
 #pragma unroll
         for (int p = 0; p < PA; ++p)
-            if (RT == 4 || w < 4) AR::put(Bs, 32 * ar + l, 32 * (ac + p), A[p]);
+            if (first) AR::put(Bs, 32 * ar + l, 32 * (ac + p), A[p]);
         __syncthreads();
         if (live) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int v = 0; v < 16; ++v) X[i][j][v] *= a.a;
             for (int k0 = 0; k0 < ks; ++k0)
 #pragma unroll
-                for (int kk = 4 * k0, u = 0; u < 4; ++u, ++kk) {
-                    f16x8_t b[2], x[2];
+                for (int kk = 2 * k0, u = 0; u < 2; ++u, ++kk) {
+                    f16x8_t b[MT];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) b[i] = AR::along(Bs, m0 + 32 * i + l, kk);
+                    for (int i = 0; i < MT; ++i) b[i] = AR::along(Bs, m0 + 32 * i + l, kk);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) x[j] = XR::across(Xs, n0 + 32 * j, kk);
+                    for (int j = 0; j < NT; ++j) {
+                        const f16x8_t x = XR::across(Xs, n0 + 32 * j, kk);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) X[i][j] = mfma(x[j], b[i], X[i][j]);
+                        for (int i = 0; i < MT; ++i) X[i][j] = mfma(x, b[i], X[i][j]);
+                    }
                 }
         }
     }
     const float scale = a.scale / a.size;
     uint16_t *out = a.out + (int64_t)blockIdx.x * a.N * a.K;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int m = m0 + 32 * i + l, c = n0 + 32 * j + 8 * q + 4 * h;

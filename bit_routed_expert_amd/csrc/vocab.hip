@@ -147,6 +147,7 @@ strata_status check_vocab(int32_t T, int32_t V, int32_t d) {
     if (T < 0) return STRATA_EINVAL;
     if (V < 1 || V > VOCAB_V || d < 8 || d % 8 || d > VOCAB_D || T > VOCAB_T || (int64_t)T * d > ((int64_t)1 << 33))
         return STRATA_EUNSUPPORTED;
+    if ((int64_t)T * V > ((int64_t)1 << 38)) return STRATA_EUNSUPPORTED;   // a grid of fewer than 2^32 threads
     return STRATA_OK;
 }
 

@@ -89,7 +89,7 @@ enum { STRATA_ACCUMULATE = 1u }; /* flags: the gradient is added to what the mat
 size_t strata_embed_backward_workspace_bytes(int32_t T, int32_t V, int32_t d);
 
 /* dW[v] = scale * sum of dout[t] over the t with ids[t] = v: the tokens are sorted by id and each row's are
- * summed in an order that T alone decides.
+ * summed in an order that the ids alone decide.
  *   dout [dev] [T][d] of odtype, dW [dev] [V][d] of wdtype.
  *   flags: 0: every row is written, one without tokens with zeros (T = 0 writes all zeros);
  *          STRATA_ACCUMULATE: rows with tokens get dW + the sum (added in fp32), others are left as they were.
@@ -108,7 +108,7 @@ strata_status strata_embed_backward(const void *dout, strata_xdtype odtype, cons
  * whose target is outside 0..V-1 (a prompt's, padding) has loss 0 and lse 0,
  * no gradient, and costs no products; what its h, dloss and dlse hold is not
  * used.  Limits: d % 8 == 0, 8 <= d <= 16384, 1 <= V <= 2^20, T <= 2^20,
- * T*d <= 2^33, else EUNSUPPORTED.
+ * T*d <= 2^33, T*V <= 2^38, else EUNSUPPORTED.
  */
 
 /* Bytes of workspace the calls need; 0 for arguments they refuse. */
@@ -142,7 +142,8 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
  * (the same polynomial from the right where N > K).  Operands of the products
  * are fp16 (11 bits), X itself is kept in two fp16 pieces (22 bits), so that
  * directions that G lacks are not made of its roundings; sums are fp32.
- * A matrix of zeros gives zeros; infinities and NaN stay in their matrix.
+ * A matrix of zeros gives zeros; infinities and NaN stay in their matrix, and
+ * coefficients that take X or b A + c A^2 out of fp16's range make infinities.
  */
 
 /* Bytes of workspace the call needs; 0 for arguments it refuses. */

@@ -420,7 +420,10 @@ def test_vocab_nan_stays_in_its_row():
 
 COEF = (3.4445, -4.7750, 2.0315)
 ORTH = [(1, 1, 1), (2, 1, 9), (1, 9, 1), (3, 8, 8), (2, 17, 40), (2, 63, 65), (1, 64, 130), (2, 130, 64), (3, 100, 300),
-        (2, 300, 100), (1, 257, 513), (1, 520, 264), (2, 136, 1000), (40, 33, 70), (1, 129, 127)]
+        (2, 300, 100), (1, 257, 513), (1, 520, 264), (2, 136, 1000), (40, 33, 70), (1, 129, 127),
+        # a matrix to a block: its longest and their neighbours
+        (2, 32, 1792), (1, 1791, 31), (2, 31, 257), (1, 32, 1793), (2, 64, 1024), (1, 1023, 61), (1, 33, 513), (1, 65, 1024),
+        (2, 128, 384), (1, 383, 97), (1, 128, 385), (3, 128, 256), (2, 64, 512), (1, 7, 300)]
 
 
 def size_of(N, K):
