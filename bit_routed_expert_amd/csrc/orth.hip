@@ -98,17 +98,18 @@ struct OrthPlan {
     size_t factor, hi, next, lo, A, B, bytes;
 };
 
-// Tiles of a step by how many of 128 square there are (us of a step): below 144,
-// 64 x 128 (2 of 512 x 2048, 128 tiles: 10.0 against 13.2; 1 of 1000 x 1000: 11.4
-// against 14.5); up to 256, 128 square with four buffers (1 of 2048 x 2048: 27.6
-// against 33.6 and, with two buffers, 31.7), up to 2048 with two, two blocks to a CU
-// (8 of 2048 x 768, 768 tiles: 40.6 against 46.8; 32 of 512 x 512: 24.0 against
-// 29.6); then 128 x 256 (16 of 1536 x 2048: 244 against 251; 256 square 249).
+// Tiles of a step by how many of 128 square there are: below 144, 64 x 128 (a
+// step of 2 of 512 x 2048, 128 tiles: 10.0 us against 13.2; of 1 of 1000 x 1000:
+// 11.4 against 14.5); up to 256, 128 square with four buffers (1 of 2048 x 2048:
+// 27.6 against 33.6); below 1024 with two, two blocks of 8 waves to a CU (whole
+// passes of 8 of 2048 x 768, 768 tiles: 306 us, 256 square 319; 32 of 512 x 512:
+// 239 and 274); then 256 square (4 of 2048 x 2048: 940, 128 square 980; 16 of
+// 1536 x 2048: 1892 and 2055, 128 x 256 1956).
 enum StepTile { STEP_64, STEP_128, STEP_128_TWO, STEP_256 };
-constexpr int STEP_ROWS[] = {64, 128, 128, 128}, STEP_COLS[] = {128, 128, 128, 256};
+constexpr int STEP_ROWS[] = {64, 128, 128, 256}, STEP_COLS[] = {128, 128, 128, 256};
 StepTile step_tile(int32_t n, int32_t N, int32_t K) {
     const int64_t tiles = (int64_t)n * ((N + 127) / 128) * ((K + 127) / 128);
-    return tiles < 144 ? STEP_64 : tiles <= 256 ? STEP_128 : tiles <= 2048 ? STEP_128_TWO : STEP_256;
+    return tiles < 144 ? STEP_64 : tiles <= 256 ? STEP_128 : tiles < 1024 ? STEP_128_TWO : STEP_256;
 }
 
 OrthPlan orth_plan(int32_t n, int32_t N, int32_t K) {
@@ -210,8 +211,8 @@ template <int TALL> hipError_t steps_of(const OrthArgs &a, hipStream_t s) {
     switch (step_tile(a.n, a.N, a.K)) {
         case STEP_64: step<64, 128, 2, 2, 4, TALL>(a, s); break;
         case STEP_128: step<128, 128, 2, 2, 4, TALL>(a, s); break;
-        case STEP_128_TWO: step<128, 128, 2, 2, 2, TALL>(a, s); break;
-        default: step<128, 256, 2, 4, 3, TALL>(a, s);
+        case STEP_128_TWO: step<128, 128, 2, 4, 2, TALL>(a, s); break;
+        default: step<256, 256, 2, 4, 2, TALL>(a, s);
     }
     return hipGetLastError();
 }

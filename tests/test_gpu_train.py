@@ -467,7 +467,7 @@ def test_orthogonalise(n, N, K, dt):
 
 
 @pytest.mark.parametrize("n,N,K", [(200, 60, 72), (200, 72, 60), (70, 200, 264), (70, 264, 200), (70, 500, 520), (66, 520, 500),
-                                   (16, 1030, 520), (16, 520, 1030), (8, 1100, 1290), (8, 1290, 1100)])
+                                   (16, 1030, 520), (16, 520, 1030), (8, 1100, 1290), (8, 1290, 1100), (20, 1000, 1010), (20, 1010, 1000)])
 def test_orthogonalise_every_tile(n, N, K):
     """Enough matrices for the larger tiles: one step elementwise, in 64 bits on the GPU."""
     print(f"case orth tiles n={n} N={N} K={K}", flush=True)
