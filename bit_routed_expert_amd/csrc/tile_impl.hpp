@@ -265,7 +265,7 @@ __device__ __forceinline__ void contract(const OA &A, const OB &B, uint8_t *a0, 
 // columns outside the tile fall outside the buffer resource.
 template <int MT, int NT2>
 __device__ __forceinline__ void store_tile(void *C, int c_bf16, int m0, int M, int n0, int Nn,
-                                           const f32x16_t (&acc)[MT][NT2]) {
+                                           const f32x16_t (&acc)[MT][NT2], float by = 1.f) {
     const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
     const uint32_t esz = c_bf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(C, 0, (int)((uint32_t)M * (uint32_t)Nn * esz), 0x00020000);
@@ -274,7 +274,9 @@ __device__ __forceinline__ void store_tile(void *C, int c_bf16, int m0, int M, i
         const uint32_t row = (uint32_t)(m0 + 32 * i + l) * (uint32_t)Nn;
 #pragma unroll
         for (int j = 0; j < NT2; ++j) {
-            const f32x16_t &v = acc[i][j];
+            f32x16_t v = acc[i][j];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] *= by;
             if (c_bf16) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {

@@ -12,7 +12,11 @@
 // dW = dz^T h of the piece and dh += dz W, its contraction cut into spans
 // where the tiles of dh are fewer than the CUs.  Where an output is fp32, dz
 // is kept in two bf16 pieces (16 bits) and its product run over both: the
-// rounding of one piece, 2^-9, is more than such an output shows.
+// rounding of one piece, 2^-8 at most, is more than such an output shows.  dz is kept
+// over a unit, the first dloss without its exponent: of a mean, where all are the
+// same 1/n, the targets' entries, the largest of each row, are then a power of two
+// less a small number, which bf16 holds, and not 1/n, whose rounding would be the
+// same in every row (up to 2^-8 of both gradients).
 #include <cmath>
 
 #include "vocab_impl.hpp"
@@ -36,6 +40,19 @@ template <int GRAD> __global__ __launch_bounds__(256) void vocab_pack_kernel(Voc
     if (lane == 0) cnt[w] = before;
     __syncthreads();
     int base = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+    if (GRAD && blockIdx.x == 0) {   // the unit of dz: the first weight's that is not zero, without its exponent
+        __shared__ int first[4];
+        int f = a.T;
+        for (int t0 = 0; f == a.T && t0 < a.T; t0 += 256) {
+            const int t = t0 + th;
+            const uint64_t m = __ballot(t < a.T && has(t) && a.dloss[t] != 0.f);
+            if (lane == 0) first[w] = m ? t0 + 64 * w + __builtin_ctzll(m) : a.T;
+            __syncthreads();
+            f = min(min(first[0], first[1]), min(first[2], first[3]));
+            __syncthreads();
+        }
+        if (th == 0) *a.unit = f < a.T ? __uint_as_float((__float_as_uint(a.dloss[f]) & 0x7fffffu) | 0x3f800000u) : 1.f;
+    }
     const int nv = a.d / 8;
     for (int c = t0; c < t1; c += 256) {
         __syncthreads();
@@ -129,7 +146,7 @@ __global__ __launch_bounds__(256) void vocab_dh_out_kernel(VocabArgs a) {
         const int row = (int)(i / nq), c = (int)(i - (int64_t)row * nq) * 4;
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
         for (int s = 0; s < a.splits; ++s) v += *(const f32x4_t *)(a.acc + ((int64_t)s * a.T + row) * a.d + c);
-        const float q[4] = {v[0], v[1], v[2], v[3]};
+        const float unit = *a.unit, q[4] = {v[0] * unit, v[1] * unit, v[2] * unit, v[3] * unit};
         const int64_t at = (int64_t)a.map[row] * a.d + c;
         if (a.dh_bf16) store_values<4>((uint16_t *)a.dh, at, q);
         else store_values<4>((float *)a.dh, at, q);
@@ -258,6 +275,7 @@ bool bad_vector(const void *p) { return !p || ((uintptr_t)p & 3u); }
 
 void vocab_common(VocabArgs &a, const VocabPlan &p, char *w) {
     a.n = (int32_t *)w;
+    a.unit = (float *)w + 1;
     a.map = (int32_t *)(w + p.map);
     a.tc = (int32_t *)(w + p.tc);
     a.hc = (uint16_t *)(w + p.hc);

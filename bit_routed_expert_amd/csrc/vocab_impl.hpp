@@ -13,6 +13,7 @@ struct VocabArgs {
     int T, V, d, dh_bf16, dw_bf16, add;
     // workspace: the rows with a target, packed
     int32_t *n;                     // how many
+    float *unit;                    // gradient: dz is kept as a multiple of it
     int32_t *map, *tc;              // their tokens and targets
     uint16_t *hc;                   // their rows
     float *zt;                      // forward: the target's logit
@@ -47,9 +48,9 @@ __device__ __forceinline__ void each_quad(int m0, int n0, f32x16_t (&acc)[MT][NT
     }
 }
 
-// acc += what the tile's C holds (rows below M, columns below Nn, Nn a multiple of 4).
+// acc * by += what the tile's C holds (rows below M, columns below Nn, Nn a multiple of 4).
 template <int MT, int NT2>
-__device__ __forceinline__ void add_tile(const void *C, int c_bf16, int m0, int M, int n0, int Nn, f32x16_t (&acc)[MT][NT2]) {
+__device__ __forceinline__ void add_tile(const void *C, int c_bf16, int m0, int M, int n0, int Nn, f32x16_t (&acc)[MT][NT2], float by = 1.f) {
     const uint32_t esz = c_bf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<void *>(C), 0, __builtin_amdgcn_readfirstlane((int)((uint32_t)M * (uint32_t)Nn * esz)), 0x00020000);
@@ -57,12 +58,10 @@ __device__ __forceinline__ void add_tile(const void *C, int c_bf16, int m0, int 
         const uint32_t at = n < Nn ? ((uint32_t)m * (uint32_t)Nn + n) * esz : 0xFFFFFFF0u;
         if (c_bf16) {
             const u32x2_t w = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
-            v[0] += __uint_as_float(w[0] << 16);
-            v[1] += __uint_as_float(w[0] & 0xFFFF0000u);
-            v[2] += __uint_as_float(w[1] << 16);
-            v[3] += __uint_as_float(w[1] & 0xFFFF0000u);
+            v = v * by + f32x4_t{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+                                 __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
         } else {
-            v += __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+            v = v * by + __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
         }
     });
 }
@@ -200,14 +199,15 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
         }
     } else {
         if (!active) return;
+        const float unit = *a.unit;
         float lse[MT], up[MT], un[MT];
         int want[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int row = min(row0 + m0 + 32 * i + l, n - 1);
             lse[i] = a.lc[row];
-            up[i] = a.gc[row];
-            un[i] = a.dc[row];
+            up[i] = a.gc[row] / unit;
+            un[i] = a.dc[row] / unit;
             want[i] = a.tc[row] - a.v0;
         }
         const bool ragged = c0 + n0 + 32 * NT2 > a.pw;   // columns behind the last one
@@ -291,7 +291,9 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_dw_kernel(VocabArgs a) {
     if (!active) return;
     const int M = min(a.pw - r0, BM);
     char *C0 = (char *)a.dW + ((int64_t)a.v0 + r0) * a.d * (a.dw_bf16 ? 2 : 4);
-    if (a.add) add_tile<MT, NT2>(C0, a.dw_bf16, m0, M, k0 + n0, a.d, acc);
+    const float unit = *a.unit;
+    if (!a.add) return store_tile<MT, NT2>(C0, a.dw_bf16, m0, M, k0 + n0, a.d, acc, unit);
+    add_tile<MT, NT2>(C0, a.dw_bf16, m0, M, k0 + n0, a.d, acc, unit);
     store_tile<MT, NT2>(C0, a.dw_bf16, m0, M, k0 + n0, a.d, acc);
 }
 

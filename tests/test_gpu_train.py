@@ -389,6 +389,29 @@ def test_vocab_gradients_apart():
             assert same((dh, dW), both)
 
 
+@pytest.mark.parametrize("weighted", [False, True])
+def test_vocab_gradients_of_a_mean_have_no_bias(weighted):
+    """dloss = 1 / 510 in every row (1 + 2^-8 of a power of two: half a step of bf16): rounded as such, the targets'
+    entries of dz, and with them both gradients, would be 2^-8 off along themselves.  As multiples of it they are 1 less
+    a probability of about 2^-12, rounded at most to 1; the output's rounding averages over T d = 65280 values and V d."""
+    T, V, d = 510, 4096, 128
+    h, W = rand(T, d, seed=1, dtype=BF).cuda(), rand(V, d, seed=2, dtype=BF, scale=0.01).cuda()
+    t = torch.randint(0, V, (T,), generator=gen(3), dtype=torch.int32).cuda()
+    dloss = torch.full((T,), 1 / 510, device="cuda")
+    if weighted:
+        dloss[:300] = 0          # rows without weight ahead of it
+    _, lse = run_vocab(h, W, t, T, V, d)
+    dh, dW = torch.full((T, d), 7.0, dtype=BF, device="cuda"), torch.full((V, d), 7.0, dtype=BF, device="cuda")
+    nb = brx.vocab_loss_backward_workspace_bytes(T, V, d)
+    brx.vocab_loss_backward(h, W, t, T, V, d, lse, dloss, ws_of(nb), nb, dh=dh, dW=dW)
+    p = torch.softmax(h.double() @ W.double().t(), 1)
+    p[torch.arange(T), t.long()] -= 1
+    dz = p * dloss.double()[:, None]
+    for got, ref in ((dh, dz @ W.double()), (dW, dz.t().contiguous() @ h.double())):
+        along = float(((got.double() - ref) * ref).sum() / ref.square().sum())
+        assert abs(along) <= 2.0 ** -10, along
+
+
 def test_vocab_loss_of_sharp_and_far_logits():
     """Logits of hundreds: the maximum is taken out, the loss of a certain token is small or exact."""
     for T in (9, 200, 600):
