@@ -9,8 +9,14 @@
 // the block has waves, its contraction is dealt to them and their sums meet in
 // LDS.
 //
-// 5 steps, against 3 launches of tiles a step: 16 matrices of 128 x 256 34 and 87
-// us, 18 of 22 x 556 33 and 66, 6 of 73 x 274 54 and 76, 7 of 18 x 1225 58 and
+// The diagonals of A and B, near which most of their norms lie, stay in fp32:
+// A = D + A', A^2 = D^2 + D A' + A' D + A' A', B X = (diagonal) X + B' X.  With
+// them rounded to fp16, b A and a X + B X, which nearly cancel, left matrices of
+// equal singular values up to 7e-3 off, all in one direction.  16 of 128 x 256
+// take 37.1 us in place of 34.5 for it, the other forms no more.
+//
+// 5 steps, against 3 launches of tiles a step: 16 matrices of 128 x 256 37 and 87
+// us, 18 of 22 x 556 33 and 66, 6 of 73 x 274 53 and 76, 7 of 18 x 1225 58 and
 // 81.  Bound by LDS reads and the turns between its four phases a step.
 #pragma once
 #include "orth_impl.hpp"
@@ -56,8 +62,9 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
     // B lies over the waves' sums of A, or, with none, over A
     constexpr int A_BYTES = RT * RT * 2048, SUMS = KS > 1 ? (8 - RT * RT) * 4096 : 0;
     __shared__ __attribute__((aligned(128))) uint8_t Xs[RT * CT * 2048], As[A_BYTES], more[SUMS ? SUMS : 128];
-    static_assert(sizeof(Xs) + sizeof(As) + sizeof(more) + 128 <= 160 * 1024 && (!SUMS || A_BYTES <= SUMS), "fits the LDS");
+    static_assert(sizeof(Xs) + sizeof(As) + sizeof(more) + 256 * RT + 128 <= 160 * 1024 && (!SUMS || A_BYTES <= SUMS), "fits the LDS");
     __shared__ double sums[8];
+    __shared__ __attribute__((aligned(16))) float dA[32 * RT], dB[32 * RT];   // the diagonals
     uint8_t *const Bs = SUMS ? more : As;
     const int th = threadIdx.x, lane = th & 63, l = lane & 31, h = lane >> 5, w = __builtin_amdgcn_readfirstlane(th >> 6);
     const int m0 = (w / WN) * 32 * MT, n0 = (w % WN) * 32 * NT;
@@ -100,6 +107,7 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
 #pragma unroll
     for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
     if (lane == 0) sums[w] = s;
+    if (th < 32 * RT) dB[th] = 0.f;   // also of rows without a subtile of A
     __syncthreads();
     s = 0.0;
 #pragma unroll
@@ -116,6 +124,16 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
     // subtiles of A: row ar, columns ac + p; the kp-th of KS shares of the contraction
     const int kp = RT == 4 ? 0 : RT == 2 ? w >> 2 : w;
     const int ar = RT == 4 ? w >> 1 : RT == 2 ? (w >> 1) & 1 : 0, ac = RT == 4 ? 2 * (w & 1) : RT == 2 ? w & 1 : 0;
+    const int on = (l >> 2 & 1) == h ? 4 * (l >> 3) + (l & 3) : -1;   // which of the 16 values lies on a diagonal, if one does
+    const auto take = [&](f32x16_t &m) {   // it, left as zero
+        float d = 0.f;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            d = v == on ? m[v] : d;
+            m[v] = v == on ? 0.f : m[v];
+        }
+        return d;
+    };
     const bool squares = 32 * ar < a.side && 32 * ac < a.side;
     for (int step = 0; step < steps; ++step) {
         if (step) __syncthreads();   // everyone has read the last X
@@ -158,7 +176,13 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
         for (int p = 0; p < PA; ++p) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) A[p][v] *= unsize;
-            if (first) AR::put(As, 32 * ar + l, 32 * (ac + p), A[p]);
+            if (first) {
+                if (ar == ac + p) {
+                    const float d = take(A[p]);
+                    if (on >= 0) dA[32 * ar + l] = d;
+                }
+                AR::put(As, 32 * ar + l, 32 * (ac + p), A[p]);
+            }
         }
         __syncthreads();
         if (squares && first) {
@@ -174,10 +198,23 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
 #pragma unroll
                     for (int p = 0; p < PA; ++p) S[p] = mfma(AR::along(As, 32 * (ac + p) + l, kk), x, S[p]);
                 }
+            const float di = dA[32 * ar + l];
 #pragma unroll
-            for (int p = 0; p < PA; ++p)
+            for (int p = 0; p < PA; ++p) {
+                if (ar == ac + p) {
+                    const float d = take(S[p]);
+                    if (on >= 0) dB[32 * ar + l] = fmaf(a.c, fmaf(di, di, d), a.b * di);
+                }
 #pragma unroll
-                for (int v = 0; v < 16; ++v) A[p][v] = fmaf(a.c, S[p][v], a.b * A[p][v]);
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4_t dj = *(const f32x4_t *)&dA[32 * (ac + p) + 8 * q + 4 * h];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int v = 4 * q + k;
+                        A[p][v] = fmaf(a.c, fmaf(di + dj[k], A[p][v], S[p][v]), a.b * A[p][v]);
+                    }
+                }
+            }
         }
         if constexpr (!SUMS) __syncthreads();   // B over A
 #pragma unroll
@@ -186,11 +223,13 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
         __syncthreads();
         if (live) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i) {
+                const float d = a.a + dB[m0 + 32 * i + l];
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) X[i][j][v] *= a.a;
+                    for (int v = 0; v < 16; ++v) X[i][j][v] *= d;
+            }
             for (int k0 = 0; k0 < ks; ++k0)
 #pragma unroll
                 for (int kk = 2 * k0, u = 0; u < 2; ++u, ++kk) {

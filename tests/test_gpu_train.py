@@ -565,6 +565,24 @@ def test_orthogonalise_in_place():
             assert torch.equal(own, want)
 
 
+@pytest.mark.parametrize("n,N,K", [(3, 4, 300), (2, 7, 1225), (3, 18, 556), (3, 22, 556), (2, 33, 90), (3, 48, 256), (2, 200, 64),
+                                   (2, 73, 274), (2, 100, 200), (2, 127, 256)])
+def test_orthogonalise_of_equal_singular_values(n, N, K):
+    """All diagonals of X X^T are the same number, whose rounding to 11 bits would not average out: after 5 steps up to
+    7e-3 of the result, along itself.  In fp32 what is left averages over the values of a row: X's 11 bits in X X^T are
+    2^-11 / sqrt(3) of each of K / 2 products or more off, 5e-5 together for K = 64, and a step makes at most
+    (|b| + 2 |c|) 2 = 18 times that of a result of 0.7 or more if it keeps it.  The output's rounding, at most 2^-8,
+    averages over N K values, 1200 or more.  2^-10 lies between."""
+    print(f"case orth equal n={n} N={N} K={K}", flush=True)
+    side, long = min(N, K), max(N, K)
+    q = torch.linalg.qr(rand(n, long, side, seed=6).double()).Q * 3
+    G = (q if N > K else q.transpose(1, 2)).float().contiguous()
+    got = run_orth(G.cuda(), 5, COEF, 1.0, 1e-7).cpu().double()
+    ref = R.orthogonalise(G.double(), 5, tuple(f32(v) for v in COEF), 1.0, f32(1e-7))
+    along = ((got - ref) * ref).sum((1, 2)) / ref.square().sum((1, 2))
+    assert float(along.abs().max()) <= 2.0 ** -10, along
+
+
 # --------------------------------------------- graphs, streams, repetition
 
 def every_call(seed):
