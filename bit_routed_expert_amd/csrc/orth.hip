@@ -95,7 +95,7 @@ strata_status check_orth(int32_t n, int32_t N, int32_t K) {
 
 struct OrthPlan {
     int side, ldx, lds;
-    size_t factor, hi, next, lo, A, B, bytes;
+    size_t factor, hi, next, lo, A, B, dA, dB, bytes;
 };
 
 // Tiles of a step by how many of 128 square there are: below 144, 64 x 128 (a
@@ -132,6 +132,8 @@ OrthPlan orth_plan(int32_t n, int32_t N, int32_t K) {
     p.lo = take(n * rows * ((K + STEP_COLS[t] - 1) / STEP_COLS[t] * STEP_COLS[t]));   // whole tiles
     p.A = take(s);
     p.B = take(s);
+    p.dA = take((size_t)n * p.lds * 2);
+    p.dB = take((size_t)n * p.lds * 2);
     p.bytes = at;
     return p;
 }
@@ -258,6 +260,8 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     a.lo = (uint16_t *)(w + p.lo);
     a.A = (uint16_t *)(w + p.A);
     a.B = (uint16_t *)(w + p.B);
+    a.dA = (float *)(w + p.dA);
+    a.dB = (float *)(w + p.dB);
     a.n = n;
     a.N = N;
     a.K = K;

@@ -17,6 +17,7 @@ struct OrthArgs {
     float *factor;              // [n] X_0 / G, size included
     uint16_t *hi, *next, *lo;   // X = hi + lo, the next X's hi
     uint16_t *A, *B;
+    float *dA, *dB;             // [n][lds] what the rounding of A's diagonal left, and what B's lacks for both
     int n, N, K, side, ldx, lds, parts, g_bf16;
     int first, lo_in, lo_out, last;   // of a step: its X is G's, X has a lo, X' gets one, X' goes to out
     float size, a, b, c, b_over_c, scale, eps;
@@ -62,11 +63,24 @@ __device__ __forceinline__ bool range_tile(int64_t total, int64_t &t) {
     return q < per && t < total;
 }
 
-// a X added to a tile's sums while the rows (TALL: columns) of the tile pass
-// through LDS as an operand: a wave's subtiles that lie in step s.
+// Of a value per row i (TALL: column `lane` of 64 at most) that of a lane's value 4 q + k of subtile (i, j).
+template <int TALL, int MT> __device__ __forceinline__ float diagonal(const float (&d)[MT], int i, int j, int q, int k) {
+    if constexpr (!TALL) {
+        return d[i];
+    } else {
+        const int bits = __builtin_bit_cast(int, d[0]), c = 32 * j + 8 * q + k;
+        const int x = __builtin_amdgcn_readlane(bits, c), y = __builtin_amdgcn_readlane(bits, c + 4);
+        return __builtin_bit_cast(float, (threadIdx.x >> 5) & 1 ? y : x);
+    }
+}
+
+// a X, or (a + d) X with a d for each row (TALL: column), added to a tile's sums
+// while the rows (TALL: columns) of the tile pass through LDS as an operand: a
+// wave's subtiles that lie in step s.
 template <int BN, int MT, int NT2, int TALL> struct AddX {
     f32x16_t (&acc)[MT][NT2];
     float a;
+    const float (&d)[MT];   // of row 32 i + lane % 32; TALL: of column `lane`, in d[0]
     int from, m0, n0;   // the wave's first row (TALL: column) in the matrix; its place in the tile
     bool on;
     __device__ __forceinline__ void operator()(int s, const uint8_t *ta, const uint8_t *tb) const {
@@ -74,13 +88,17 @@ template <int BN, int MT, int NT2, int TALL> struct AddX {
         if (!on || 64 * s + 64 <= from || 64 * s >= from + L) return;
         const int l = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int u = 0; u < (TALL ? NT2 : MT); ++u) {
+            const int at = from + 32 * u - 64 * s;   // the subtile in the step
+            if (at < 0 || at >= 64) continue;
 #pragma unroll
-            for (int j = 0; j < NT2; ++j) {
-                const int at = from + 32 * (TALL ? j : i) - 64 * s;   // the subtile in the step
-                if (at < 0 || at >= 64) continue;
+            for (int q = 0; q < 4; ++q) {
+                float f[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int k = 0; k < 4; ++k) f[k] = a + diagonal<TALL>(d, u, u, q, k);
+#pragma unroll
+                for (int v = 0; v < (TALL ? MT : NT2); ++v) {
+                    const int i = TALL ? v : u, j = TALL ? u : v;
                     u32x2_t w;
                     if (TALL) {
                         const int r = m0 + 32 * i + l;
@@ -91,9 +109,10 @@ template <int BN, int MT, int NT2, int TALL> struct AddX {
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        acc[i][j][4 * q + k] = fmaf(a, half_value(w[k / 2], k & 1), acc[i][j][4 * q + k]);
+                        acc[i][j][4 * q + k] = fmaf(f[k], half_value(w[k / 2], k & 1), acc[i][j][4 * q + k]);
                 }
             }
+        }
     }
 };
 
@@ -101,7 +120,10 @@ template <int BN, int MT, int NT2, int TALL> struct AddX {
 // only the tiles of the lower half are computed.  Those off the diagonal are
 // stored a second time, transposed: a wave turns its part in LDS, where 16-byte
 // stores would otherwise be 2-byte ones.  b A is met as an operand passes
-// through LDS (b/c A is, ahead of the factor c).
+// through LDS (b/c A is, ahead of the factor c).  The diagonals, near which most
+// of the norms lie, are known in fp32: what their rounding to fp16 left of B's
+// (of A's, times b + 2 c A) meets X with a, without which matrices of equal
+// singular values came out up to 7e-3 off, all in one direction.
 template <int BM, int WM, int WN, int ST, int C, int SQUARE, int ACROSS>
 __global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
     constexpr int NT = 64 * WM * WN, MT = BM / 32 / WM, NT2 = BM / 32 / WN;
@@ -139,7 +161,8 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
     if (!active) {
         contract<ST, false, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
     } else if constexpr (SQUARE) {
-        const AddX<BM, MT, NT2, 1> hook{acc, a.b_over_c, k0 + n0, m0, n0, true};
+        const float none[MT] = {};
+        const AddX<BM, MT, NT2, 1> hook{acc, a.b_over_c, none, k0 + n0, m0, n0, true};
         contract<ST, true, BM, BM, C, MT, NT2, 0, 0, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
     } else {
         contract<ST, true, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
@@ -154,6 +177,27 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
             for (int q = 0; q < 8; ++q) w[i][j][q] = half_pair(acc[i][j][2 * q] * r, acc[i][j][2 * q + 1] * r);
+    if (ti == tj && active) {   // this wave's values of the diagonal, and what their rounding left
+        const int on = (l >> 2 & 1) == h ? 4 * (l >> 3) + (l & 3) : -1;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT2; ++j) {
+                const int row = r0 + m0 + 32 * i + l;
+                if (m0 + 32 * i != n0 + 32 * j) continue;
+                float v = 0.f, x = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    v = k == on ? acc[i][j][k] * r : v;
+                    x = k == on ? half_value(w[i][j][k / 2], k & 1) : x;
+                }
+                if (on < 0 || row >= a.lds) continue;
+                const int64_t at = (int64_t)e * a.lds + row;
+                if (!SQUARE) a.dA[at] = v - x;
+                else if (row >= a.side) a.dB[at] = 0.f;
+                else a.dB[at] = fmaf(fmaf(2.f * a.c, half_to_float(A0[(int64_t)row * a.lds + row]), a.b), a.dA[at], v - x);
+            }
+    }
     if (ti != tj) {
         // the wave's part [32 NT2 columns][32 MT rows], rows 16 bytes apart from a multiple of the banks
         constexpr int LD = 32 * MT + 8, PER = ST == 2 ? 2 : 1, PART = OA::BYTES / PER;
@@ -225,19 +269,27 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     const int steps = (a.lds + C - 1) / C;
+    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+    float d[MT];
+    {
+        static_assert(NT2 <= 2, "a lane for each column");
+        const float *dB = a.dB + (int64_t)e * a.lds;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) d[i] = TALL && i ? 0.f : dB[min(TALL ? k0 + n0 + lane : r0 + m0 + 32 * i + l, a.lds - 1)];
+    }
     if (m0 >= M || k0 + n0 >= a.ldx) {
         contract<ST, false, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
         return;
     }
-    const AddX<BN, MT, NT2, TALL> hook{acc, a.a, TALL ? k0 + n0 : r0 + m0, m0, n0, !a.first};
+    const AddX<BN, MT, NT2, TALL> hook{acc, a.a, d, TALL ? k0 + n0 : r0 + m0, m0, n0, !a.first};
     contract<ST, true, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
-    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
     if (a.first) {   // X is G, to all of its digits
-        const float r = a.a * a.factor[e];
+        const float r = a.factor[e];
         const int64_t g0 = ((int64_t)e * a.N + r0) * a.K;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             __builtin_amdgcn_sched_barrier(0);   // no more than a subtile row's loads ahead: registers
+            if (TALL) asm volatile("" : "+v"(d[0]));   // nor its values kept from one row to the next
 #pragma unroll
             for (int j = 0; j < NT2; ++j)
 #pragma unroll
@@ -266,7 +318,8 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[i][j][4 * q + k] = fmaf(r, x[k], acc[i][j][4 * q + k]);
+                    for (int k = 0; k < 4; ++k)
+                        acc[i][j][4 * q + k] = fmaf(r * (a.a + diagonal<TALL>(d, i, j, q, k)), x[k], acc[i][j][4 * q + k]);
                 }
         }
     }

@@ -583,6 +583,21 @@ def test_orthogonalise_of_equal_singular_values(n, N, K):
     assert float(along.abs().max()) <= 2.0 ** -10, along
 
 
+@pytest.mark.parametrize("n,N,K", [(2, 130, 300), (2, 301, 131), (2, 200, 1800), (1, 512, 1024), (3, 1040, 520), (16, 264, 530),
+                                   (14, 768, 1024), (14, 1024, 765), (28, 520, 1100), (28, 1100, 520)])
+def test_orthogonalise_of_equal_singular_values_in_tiles(n, N, K):
+    """As above where a matrix is cut into tiles, each of the steps' and of the squares' tiles."""
+    print(f"case orth equal n={n} N={N} K={K}", flush=True)
+    side, long = min(N, K), max(N, K)
+    q = torch.linalg.qr(rand(1, long, side, seed=6).double()).Q * 3
+    g = (q if N > K else q.transpose(1, 2)).float().contiguous()
+    got = run_orth(g.expand(n, N, K).contiguous().cuda(), 5, COEF, 1.0, 1e-7)
+    assert bool((got == got[:1]).all())
+    ref = R.orthogonalise(g.cuda().double(), 5, tuple(f32(v) for v in COEF), 1.0, f32(1e-7))
+    along = ((got[:1].double() - ref) * ref).sum() / ref.square().sum()
+    assert abs(float(along)) <= 2.0 ** -10, along
+
+
 # --------------------------------------------- graphs, streams, repetition
 
 def every_call(seed):
