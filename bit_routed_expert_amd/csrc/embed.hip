@@ -11,6 +11,13 @@
 // that crosses chunks (frequent tokens) leaves one partial sum per chunk,
 // and a second launch joins them where the run starts.  No atomics: the
 // order of every sum follows from the ids.
+//
+// Up to EB_FEW tokens take one launch: a block for each token finds the tokens
+// of the same id and, where its own is the first, adds their rows; others write
+// the zeros between.  us against the launches above, drawn ids and all of one row: 9
+// tokens of 531 x 640 3.6 and 3.3 against 8.9 and 7.9; 128 3.3 and 10.7 against 12
+// and 11; 256 3.4 and 19 against 13 and 12; 256 of 5000 x 2048, zeros included, 5.4
+// (bf16) and 34 (fp32) against 18 and 21.
 #include <cmath>
 #include <type_traits>
 
@@ -24,6 +31,8 @@ constexpr int EB_BITS = 10;          // of a sort pass
 constexpr int EB_DIGIT = 1 << EB_BITS;
 constexpr int EB_VOCAB = (1 << 20) - 1;
 constexpr int EB_TOKENS = 1 << 22;
+constexpr int EB_FEW = 256;          // tokens of a call of one launch, at most a block's threads
+constexpr int EB_FEW_ZEROS = 2048;   // most blocks of its zeros
 
 template <typename W, typename O, int V, int G>
 __global__ __launch_bounds__(256) void embed_kernel(const W *__restrict__ table, const int32_t *__restrict__ ids, O *out,
@@ -184,6 +193,65 @@ template <typename W, int V> __global__ __launch_bounds__(256) void embed_join_k
     }
 }
 
+// A call of few tokens: T * shares blocks for the tokens, the others for the zeros of `per` rows each.
+template <typename W, typename O, int V> __global__ __launch_bounds__(256) void embed_few_kernel(EmbedBack a, int vocab, int shares, int per) {
+    __shared__ int tok[EB_FEW], cnt[4];
+    __shared__ uint32_t taken[((EB_VOCAB + EB_FEW_ZEROS) / EB_FEW_ZEROS + 31) / 32];
+    const int th = threadIdx.x, lane = th & 63, w = __builtin_amdgcn_readfirstlane(th >> 6);
+    const int b = blockIdx.x, id = th < a.T ? a.ids[th] : -1;
+    if (b < a.T * shares) {
+        const int t = b / shares, mine = a.ids[t];
+        if ((uint32_t)mine >= (uint32_t)vocab) return;
+        const uint64_t m = __ballot(id == mine);
+        if (lane == 0) cnt[w] = __popcll(m);
+        __syncthreads();
+        int at = __popcll(m & ((1ull << lane) - 1)), n = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q < w) at += cnt[q];
+            n += cnt[q];
+        }
+        if (id == mine) tok[at] = th;
+        __syncthreads();
+        if (tok[0] != t) return;
+        const O *dout = (const O *)a.dout;
+        for (int i = ((b - t * shares) * 256 + th) * V; i < a.d; i += shares * 256 * V) {
+            float s[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = 0.f;
+            const auto rows = [&](int r0, auto many) {
+                constexpr int R = decltype(many)::value;
+                Raw<O, V> v[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r)   // behind the last one that again, so that no load waits behind a branch
+                    load_raw<V, true>(dout, (int64_t)tok[min(r0 + r, n - 1)] * a.d + i, v[r]);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (r0 + r < n) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) s[j] += value<V>(v[r], j);
+                    }
+            };
+            int r0 = 0;
+            for (; r0 + 16 <= n; r0 += 16) rows(r0, std::integral_constant<int, 16>());
+            for (; r0 < n; r0 += 4) rows(r0, std::integral_constant<int, 4>());
+            embed_store<W, V>(a, mine, i, s);
+        }
+        return;
+    }
+    const int v0 = (b - a.T * shares) * per, rows = min(per, vocab - v0);
+    for (int i = th; i < (rows + 31) / 32; i += 256) taken[i] = 0;
+    __syncthreads();
+    if ((uint32_t)(id - v0) < (uint32_t)rows && id >= 0) atomicOr(&taken[(id - v0) >> 5], 1u << ((id - v0) & 31));
+    __syncthreads();
+    const uint32_t nq = (uint32_t)(a.d / V);
+    const float zero[V] = {};
+    for (int r = 0; r < rows; ++r) {
+        if (taken[r >> 5] >> (r & 31) & 1) continue;
+        for (uint32_t q = th; q < nq; q += 256) store_values<V>((W *)a.dW, (int64_t)(v0 + r) * a.d + q * V, zero);
+    }
+}
+
 // n 16-byte pieces of zeros, and the bytes behind them: the share of block b of
 // nb, in one piece (524 MB beside the sort: 126 us the gradient, 133 where the
 // blocks go through it side by side).
@@ -233,6 +301,12 @@ struct BackCall {
     hipStream_t s;
 };
 
+struct FewCall {
+    EmbedBack a;
+    int V, d;
+    hipStream_t s;
+};
+
 struct Chunks {
     template <typename W, typename O, int V> static void run(const BackCall &c) {
         const RowGroups q = row_groups(c.a.chunks, c.d / V, 16);
@@ -250,6 +324,17 @@ struct Join {
         if (!std::is_same<O, float>::value) return;   // the partial sums have one type
         const int slabs = (c.d + 64 * V - 1) / (64 * V);
         STRATA_LAUNCH((embed_join_kernel<W, V>), dim3(c.a.chunks, slabs < 64 ? slabs : 64), dim3(256), 0, c.s, c.a);
+    }
+};
+
+struct Few {
+    template <typename W, typename O, int V> static void run(const FewCall &c) {
+        const int64_t pieces = c.d / V;
+        int shares = (int)((pieces + 255) / 256);   // of a row
+        shares = shares < 16 ? shares : 16;
+        const int zeros = c.a.add ? 0 : c.V < EB_FEW_ZEROS ? c.V : EB_FEW_ZEROS, per = zeros ? (c.V + zeros - 1) / zeros : 1;
+        STRATA_LAUNCH((embed_few_kernel<W, O, V>), dim3(c.a.T * shares + (zeros ? (c.V + per - 1) / per : 0)), dim3(256), 0, c.s, c.a,
+                      c.V, shares, per);
     }
 };
 
@@ -360,6 +445,9 @@ strata_status strata_embed_backward(const void *dout, strata_xdtype odtype, cons
     if (T > 0 && (overlap(dW, bytes, ws, p.bytes) || overlap(dW, bytes, ids, (size_t)T * 4) ||
                   overlap(ws, p.bytes, ids, (size_t)T * 4)))
         return STRATA_EINVAL;
+    if (T > 0 && T <= EB_FEW)
+        return hip_status(embed_types<Few>(FewCall{EmbedBack{dout, ids, nullptr, dW, nullptr, nullptr, T, d, 0, add, scale}, V, d, s}, wdtype,
+                                           odtype));
     // The zeros: beside the sort's passes where those are one launch each.
     const bool two = V > EB_DIGIT, beside = T > 0 && T <= SORT_ONCE;
     Zeros z{(u32x4_t *)dW, add ? 0 : bytes / 16, add ? 0 : (int)(bytes % 16)};
@@ -389,7 +477,7 @@ strata_status strata_embed_backward(const void *dout, strata_xdtype odtype, cons
     }
     BackCall c{EmbedBack{dout, ids, order, dW, (float *)(w + p.head), (float *)(w + p.tail), T, d, p.chunks, add, scale}, d, s};
     e = embed_types<Chunks>(c, wdtype, odtype);
-    if (e != hipSuccess || p.chunks == 1) return hip_status(e);
+    if (e != hipSuccess) return hip_status(e);
     return hip_status(embed_types<Join>(c, wdtype, STRATA_X_F32));
 }
 

@@ -241,6 +241,35 @@ def test_embed_gradient_of_long_runs_and_many_tokens(T, V, d, kind):
     check(got, ref, (n[:, None] + 2) * U * mag, "dW")
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,V,d,kind", [(256, 5001, 33, "mixed"), (257, 5001, 33, "mixed"), (256, (1 << 20) - 1, 3, "mixed"),
+                                        (255, 700, 5002, "one"), (272, 9, 8, "one"), (257, 1, 1, "one"), (64, 2049, 130, "none"),
+                                        (256, 4097, 24, "pairs")])
+def test_embed_gradient_about_the_border_of_one_launch(T, V, d, kind, dt):
+    """Few tokens (one launch) and just more: every row between them zero, or left as it was, runs of all lengths."""
+    print(f"case embed border T={T} V={V} d={d} {kind} {dt}", flush=True)
+    ids = draw_ids(T, V, 8)
+    if kind == "one":
+        ids = torch.full((T,), V - 1, dtype=torch.int32)
+    elif kind == "none":
+        ids = torch.full((T,), V, dtype=torch.int32)
+    elif kind == "pairs":   # the same id far apart, the first and the last rows
+        ids = torch.arange(T, dtype=torch.int32) % (T // 2)
+        ids[::7] = V - 1
+    dout = rand(T, d, seed=6, dtype=dt)
+    ref, mag, n = R.embed_backward(dout.double(), ids, V, -0.5)
+    nb = brx.embed_backward_workspace_bytes(T, V, d)
+    base = rand(V, d, seed=3, dtype=dt)
+    for flags in (0, brx.ACCUMULATE):
+        dW = Out(V, d, dtype=dt)
+        if flags:
+            dW.t.copy_(base)
+        brx.embed_backward(dout.cuda(), CODE[dt], ids.cuda(), T, V, d, -0.5, dW.t, CODE[dt], ws_of(nb), nb, flags=flags)
+        got, was = dW.guarded().cpu(), base if flags else torch.zeros_like(base)
+        assert torch.equal(got[n == 0], was[n == 0])
+        check(got, ref + was.double(), (n[:, None] + 3) * U * (mag + was.double().abs()), f"flags {flags}")
+
+
 def test_embed_past_32_bits_and_without_tokens():
     V, d = (1 << 19) + 7, 4104   # 2^31 elements are behind row 523,287
     assert V * d > 1 << 31
