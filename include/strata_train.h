@@ -126,8 +126,8 @@ strata_status strata_vocab_loss(const void *h, const void *W, const int32_t *tar
  *   dh[t] = sum_v dz[t][v] W[v]     [dev] [T][d] of dhdtype, nullable
  *   dW[v] = sum_t dz[t][v] h[t]     [dev] [V][d] of dwdtype, nullable
  *   flags: STRATA_ACCUMULATE: dW + the sum is written to dW (added in fp32), else the sum.
- * dz enters the products as bf16 where the output is bf16, and as two bf16 pieces (16 bits together) where
- * it is fp32.  T = 0 writes zeros to dW (without the flag).  Errors as above, and EINVAL for a bad dtype of
+ * dz enters the products as bf16 (over the first dloss's mantissa) where the output is bf16, and as two bf16
+ * pieces (16 bits together) where it is fp32.  T = 0 writes zeros to dW (without the flag).  Errors as above, and EINVAL for a bad dtype of
  * an output that is given, or unknown flags. */
 strata_status strata_vocab_loss_backward(const void *h, const void *W, const int32_t *targets, int32_t T, int32_t V,
                                          int32_t d, const float *lse, const float *dloss, const float *dlse, void *dh,
@@ -141,7 +141,8 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
  *   out = scale * X_steps
  * (the same polynomial from the right where N > K).  Operands of the products
  * are fp16 (11 bits), X itself is kept in two fp16 pieces (22 bits), so that
- * directions that G lacks are not made of its roundings; sums are fp32.
+ * directions that G lacks are not made of its roundings; the diagonals of A and
+ * of b A + c A^2 count in fp32, and sums are fp32.
  * A matrix of zeros gives zeros; infinities and NaN stay in their matrix, and
  * coefficients that take X or b A + c A^2 out of fp16's range make infinities.
  */
