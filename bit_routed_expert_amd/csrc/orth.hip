@@ -8,7 +8,7 @@
 // are in known ranges (|X| and |A| at most about 1, X kept times a power of
 // two), and 11 bits, with the diagonals of A and B in fp32, leave the result
 // about 5e-4 off, less than its own rounding to bf16 (1.7e-3), where bf16's 8
-// would leave 5e-3.  X itself is hi + lo, 22 bits (X_0 is G): with hi alone the rounding
+// would leave 5e-3.  X itself is hi + lo, 22 bits: with hi alone the rounding
 // of X, a matrix of full rank, would be multiplied by a at every step like the
 // small directions of G itself (3.4^5 = 485 in five steps; a gradient of 80 rows
 // in 1536 x 2048 would come out 2% off).  The last step takes hi alone: one
@@ -53,40 +53,82 @@ template <typename G, int V> __global__ __launch_bounds__(256) void orth_norm_ke
     if (threadIdx.x == 0) a.norms[e * a.parts + part] = sh[0] + sh[1] + sh[2] + sh[3];
 }
 
-// X_0 = G / (|G| + eps), times size, rounded to fp16 (or, without steps, times scale to out).
-template <typename G, int V> __global__ __launch_bounds__(256) void orth_start_kernel(OrthArgs a, int steps) {
+// 1 / (|G| + eps) of matrix e.
+__device__ __forceinline__ double one_over_norm(const OrthArgs &a, int e) {
+    static_assert(ORTH_PARTS <= 64, "a lane for each");
+    const int lane = threadIdx.x & 63;
+    double s = lane < a.parts ? a.norms[e * a.parts + lane] : 0.0;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
+    return 1.0 / (sqrt(s) + (double)a.eps);
+}
+
+// No steps: out = scale G / (|G| + eps).
+template <typename G, int V> __global__ __launch_bounds__(256) void orth_scale_kernel(OrthArgs a) {
     const int e = blockIdx.y;
-    double s = 0.0;
-    for (int q = 0; q < a.parts; ++q) s += a.norms[e * a.parts + q];
-    const double r = 1.0 / (sqrt(s) + (double)a.eps) * (steps ? (double)a.size : (double)a.scale);
-    const float f = (float)r;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.factor[e] = f;
-    const int nc = (steps ? a.ldx : a.K) / V;   // pieces of a row, those of zeros behind its end too
-    const G *g = (const G *)a.G + (int64_t)e * a.N * a.K;
-    const int64_t all = (int64_t)a.N * nc;
+    const double r = one_over_norm(a, e) * (double)a.scale;
+    const int64_t m0 = (int64_t)e * a.N * a.K, all = (int64_t)a.N * a.K / V;
     for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < all; p += (int64_t)gridDim.x * 256) {
-        const int64_t m = p / nc;
-        const int c = (int)(p - m * nc) * V;
         float v[V];
+        piece_values<V, G>((const G *)a.G + m0, p * V, v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = 0.f;
-        if (c < a.K) piece_values<V, G>(g, m * a.K + c, v);
-        if (!steps) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = (float)((double)v[j] * r);
-            store_values<V>(a.out + (int64_t)e * a.N * a.K, m * a.K + c, v);
-            continue;
-        }
-        uint16_t *hi = a.hi + ((int64_t)e * a.N + m) * a.ldx + c;
-        if constexpr (V == 1) {
-            *hi = (uint16_t)half_pair(v[0] * f, 0.f);
-        } else {
-            uint32_t w[V / 2];
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) w[j] = half_pair(v[2 * j] * f, v[2 * j + 1] * f);
-            __builtin_memcpy(__builtin_assume_aligned(hi, 2 * V), w, 2 * V);
-        }
+        for (int j = 0; j < V; ++j) v[j] = (float)((double)v[j] * r);
+        store_values<V>(a.out + m0, p * V, v);
     }
+}
+
+// The tiles of a step, and their subtiles in the order of lo: tile, wave, row of subtiles, column.
+struct StepShape {
+    int bm, bn, wm, wn;
+};
+
+// X_0 = G / (|G| + eps), times size, as hi and lo: a wave takes a subtile of the
+// steps' tiles, zeros where it lies outside the matrix.  201 MB to 101 us, 4 TB/s
+// (a first step that read G in place of lo, in its few waves' epilogue, took 280 us
+// for 215 and this kernel 50: the same in all for 16 of 1536 x 2048, but 316 for
+// 307 us of 1 of 2048 x 2048 and 98 for 95 of 6 of 173 x 874).
+template <typename G, int V> __global__ __launch_bounds__(256) void orth_start_kernel(OrthArgs a, StepShape k, int64_t all) {
+    const int64_t s = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (s >= all) return;
+    const int mt = k.bm / 32 / k.wm, nt = k.bn / 32 / k.wn, per = k.wm * k.wn * mt * nt;
+    const int64_t t = s / per;
+    const int u = (int)(s - t * per), j = u % nt, i = u / nt % mt, w = u / (nt * mt);
+    const int nk = (a.K + k.bn - 1) / k.bn, nr = (a.N + k.bm - 1) / k.bm;
+    const int e = (int)(t / (nr * nk)), at = (int)(t - (int64_t)e * nr * nk);
+    int m0, n0;
+    wave_place_of(w, k.wm, k.wn, mt, nt, m0, n0);
+    const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
+    const int row0 = at / nk * k.bm, m = row0 + m0 + 32 * i + l, n = at % nk * k.bn + n0 + 32 * j;
+    const double r = one_over_norm(a, e) * (double)a.size;
+    const float f = (float)r;
+    const G *g = (const G *)a.G + (int64_t)e * a.N * a.K;
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; c += V) {
+            float v[V];
+#pragma unroll
+            for (int p = 0; p < V; ++p) v[p] = 0.f;
+            const int col = n + 8 * q + 4 * h + c;
+            if (m < a.N && col < a.K) piece_values<V, G>(g, (int64_t)m * a.K + col, v);
+#pragma unroll
+            for (int p = 0; p < V; ++p) x[4 * q + c + p] = v[p] * f;
+        }
+    u32x2_t *const lo = (u32x2_t *)a.lo + s * 256 + lane;
+    uint32_t w2[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        u32x2_t y;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t z = half_pair_kept(x[4 * q + 2 * p], x[4 * q + 2 * p + 1]);
+            w2[2 * q + p] = z;
+            y[p] = half_pair(x[4 * q + 2 * p] - half_value(z, 0), x[4 * q + 2 * p + 1] - half_value(z, 1));
+        }
+        lo[q * 64] = y;
+    }
+    store_halves(half_rows(a.hi + ((int64_t)e * a.N + row0) * a.ldx, min(a.N - row0, k.bm), a.ldx), m0 + 32 * i, n, a.ldx, 0, 0, w2);
 }
 
 namespace {
@@ -99,7 +141,7 @@ strata_status check_orth(int32_t n, int32_t N, int32_t K) {
 
 struct OrthPlan {
     int side, ldx, lds;
-    size_t factor, hi, next, lo, A, B, dA, dB, bytes;
+    size_t hi, next, lo, A, B, dA, dB, bytes;
 };
 
 // Tiles of a step by how many of 128 square there are: below 144, 64 x 128 (a
@@ -110,7 +152,7 @@ struct OrthPlan {
 // 239 and 274); then 256 square (4 of 2048 x 2048: 940, 128 square 980; 16 of
 // 1536 x 2048: 1892 and 2055, 128 x 256 1956).
 enum StepTile { STEP_64, STEP_128, STEP_128_TWO, STEP_256 };
-constexpr int STEP_ROWS[] = {64, 128, 128, 256}, STEP_COLS[] = {128, 128, 128, 256};
+constexpr StepShape STEP_SHAPES[] = {{64, 128, 2, 2}, {128, 128, 2, 2}, {128, 128, 2, 4}, {256, 256, 2, 4}};
 StepTile step_tile(int32_t n, int32_t N, int32_t K) {
     const int64_t tiles = (int64_t)n * ((N + 127) / 128) * ((K + 127) / 128);
     return tiles < 144 ? STEP_64 : tiles <= 256 ? STEP_128 : tiles < 1024 ? STEP_128_TWO : STEP_256;
@@ -128,12 +170,11 @@ OrthPlan orth_plan(int32_t n, int32_t N, int32_t K) {
         return q;
     };
     const size_t x = (size_t)n * N * p.ldx, s = (size_t)n * p.side * p.lds;
-    const StepTile t = step_tile(n, N, K);
-    const size_t rows = (size_t)(N + STEP_ROWS[t] - 1) / STEP_ROWS[t] * STEP_ROWS[t];
-    p.factor = take((size_t)(n > 0 ? n : 1) * 2);
+    const StepShape k = STEP_SHAPES[step_tile(n, N, K)];
+    const size_t rows = (size_t)(N + k.bm - 1) / k.bm * k.bm, cols = (size_t)(K + k.bn - 1) / k.bn * k.bn;
     p.hi = take(x);
     p.next = take(x);
-    p.lo = take(n * rows * ((K + STEP_COLS[t] - 1) / STEP_COLS[t] * STEP_COLS[t]));   // whole tiles
+    p.lo = take(n * rows * cols);   // whole tiles
     p.A = take(s);
     p.B = take(s);
     p.dA = take((size_t)n * p.lds * 2);
@@ -146,8 +187,14 @@ template <typename G, int V> hipError_t orth_begin(const OrthArgs &a, int steps,
     STRATA_LAUNCH((orth_norm_kernel<G, V>), dim3(a.parts, a.n), dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t pieces = (int64_t)a.N * a.ldx / V, blocks = (pieces + 1023) / 1024, most = 8192 / a.n + 1;
-    STRATA_LAUNCH((orth_start_kernel<G, V>), dim3((unsigned)(blocks < most ? blocks : most), a.n), dim3(256), 0, s, a, steps);
+    if (steps == 0) {
+        const int64_t blocks = ((int64_t)a.N * a.K / V + 1023) / 1024, most = 8192 / a.n + 1;
+        STRATA_LAUNCH((orth_scale_kernel<G, V>), dim3((unsigned)(blocks < most ? blocks : most), a.n), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    const StepShape k = STEP_SHAPES[step_tile(a.n, a.N, a.K)];
+    const int64_t tiles = (int64_t)a.n * ((a.N + k.bm - 1) / k.bm) * ((a.K + k.bn - 1) / k.bn), all = tiles * (k.bm / 32) * (k.bn / 32);
+    STRATA_LAUNCH((orth_start_kernel<G, V < 4 ? V : 4>), dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, a, k, all);
     return hipGetLastError();
 }
 
@@ -257,8 +304,6 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     a.G = G;
     a.out = (uint16_t *)out;
     a.norms = (double *)w;
-    a.factor = (float *)(w + p.factor);
-    a.g_bf16 = gdtype == STRATA_X_BF16;
     a.hi = (uint16_t *)(w + p.hi);
     a.next = (uint16_t *)(w + p.next);
     a.lo = (uint16_t *)(w + p.lo);
@@ -290,9 +335,8 @@ strata_status strata_orthogonalise(const void *G, strata_xdtype gdtype, int32_t 
     hipError_t e = gdtype == STRATA_X_BF16 ? orth_begin_width<uint16_t>(a, steps, s) : orth_begin_width<float>(a, steps, s);
     for (int i = 0; i < steps && e == hipSuccess; ++i) {
         const int left = steps - 1 - i;   // steps behind this one
-        a.first = i == 0;
         a.last = left == 0;
-        a.lo_in = i > 0 && left > 0;
+        a.lo_in = left > 0 || steps == 1;
         a.lo_out = left > 1;
         e = tall ? squares<0, 1>(a, s) : squares<0, 0>(a, s);
         if (e == hipSuccess) e = squares<1, 0>(a, s);

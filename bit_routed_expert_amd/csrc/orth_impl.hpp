@@ -14,12 +14,11 @@ struct OrthArgs {
     const void *G;
     uint16_t *out;              // bf16 [n][N][K]
     double *norms;              // [n][parts] sums of squares
-    float *factor;              // [n] X_0 / G, size included
     uint16_t *hi, *next, *lo;   // X = hi + lo, the next X's hi
     uint16_t *A, *B;
     float *dA, *dB;             // [n][lds] what the rounding of A's diagonal left, and what B's lacks for both
-    int n, N, K, side, ldx, lds, parts, g_bf16;
-    int first, lo_in, lo_out, last;   // of a step: its X is G's, X has a lo, X' gets one, X' goes to out
+    int n, N, K, side, ldx, lds, parts;
+    int lo_in, lo_out, last;   // of a step: X's lo counts, X' gets one, X' goes to out
     float size, a, b, c, b_over_c, scale, eps;
 };
 
@@ -27,6 +26,15 @@ __device__ __forceinline__ float half_value(uint32_t w, int high) { return half_
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
     typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});
+}
+
+// The same, as bits that every use shares: rounded twice in one place and, fused
+// with the product ahead of it, once in another, hi and what is subtracted for
+// lo would differ (by 2^-11 at a tie).
+__device__ __forceinline__ uint32_t half_pair_kept(float a, float b) {
+    uint32_t w = half_pair(a, b);
+    asm volatile("" : "+v"(w));
+    return w;
 }
 
 // Buffer of M rows of ld 16-bit values.
@@ -82,10 +90,9 @@ template <int BN, int MT, int NT2, int TALL> struct AddX {
     float a;
     const float (&d)[MT];   // of row 32 i + lane % 32; TALL: of column `lane`, in d[0]
     int from, m0, n0;   // the wave's first row (TALL: column) in the matrix; its place in the tile
-    bool on;
     __device__ __forceinline__ void operator()(int s, const uint8_t *ta, const uint8_t *tb) const {
         constexpr int L = 32 * (TALL ? NT2 : MT);
-        if (!on || 64 * s + 64 <= from || 64 * s >= from + L) return;
+        if (64 * s + 64 <= from || 64 * s >= from + L) return;
         const int l = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
 #pragma unroll
         for (int u = 0; u < (TALL ? NT2 : MT); ++u) {
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
         contract<ST, false, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
     } else if constexpr (SQUARE) {
         const float none[MT] = {};
-        const AddX<BM, MT, NT2, 1> hook{acc, a.b_over_c, none, k0 + n0, m0, n0, true};
+        const AddX<BM, MT, NT2, 1> hook{acc, a.b_over_c, none, k0 + n0, m0, n0};
         contract<ST, true, BM, BM, C, MT, NT2, 0, 0, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
     } else {
         contract<ST, true, BM, BM, C, MT, NT2, ACROSS, ACROSS, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_square_kernel(OrthArgs a) {
 #pragma unroll
         for (int j = 0; j < NT2; ++j)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) w[i][j][q] = half_pair(acc[i][j][2 * q] * r, acc[i][j][2 * q + 1] * r);
+            for (int q = 0; q < 8; ++q) w[i][j][q] = half_pair_kept(acc[i][j][2 * q] * r, acc[i][j][2 * q + 1] * r);
     if (ti == tj && active) {   // this wave's values of the diagonal, and what their rounding left
         const int on = (l >> 2 & 1) == h ? 4 * (l >> 3) + (l & 3) : -1;
 #pragma unroll
@@ -281,48 +288,8 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
         contract<ST, false, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc);
         return;
     }
-    const AddX<BN, MT, NT2, TALL> hook{acc, a.a, d, TALL ? k0 + n0 : r0 + m0, m0, n0, !a.first};
+    const AddX<BN, MT, NT2, TALL> hook{acc, a.a, d, TALL ? k0 + n0 : r0 + m0, m0, n0};
     contract<ST, true, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
-    if (a.first) {   // X is G, to all of its digits
-        const float r = a.factor[e];
-        const int64_t g0 = ((int64_t)e * a.N + r0) * a.K;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            __builtin_amdgcn_sched_barrier(0);   // no more than a subtile row's loads ahead: registers
-            if (TALL) asm volatile("" : "+v"(d[0]));   // nor its values kept from one row to the next
-#pragma unroll
-            for (int j = 0; j < NT2; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = m0 + 32 * i + l, n = k0 + n0 + 32 * j + 8 * q + 4 * h;
-                    float x[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (m < M && n < a.K) {
-                        const int64_t p = g0 + (int64_t)m * a.K + n;
-                        if (a.K % 4 == 0) {
-                            if (a.g_bf16) {
-                                Raw<uint16_t, 4> w;
-                                load_raw<4>((const uint16_t *)a.G, p, w);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) x[k] = value<4>(w, k);
-                            } else {
-                                Raw<float, 4> w;
-                                load_raw<4>((const float *)a.G, p, w);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) x[k] = value<4>(w, k);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (n + k < a.K)
-                                    x[k] = a.g_bf16 ? bf16_to_float(((const uint16_t *)a.G)[p + k]) : ((const float *)a.G)[p + k];
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[i][j][4 * q + k] = fmaf(r * (a.a + diagonal<TALL>(d, i, j, q, k)), x[k], acc[i][j][4 * q + k]);
-                }
-        }
-    }
     u32x2_t *const lo = (u32x2_t *)a.lo + (t * (WM * WN) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * (MT * NT2 * 4 * 64) + lane;
     if (a.lo_in) {
 #pragma unroll
@@ -367,7 +334,7 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
         for (int j = 0; j < NT2; ++j) {
             uint32_t w[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = half_pair(acc[i][j][2 * q], acc[i][j][2 * q + 1]);
+            for (int q = 0; q < 8; ++q) w[q] = half_pair_kept(acc[i][j][2 * q], acc[i][j][2 * q + 1]);
             if (a.lo_out) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {

@@ -308,10 +308,13 @@ __device__ __forceinline__ void store_tile(void *C, int c_bf16, int m0, int M, i
 // still keeps as many SIMDs busy as it has waves.  32768 rows of 16 experts,
 // 1288 x 1288, the last tiles 8 wide, with waves outside them idle: product 128
 // -> 121 us, wgrad 152 -> 130 us.
+__device__ __forceinline__ void wave_place_of(int wv, int wm, int wn, int mt, int nt, int &m0, int &n0) {
+    const int m = wv / wn;
+    m0 = m * 32 * mt;
+    n0 = (wm == 2 && wn == 4 ? (wv % wn) ^ (2 * m) : wv % wn) * 32 * nt;
+}
 template <int WM, int WN, int MT, int NT2> __device__ __forceinline__ void wave_place(int &m0, int &n0) {
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), m = wv / WN;
-    m0 = m * 32 * MT;
-    n0 = (WM == 2 && WN == 4 ? (wv % WN) ^ (2 * m) : wv % WN) * 32 * NT2;
+    wave_place_of(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6), WM, WN, MT, NT2, m0, n0);
 }
 
 }  // namespace strata
