@@ -15,7 +15,7 @@
 // factor a.
 //
 // 16 of 1536 x 2048, a step: A 116 us, B 84 (0.66 and 0.69 PFLOP/s of the halves
-// computed), X' 196 (0.79); bound by what the products wait for their loads.
+// computed), X' 189 (0.82); bound by what the products wait for their loads.
 #include <cmath>
 
 #include "orth_small.hpp"
