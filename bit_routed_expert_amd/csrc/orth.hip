@@ -15,7 +15,7 @@
 // factor a.
 //
 // 16 of 1536 x 2048, a step: A 116 us, B 84 (0.66 and 0.69 PFLOP/s of the halves
-// computed), X' 189 (0.82); bound by what the products wait for their loads.
+// computed), X' 184 (0.84); bound by what the products wait for their loads.
 #include <cmath>
 
 #include "orth_small.hpp"
@@ -87,8 +87,8 @@ struct StepShape {
 // (a first step that read G in place of lo, in its few waves' epilogue, took 280 us
 // for 215 and this kernel 50: the same in all for 16 of 1536 x 2048, but 316 for
 // 307 us of 1 of 2048 x 2048 and 98 for 95 of 6 of 173 x 874).
-template <typename G, int V> __global__ __launch_bounds__(256) void orth_start_kernel(OrthArgs a, StepShape k, int64_t all) {
-    const int64_t s = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <typename G, int V> __global__ __launch_bounds__(512) void orth_start_kernel(OrthArgs a, StepShape k, int64_t all) {
+    const int64_t s = (int64_t)blockIdx.x * 8 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (s >= all) return;
     const int mt = k.bm / 32 / k.wm, nt = k.bn / 32 / k.wn, per = k.wm * k.wn * mt * nt;
     const int64_t t = s / per;
@@ -194,7 +194,7 @@ template <typename G, int V> hipError_t orth_begin(const OrthArgs &a, int steps,
     }
     const StepShape k = STEP_SHAPES[step_tile(a.n, a.N, a.K)];
     const int64_t tiles = (int64_t)a.n * ((a.N + k.bm - 1) / k.bm) * ((a.K + k.bn - 1) / k.bn), all = tiles * (k.bm / 32) * (k.bn / 32);
-    STRATA_LAUNCH((orth_start_kernel<G, V < 4 ? V : 4>), dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, a, k, all);
+    STRATA_LAUNCH((orth_start_kernel<G, V < 4 ? V : 4>), dim3((unsigned)((all + 7) / 8)), dim3(512), 0, s, a, k, all);
     return hipGetLastError();
 }
 
