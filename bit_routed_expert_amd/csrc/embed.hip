@@ -244,7 +244,8 @@ template <typename W, typename O, int V> __global__ __launch_bounds__(256) void 
     const int v0 = (b - a.T * shares) * per, rows = min(per, vocab - v0);
     for (int i = th; i < (rows + 31) / 32; i += 256) taken[i] = 0;
     __syncthreads();
-    if ((uint32_t)(id - v0) < (uint32_t)rows && id >= 0) atomicOr(&taken[(id - v0) >> 5], 1u << ((id - v0) & 31));
+    const uint32_t at = (uint32_t)id - (uint32_t)v0;   // ids below 0 come out past every row
+    if (at < (uint32_t)rows) atomicOr(&taken[at >> 5], 1u << (at & 31));
     __syncthreads();
     const uint32_t nq = (uint32_t)(a.d / V);
     const float zero[V] = {};
