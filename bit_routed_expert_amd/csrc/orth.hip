@@ -92,15 +92,17 @@ template <typename G, int V> __global__ __launch_bounds__(512) void orth_start_k
     if (s >= all) return;
     const int mt = k.bm / 32 / k.wm, nt = k.bn / 32 / k.wn, per = k.wm * k.wn * mt * nt;
     const int64_t t = s / per;
-    const int u = (int)(s - t * per), j = u % nt, i = u / nt % mt, w = u / (nt * mt);
+    const int sub = (int)(s - t * per), j = sub % nt, i = sub / nt % mt, w = sub / (nt * mt);
     const int nk = (a.K + k.bn - 1) / k.bn, nr = (a.N + k.bm - 1) / k.bm;
     const int e = (int)(t / (nr * nk)), at = (int)(t - (int64_t)e * nr * nk);
     int m0, n0;
     wave_place_of(w, k.wm, k.wn, mt, nt, m0, n0);
     const int lane = threadIdx.x & 63, l = lane & 31, h = lane >> 5;
     const int row0 = at / nk * k.bm, m = row0 + m0 + 32 * i + l, n = at % nk * k.bn + n0 + 32 * j;
+    // size / (|G| + eps) as two fp32 factors: alone it is past fp32 for norms below size / 3.4e38 (0 * inf for a matrix
+    // of zeros and a small eps) and has lost bits for norms above size * 8.5e37.  For r within 2^-64 .. 2^64 u is 1.
     const double r = one_over_norm(a, e) * (double)a.size;
-    const float f = (float)r;
+    const float u = r > 0x1p64 ? 0x1p64f : r < 0x1p-64 ? 0x1p-64f : 1.f, f = (float)(r / (double)u);
     const G *g = (const G *)a.G + (int64_t)e * a.N * a.K;
     float x[16];
 #pragma unroll
@@ -113,7 +115,7 @@ template <typename G, int V> __global__ __launch_bounds__(512) void orth_start_k
             const int col = n + 8 * q + 4 * h + c;
             if (m < a.N && col < a.K) piece_values<V, G>(g, (int64_t)m * a.K + col, v);
 #pragma unroll
-            for (int p = 0; p < V; ++p) x[4 * q + c + p] = v[p] * f;
+            for (int p = 0; p < V; ++p) x[4 * q + c + p] = v[p] * u * f;
         }
     u32x2_t *const lo = (u32x2_t *)a.lo + s * 256 + lane;
     uint32_t w2[8];
