@@ -11,8 +11,8 @@
 // would leave 5e-3.  X itself is hi + lo, 22 bits: with hi alone the rounding
 // of X, a matrix of full rank, would be multiplied by a at every step like the
 // small directions of G itself (3.4^5 = 485 in five steps; a gradient of 80 rows
-// in 1536 x 2048 would come out 2% off).  The last step takes hi alone: one
-// factor a.
+// in 1536 x 2048 would come out 2% off).  The last of several steps takes hi
+// alone: one factor a.
 //
 // 16 of 1536 x 2048, a step: A 116 us, B 84 (0.66 and 0.69 PFLOP/s of the halves
 // computed), X' 184 (0.84); bound by what the products wait for their loads.
@@ -126,7 +126,7 @@ template <typename G, int V> __global__ __launch_bounds__(512) void orth_start_k
         for (int p = 0; p < 2; ++p) {
             const uint32_t z = half_pair_kept(x[4 * q + 2 * p], x[4 * q + 2 * p + 1]);
             w2[2 * q + p] = z;
-            y[p] = half_pair(x[4 * q + 2 * p] - half_value(z, 0), x[4 * q + 2 * p + 1] - half_value(z, 1));
+            y[p] = half_pair_left(x[4 * q + 2 * p], x[4 * q + 2 * p + 1], z);
         }
         lo[q * 64] = y;
     }

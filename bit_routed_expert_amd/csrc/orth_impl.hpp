@@ -9,7 +9,11 @@ namespace strata {
 // about 1 in size at the end).  hi, its fp16 rounding, lies in rows of ldx
 // values, A and B in rows of lds; what lies in a row behind its last column is
 // zero.  lo, what the rounding left, is the step kernel's alone and lies in the
-// order of its lanes: 4 values to a lane, the wave's lanes side by side.
+// order of its lanes: 4 values to a lane, the wave's lanes side by side.  It is
+// kept times 2^11: hi's values of 2^-5 to 2^-7 leave 2^-17 and less, of which
+// fp16, subnormal below 2^-14, would hold a few bits (2^-24 is its least step),
+// and nothing of values below 2^-13.  What hi leaves is at most 16 (next to
+// 65504), so 2^11 of it is in range.
 struct OrthArgs {
     const void *G;
     uint16_t *out;              // bf16 [n][N][K]
@@ -21,6 +25,8 @@ struct OrthArgs {
     int lo_in, lo_out, last;   // of a step: X's lo counts, X' gets one, X' goes to out
     float size, a, b, c, b_over_c, scale, eps;
 };
+
+constexpr float ORTH_LO = 0x1p11f;
 
 __device__ __forceinline__ float half_value(uint32_t w, int high) { return half_to_float((uint16_t)(high ? w >> 16 : w)); }
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
@@ -35,6 +41,11 @@ __device__ __forceinline__ uint32_t half_pair_kept(float a, float b) {
     uint32_t w = half_pair(a, b);
     asm volatile("" : "+v"(w));
     return w;
+}
+
+// What hi (the pair w) leaves of a and b, as lo holds it.
+__device__ __forceinline__ uint32_t half_pair_left(float a, float b, uint32_t w) {
+    return half_pair((a - half_value(w, 0)) * ORTH_LO, (b - half_value(w, 1)) * ORTH_LO);
 }
 
 // Buffer of M rows of ld 16-bit values.
@@ -292,6 +303,7 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
     contract<ST, true, BM, BN, C, MT, NT2, 0, !TALL, f16x8_t>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, steps, m0, n0, acc, hook);
     u32x2_t *const lo = (u32x2_t *)a.lo + (t * (WM * WN) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * (MT * NT2 * 4 * 64) + lane;
     if (a.lo_in) {
+        const float by = a.a * (1.f / ORTH_LO);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             __builtin_amdgcn_sched_barrier(0);
@@ -302,7 +314,7 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
                     const u32x2_t w = lo[((i * NT2 + j) * 4 + q) * 64];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        acc[i][j][4 * q + k] = fmaf(a.a, half_value(w[k / 2], k & 1), acc[i][j][4 * q + k]);
+                        acc[i][j][4 * q + k] = fmaf(by, half_value(w[k / 2], k & 1), acc[i][j][4 * q + k]);
                 }
         }
     }
@@ -341,8 +353,7 @@ __global__ __launch_bounds__(64 * WM *WN) void orth_step_kernel(OrthArgs a) {
                     u32x2_t x;
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
-                        x[p] = half_pair(acc[i][j][4 * q + 2 * p] - half_value(w[2 * q + p], 0),
-                                         acc[i][j][4 * q + 2 * p + 1] - half_value(w[2 * q + p], 1));
+                        x[p] = half_pair_left(acc[i][j][4 * q + 2 * p], acc[i][j][4 * q + 2 * p + 1], w[2 * q + p]);
                     lo[((i * NT2 + j) * 4 + q) * 64] = x;
                 }
             }

@@ -140,11 +140,13 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
  *   X_{i+1} = a X_i + (b A + c A^2) X_i,  A = X_i X_i^T     (i < steps)
  *   out = scale * X_steps
  * (the same polynomial from the right where N > K).  Operands of the products
- * are fp16 (11 bits), X itself is kept in two fp16 pieces (22 bits), so that
- * directions that G lacks are not made of its roundings; the diagonals of A and
- * of b A + c A^2 count in fp32, and sums are fp32.
+ * are fp16 (11 bits), X itself is kept in two fp16 pieces (22 bits; the last of
+ * several steps takes the first piece alone), so that directions that G lacks
+ * are not made of its roundings; the diagonals of A and of b A + c A^2 count in
+ * fp32, and sums are fp32.
  * A matrix of zeros gives zeros; infinities and NaN stay in their matrix, and
- * coefficients that take X or b A + c A^2 out of fp16's range make infinities.
+ * coefficients that take X or b A + c A^2 out of fp16's range make infinities
+ * or NaN.
  */
 
 /* Bytes of workspace the call needs; 0 for arguments it refuses. */

@@ -1,12 +1,13 @@
-"""Orthogonalised updates on the GPU, further: the ends of the types' ranges,
-in each of the forms that a size selects."""
+"""Orthogonalised updates on the GPU, further: the ends of the types' ranges
+and of X's two pieces, in each of the forms that a size selects."""
 from __future__ import annotations
 
 import pytest
 import torch
 
+from tests import train_ref as R
 from tests.test_gpu_ops import BF, F32, gen
-from tests.test_gpu_train import COEF, run_orth
+from tests.test_gpu_train import COEF, check, f32, run_orth, size_of
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,19 @@ def test_orthogonalise_at_the_ends_of_the_range(n, N, K, dt):
         g = (G.double() * s).to(dt)
         assert torch.equal(g.double(), G.double() * s)
         assert torch.equal(run_orth(g.cuda(), 5, COEF, 1.0, s), want), s
+
+
+@pytest.mark.parametrize("n,N,K", FORMS)
+def test_orthogonalise_keeps_values_far_below_the_largest(n, N, K):
+    """One value of a matrix holds its norm, the others lie 2^-18 to 2^-27 below: fp16 keeps a few bits of them, and
+    both pieces together the 22 that the bound of one step counts (X' = X here, so nothing else enters)."""
+    print(f"case orth far values n={n} N={N} K={K}", flush=True)
+    g = gen(3)
+    G = torch.randn(n, N, K, generator=g) * 2.0 ** torch.randint(-27, -17, (n, N, K), generator=g)
+    for e, at in enumerate(torch.randint(0, N * K, (n,), generator=g).tolist()):
+        G[e].view(-1)[at] = -3.0 if e % 2 else 3.0
+    c, eps = (1.0, 0.0, 0.0), f32(1e-7)
+    got = run_orth(G.cuda(), 1, c, 1.0, 1e-7)
+    for e in {0, n // 2, n - 1}:
+        m = G[e:e + 1].cuda().double()
+        check(got[e:e + 1], R.orthogonalise(m, 1, c, 1.0, eps), R.orth_one_step_bound(m, c, 1.0, eps, size_of(N, K)), f"matrix {e}")
