@@ -15,6 +15,15 @@
 // equal singular values up to 7e-3 off, all in one direction.  16 of 128 x 256
 // take 37.1 us in place of 34.5 for it, the other forms no more.
 //
+// B' meets X's fp16 copy, and so does B's diagonal ahead of the last two steps:
+// its fp16 value stays in B', and what that rounding leaves meets X.  What X's
+// rounding leaves is a matrix of full rank: B of it lies within what X has, but
+// the diagonal of B alone does not and would be multiplied by a at every step (a
+// gradient of a quarter of the directions came out 6.5e-3 off for 31 x 257, 3.2e-3
+// for 128 x 256; 2.0e-3 so).  The last two steps, behind which one step at most
+// does that, take X in fp32, which gradients of all directions gain by (128 x 256
+// 1.7e-3, else 1.9e-3).
+//
 // 5 steps, against 3 launches of tiles a step: 16 matrices of 128 x 256 37 and 87
 // us, 18 of 22 x 556 33 and 66, 6 of 73 x 274 53 and 76, 7 of 18 x 1225 58 and
 // 81.  Bound by LDS reads and the turns between its four phases a step.
@@ -199,11 +208,14 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
                     for (int p = 0; p < PA; ++p) S[p] = mfma(AR::along(As, 32 * (ac + p) + l, kk), x, S[p]);
                 }
             const float di = dA[32 * ar + l];
+            const bool late = step + 2 >= steps;
 #pragma unroll
             for (int p = 0; p < PA; ++p) {
+                float copy = 0.f;   // of the diagonal, what stays in B'
                 if (ar == ac + p) {
-                    const float d = take(S[p]);
-                    if (on >= 0) dB[32 * ar + l] = fmaf(a.c, fmaf(di, di, d), a.b * di);
+                    const float d = fmaf(a.c, fmaf(di, di, take(S[p])), a.b * di);
+                    copy = late ? 0.f : (float)(_Float16)d;
+                    if (on >= 0) dB[32 * ar + l] = d - copy;
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -213,6 +225,10 @@ template <typename G, int RT, int MT, int NT> __global__ __launch_bounds__(512) 
                         const int v = 4 * q + k;
                         A[p][v] = fmaf(a.c, fmaf(di + dj[k], A[p][v], S[p][v]), a.b * A[p][v]);
                     }
+                }
+                if (ar == ac + p) {
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) A[p][v] = v == on ? copy : A[p][v];
                 }
             }
         }

@@ -1,12 +1,15 @@
 """Orthogonalised updates on the GPU, further: the ends of the types' ranges
-and of X's two pieces, in each of the forms that a size selects."""
+and of X's two pieces, several steps against 64 bits within limits that the
+mistakes planted in update_forms' model fail, infinities and NaN, in each of
+the forms that a size selects."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 from tests import train_ref as R
-from tests.test_gpu_ops import BF, F32, gen
+from tests import update_forms as F
+from tests.test_gpu_ops import BF, F32, gen, rand
 from tests.test_gpu_train import COEF, check, f32, run_orth, size_of
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +63,66 @@ def test_orthogonalise_keeps_values_far_below_the_largest(n, N, K):
     for e in {0, n // 2, n - 1}:
         m = G[e:e + 1].cuda().double()
         check(got[e:e + 1], R.orthogonalise(m, 1, c, 1.0, eps), R.orth_one_step_bound(m, c, 1.0, eps, size_of(N, K)), f"matrix {e}")
+
+
+# The one-block form's other shapes, and sizes that leave parts of tiles, waves and 16-byte pieces.
+MORE = [(2, 31, 257), (2, 257, 31), (2, 64, 500), (2, 61, 1000), (2, 128, 256), (2, 97, 383), (2, 383, 97), (2, 129, 127), (2, 130, 61),
+        (1, 257, 513), (40, 520, 264), (2, 136, 1000), (1, 1000, 1000), (1, 65, 1030)]
+
+
+def few_of(n, N, K, kind, dt):
+    """n matrices, three of them different ones."""
+    G = F.update_case(min(n, 3), N, K, kind).to(dt)
+    return G.cuda()[torch.arange(n) % len(G)].contiguous()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("kind", F.KINDS)
+@pytest.mark.parametrize("n,N,K", FORMS + MORE)
+def test_orthogonalise_five_steps(n, N, K, kind, dt):
+    print(f"case orth five steps n={n} N={N} K={K} {kind} {dt}", flush=True)
+    G = few_of(n, N, K, kind, dt)
+    got = run_orth(G, 5, F.COEF, 1.0, F.EPS)
+    off = F.off_by(got[:3], G[:3])
+    print(f"  off {float(off.max()):.2e}", flush=True)
+    assert bool((off <= F.LIMIT).all())
+    assert torch.equal(got, got[torch.arange(n) % min(n, 3)])
+
+
+@pytest.mark.parametrize("n,N,K", FORMS + MORE)
+def test_orthogonalise_makes_no_directions(n, N, K):
+    """What a gradient of few directions lacks stays missing but for the rounding of the result."""
+    G = few_of(n, N, K, "low", F32)
+    got = run_orth(G, 5, F.COEF, 1.0, F.EPS)
+    made = F.missing(got[:3].cpu(), min(N, K) // 4)
+    assert bool((made <= 1.0).all()), made
+
+
+@pytest.mark.parametrize("c", F.POLYNOMIALS)
+@pytest.mark.parametrize("n,N,K", FORMS)
+def test_orthogonalise_three_steps_of_other_polynomials(n, N, K, c):
+    for kind in ("low", "bad"):
+        G = few_of(n, N, K, kind, F32)
+        off = F.off_by(run_orth(G, 3, c, 1.0, F.EPS)[:3], G[:3], 3, c)
+        assert bool((off <= F.LIMIT).all()), (kind, off)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("n,N,K", [(6, *f[1:]) if f[0] < 6 else f for f in FORMS])
+def test_orthogonalise_infinities_stay_in_their_matrix(n, N, K, value):
+    """Operands of a tile go on into the row behind, and a matrix' last row into nothing: none reaches a neighbour."""
+    print(f"case orth {value} n={n} N={N} K={K}", flush=True)
+    G = rand(n, N, K, seed=3).cuda()
+    places = {1: (0, 0), 3: (N - 1, K - 1), n - 1: (N // 2, K - 1)}
+    for e in places:
+        G[e] = 0
+    want = run_orth(G, 5, F.COEF, 1.0, F.EPS).clone()
+    for e, (i, j) in places.items():
+        G[e] = rand(N, K, seed=4).cuda()
+        G[e, i, j] = value
+    got = run_orth(G, 5, F.COEF, 1.0, F.EPS)
+    for e in range(n):
+        if e in places:
+            assert not bool(got[e].isfinite().all()) and not want[e].any()
+        else:
+            assert torch.equal(got[e], want[e]) and bool(want[e].isfinite().all())
