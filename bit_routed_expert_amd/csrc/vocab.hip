@@ -10,9 +10,11 @@
 // dloss at the target, from the same tiles, as bf16 into the workspace (a
 // piece is sized so that it stays in the last-level cache), then
 // dW = dz^T h of the piece and dh += dz W, its contraction cut into spans
-// where the tiles of dh are fewer than the CUs.  Where an output is fp32, dz
-// is kept in two bf16 pieces (16 bits) and its product run over both: the
-// rounding of one piece, 2^-8 at most, is more than such an output shows.  dz is kept
+// where the tiles of dh are fewer than the CUs.  Where an output is fp32, dz is
+// kept in three bf16 pieces, which hold fp32's 24 bits, and its products run over
+// all of them: two hold 16, which left 2^-18 of every value of dz, 1 to 2e-6 of
+// the gradients, where fp32 sums leave 1 to 3e-7 (at 7 for 5 units of products:
+// 2047 tokens of 50001 x 1000 1455 us for 1058).  dz is kept
 // over a unit, the first dloss without its exponent: of a mean, where all are the
 // same 1/n, the targets' entries, the largest of each row, are then a power of two
 // less a small number, which bf16 holds, and not 1/n, whose rounding would be the
@@ -235,11 +237,13 @@ struct VocabPlan {
     int piece;
     Tile tile;    // of the loss
     DhTile dh;
-    size_t map, tc, hc, zt, part, lc, gc, dc, hi, lo, acc, bytes;
+    size_t map, tc, hc, zt, part, lc, gc, dc, dz, acc, bytes;
 };
 
 // Columns of a piece: a bf16 dz of 128 MiB (two of them lie in the last-level
-// cache), no fewer than 2048 so that a piece's products fill the CUs.
+// cache), no fewer than 2048 so that a piece's products fill the CUs.  Half of it
+// for fp32 outputs, whose three are past the cache, takes 2047 tokens of 50001 x
+// 1000 from 1451 to 1387 us and 4001 of 32000 x 2048 from 3207 to 3510.
 int piece_columns(int32_t T, int32_t V) {
     int64_t c = ((int64_t)1 << 26) / T / 256 * 256;
     if (c < 2048) c = 2048;
@@ -268,8 +272,7 @@ VocabPlan vocab_plan(int32_t T, int32_t V, int32_t d, bool grad) {
         p.dc = take((size_t)T * 4);
         p.piece = piece_columns(T > 0 ? T : 1, V);
         p.dh = dh_tile(T, d, p.piece);
-        p.hi = take((size_t)T * p.piece * 2);
-        p.lo = take((size_t)T * p.piece * 2);
+        p.dz = take((size_t)T * p.piece * 2 * 3);
         p.acc = take((size_t)p.dh.splits * T * d * 4);
     }
     p.bytes = at;
@@ -436,11 +439,11 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
     a.lc = (float *)(w + p.lc);
     a.gc = (float *)(w + p.gc);
     a.dc = (float *)(w + p.dc);
-    a.hi = (uint16_t *)(w + p.hi);
-    a.lo = (uint16_t *)(w + p.lo);
+    a.dz = (uint16_t *)(w + p.dz);
+    a.next = (int64_t)T * p.piece;
     a.acc = (float *)(w + p.acc);
     a.splits = p.dh.splits;
-    const bool h2 = dh && !a.dh_bf16, w2 = dW && !a.dw_bf16;   // outputs that take both pieces of dz
+    const bool h3 = dh && !a.dh_bf16, w3 = dW && !a.dw_bf16;   // outputs that take all of dz
     STRATA_LAUNCH(vocab_pack_kernel<1>, dim3((T + a.rows_block - 1) / a.rows_block), dim3(256), 0, s, a);
     VOCAB_TRY;
     for (int v0 = 0; v0 < V; v0 += p.piece) {
@@ -450,9 +453,9 @@ strata_status strata_vocab_loss_backward(const void *h, const void *W, const int
         a.first = v0 == 0;
         a.span = (int)up_to((a.pw + a.splits - 1) / a.splits, 64);
         const Tile k = logits_tile(T, a.pw);
-        strata_status q = h2 || w2 ? launch_logits<2>(a, k, s) : launch_logits<1>(a, k, s);
-        if (q == STRATA_OK && dW) q = w2 ? launch_dw<2>(a, s) : launch_dw<1>(a, s);
-        if (q == STRATA_OK && dh) q = h2 ? launch_dh<2>(a, p.dh.tile, s) : launch_dh<1>(a, p.dh.tile, s);
+        strata_status q = h3 || w3 ? launch_logits<3>(a, k, s) : launch_logits<1>(a, k, s);
+        if (q == STRATA_OK && dW) q = w3 ? launch_dw<3>(a, s) : launch_dw<1>(a, s);
+        if (q == STRATA_OK && dh) q = h3 ? launch_dh<3>(a, p.dh.tile, s) : launch_dh<1>(a, p.dh.tile, s);
         if (q != STRATA_OK) return q;
     }
     if (!dh) return STRATA_OK;

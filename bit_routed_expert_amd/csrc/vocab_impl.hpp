@@ -19,7 +19,8 @@ struct VocabArgs {
     float *zt;                      // forward: the target's logit
     float2 *part;                   // forward: [column tile][ldp] maximum and sum of a tile's row
     float *lc, *gc, *dc;            // gradient: lse, dloss + dlse, dloss
-    uint16_t *hi, *lo;              // gradient: [T][ldv] dz of a piece, its first and second bf16
+    uint16_t *dz;                   // gradient: [T][ldv] dz of a piece, its first bf16; `next` values on its second, then its third
+    int64_t next;
     float *acc;                     // gradient: [splits][T][d] sums of dh
     int rows_block, ldp, tiles;     // tokens of a packing block, row length of part, column tiles
     // a piece of the vocabulary: columns v0 .. v0 + pw - 1, ldv a multiple of 8 from pw on
@@ -92,7 +93,7 @@ __device__ __forceinline__ int bit_of(uint32_t m, int r) {
 }
 
 // Tiles of the logits z = hc W^T of a piece.  GRAD 0: the maximum and the sum
-// of each row's tile, and the targets' logits; else dz to hi (and lo).  FEW: a
+// of each row's tile, and the targets' logits; else dz in that many bf16.  FEW: a
 // call of up to 32 tokens takes its rows from h itself, no launch packs them.
 template <int BM, int BN, int WM, int WN, int ST, int GRAD, int FEW = 0>
 __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) {
@@ -211,7 +212,7 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
             want[i] = a.tc[row] - a.v0;
         }
         const bool ragged = c0 + n0 + 32 * NT2 > a.pw;   // columns behind the last one
-        uint16_t *hi = a.hi + (int64_t)row0 * a.ldv, *lo = a.lo + (int64_t)row0 * a.ldv;
+        uint16_t *dz = a.dz + (int64_t)row0 * a.ldv;
         each_quad<MT, NT2>(m0, c0 + n0, acc, [&](int, int col, int i, f32x4_t &v) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) v[c] = exp_diff(v[c], lse[i]) * up[i];
@@ -230,30 +231,32 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_logits_kernel(VocabArgs a) 
                     for (int v = 0; v < 16; ++v) acc[i][j][v] -= 32 * j + 8 * (v / 4) + (v & 3) == place ? un[i] : 0.f;
             }
         }
-        store_tile<MT, NT2>(hi, 1, m0, rows, c0 + n0, a.ldv, acc);
-        if constexpr (GRAD == 2) {   // what the first piece leaves
+        store_tile<MT, NT2>(dz, 1, m0, rows, c0 + n0, a.ldv, acc);
+#pragma unroll
+        for (int p = 1; p < GRAD; ++p) {   // what the pieces before leave
             each_quad<MT, NT2>(m0, c0 + n0, acc, [&](int, int, int, f32x4_t &v) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) v[c] -= bf16_to_float(f2bf(v[c]));
             });
-            store_tile<MT, NT2>(lo, 1, m0, rows, c0 + n0, a.ldv, acc);
+            store_tile<MT, NT2>(dz + p * a.next, 1, m0, rows, c0 + n0, a.ldv, acc);
         }
     }
 }
 
-// An operand whose contraction goes over it PIECES times, the second time from another place.
+// An operand whose contraction goes over it PIECES times, each time `next` values on.
 template <typename O, int C, int PIECES> struct Again : O {
-    const uint16_t *second;
+    int64_t next;
     int steps;
-    __device__ __forceinline__ void again(const uint16_t *p, int n) {
-        second = p;
+    __device__ __forceinline__ void again(int64_t on, int n) {
+        next = on;
         steps = n;
     }
     __device__ __forceinline__ void load(int s, uint8_t *dst) const {
         if (PIECES == 1 || s < steps) return O::load(s, dst);
+        const int p = PIECES > 2 && s >= 2 * steps ? 2 : 1;
         O o = *this;
-        o.base = second;
-        o.load(s - steps, dst);
+        o.base += p * next;
+        o.load(s - p * steps, dst);
     }
 };
 
@@ -283,9 +286,9 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_dw_kernel(VocabArgs a) {
     OA A;
     OB B;
     B.init(a.hc, a.d, k0, a.d, n);
-    A.init(a.hi, a.ldv, r0, a.pw, n);
-    A.again(a.lo, steps);
-    B.again(B.base, steps);
+    A.init(a.dz, a.ldv, r0, a.pw, n);
+    A.again(a.next, steps);
+    B.again(0, steps);
     if (active) contract<ST, true, BM, BN, C, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, PIECES * steps, m0, n0, acc);
     else contract<ST, false, BM, BN, C, MT, NT2, 1, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, PIECES * steps, m0, n0, acc);
     if (!active) return;
@@ -325,10 +328,10 @@ __global__ __launch_bounds__(64 * WM *WN) void vocab_dh_kernel(VocabArgs a) {
     const bool active = m0 < rows && k0 + n0 < a.d;
     OA A;
     OB B;
-    A.init(a.hi + (int64_t)row0 * a.ldv + c0, a.ldv, 0, rows, cda);
+    A.init(a.dz + (int64_t)row0 * a.ldv + c0, a.ldv, 0, rows, cda);
     B.init(a.W + ((int64_t)a.v0 + c0) * a.d, a.d, k0, a.d, min(a.span, a.pw - c0));
-    A.again(a.lo + (int64_t)row0 * a.ldv + c0, steps);
-    B.again(B.base, steps);
+    A.again(a.next, steps);
+    B.again(0, steps);
     if (active) contract<ST, true, BM, BN, C, MT, NT2, 0, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, PIECES * steps, m0, n0, acc);
     else contract<ST, false, BM, BN, C, MT, NT2, 0, 1>(A, B, a0, b0, a1, b1, a2, b2, a3, b3, PIECES * steps, m0, n0, acc);
     if (!active) return;

@@ -126,9 +126,9 @@ strata_status strata_vocab_loss(const void *h, const void *W, const int32_t *tar
  *   dh[t] = sum_v dz[t][v] W[v]     [dev] [T][d] of dhdtype, nullable
  *   dW[v] = sum_t dz[t][v] h[t]     [dev] [V][d] of dwdtype, nullable
  *   flags: STRATA_ACCUMULATE: dW + the sum is written to dW (added in fp32), else the sum.
- * dz enters the products as bf16 (over the first dloss's mantissa) where the output is bf16, and as two bf16
- * pieces (16 bits together) where it is fp32.  T = 0 writes zeros to dW (without the flag).  Errors as above, and EINVAL for a bad dtype of
- * an output that is given, or unknown flags. */
+ * dz enters the products as bf16 (over the first dloss's mantissa) where the output is bf16, and with all its
+ * 24 bits, as three bf16 pieces, where it is fp32.  T = 0 writes zeros to dW (without the flag).  Errors as
+ * above, and EINVAL for a bad dtype of an output that is given, or unknown flags. */
 strata_status strata_vocab_loss_backward(const void *h, const void *W, const int32_t *targets, int32_t T, int32_t V,
                                          int32_t d, const float *lse, const float *dloss, const float *dlse, void *dh,
                                          strata_xdtype dhdtype, void *dW, strata_xdtype dwdtype, uint32_t flags, void *ws,
