@@ -16,10 +16,13 @@
 //
 // Up to EB_FEW tokens take one launch: a block for each token finds the tokens
 // of the same id and, where its own is the first, adds their rows; others write
-// the zeros between.  us against the launches above, drawn ids and all of one row: 9
-// tokens of 531 x 640 3.6 and 3.3 against 8.9 and 7.9; 128 3.3 and 10.7 against 12
-// and 11; 256 3.4 and 19 against 13 and 12; 256 of 5000 x 2048, zeros included, 5.4
-// (bf16) and 34 (fp32) against 18 and 21.
+// the zeros between.  us against the launches above, of ids that differ and of one
+// id alone: 9 tokens of 531 x 640 3.4 and 3.3 against 11.5 and 11.4; 128 3.5 and 10.7
+// against 14 and 11.5; 256 3.7 and 19.4 against 12.4 and 13.8; 256 of 5000 x 2048,
+// zeros included, in bf16 5.4 and 32 against 20 and 18, in fp32 8.1 and 36 against 19
+// and 19.  One id's rows are added by the blocks of one token: up to 128 of them that
+// is no loss, 256 take up to twice as long here, which differing ids, the usual ones,
+// gain 2.4 to 3.7 times over.
 #include <cmath>
 #include <type_traits>
 

@@ -7,8 +7,8 @@
 // tiles of their lower halves are computed.  The operands are fp16: the values
 // are in known ranges (|X| and |A| at most about 1, X kept times a power of
 // two), and 11 bits, with the diagonals of A and B in fp32, leave the result
-// about 5e-4 off, less than its own rounding to bf16 (1.7e-3), where bf16's 8
-// would leave 5e-3.  X itself is hi + lo, 22 bits: with hi alone the rounding
+// 5e-4 to 1.2e-3 off, less than its own rounding to bf16 (1.7e-3), where bf16's 8
+// would leave 3e-3 to 12e-3.  X itself is hi + lo, 22 bits: with hi alone the rounding
 // of X, a matrix of full rank, would be multiplied by a at every step like the
 // small directions of G itself (3.4^5 = 485 in five steps; a gradient of 80 rows
 // in 1536 x 2048 would come out 2% off).  The last of several steps takes hi
@@ -150,9 +150,10 @@ struct OrthPlan {
 // step of 2 of 512 x 2048, 128 tiles: 10.0 us against 13.2; of 1 of 1000 x 1000:
 // 11.4 against 14.5); up to 256, 128 square with four buffers (1 of 2048 x 2048:
 // 27.6 against 33.6); below 1024 with two, two blocks of 8 waves to a CU (whole
-// passes of 8 of 2048 x 768, 768 tiles: 306 us, 256 square 319; 32 of 512 x 512:
-// 239 and 274); then 256 square (4 of 2048 x 2048: 940, 128 square 980; 16 of
-// 1536 x 2048: 1892 and 2055, 128 x 256 1956).
+// passes of 8 of 2048 x 768, 768 tiles: 318 us, 256 square 323; 32 of 512 x 512:
+// 251 and 274, on one card: others take up to a tenth more of all four); then 256
+// square, which spills 52 to 56 bytes a lane (4 of 2048 x 2048: 940, 128 square
+// 980; 16 of 1536 x 2048: 1892 and 2055, 128 x 256 1956).
 enum StepTile { STEP_64, STEP_128, STEP_128_TWO, STEP_256 };
 constexpr StepShape STEP_SHAPES[] = {{64, 128, 2, 2}, {128, 128, 2, 2}, {128, 128, 2, 4}, {256, 256, 2, 4}};
 StepTile step_tile(int32_t n, int32_t N, int32_t K) {

@@ -26,7 +26,8 @@
 //
 // 5 steps, against 3 launches of tiles a step: 16 matrices of 128 x 256 37 and 87
 // us, 18 of 22 x 556 33 and 66, 6 of 73 x 274 53 and 76, 7 of 18 x 1225 58 and
-// 81.  Bound by LDS reads and the turns between its four phases a step.
+// 81.  Bound by LDS reads and the turns between its four phases a step.  The three
+// longer shapes (1 x 7, 2 x 4 and 2 x 3 subtiles a wave) spill 92 to 316 bytes a lane.
 #pragma once
 #include "orth_impl.hpp"
 
